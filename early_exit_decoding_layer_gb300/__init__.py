@@ -35,7 +35,8 @@ EXPORTS = (
     "ee_attention_scratch_bytes", "ee_op_attention", "ee_head_scratch_bytes",
     "ee_op_vocab_head", "ee_step_io", "ee_set_profile", "ee_profile_read", "ee_last_step_ms",
     "ee_op_attention_noalloc", "ee_set_exit_criterion", "ee_set_token_source",
-    "ee_set_prefill_exit", "ee_prefill_exit_layers",
+    "ee_set_prefill_exit", "ee_prefill_exit_layers", "ee_op_prompt_attention", "ee_op_prompt_weights",
+    "ee_op_attention_weights", "ee_op_evict",
 )
 
 LISTS = ("both", "full")  # EE_LISTS_*
@@ -50,6 +51,7 @@ class EEError(RuntimeError):
 
 
 c_i32, c_f32, c_vp, c_sz = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+c_i64 = ctypes.c_int64
 P = ctypes.POINTER
 
 
@@ -130,6 +132,14 @@ def load_library(path: str = LIB_PATH):
         "ee_last_step_ms": (i32, [c_vp, P(c_f32)]),
         "ee_op_attention_noalloc": (i32, [i32, i32, i32, i32, i32, c_vp, c_vp, c_vp, c_vp, i32, c_vp,
                                           c_vp, c_vp, c_vp]),
+        "ee_op_prompt_attention": (i32, [i32, i32, i32, i32, i32, i32, c_vp, c_i64, c_vp, c_vp, i32, c_vp, i32,
+                                         c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp]),
+        "ee_op_prompt_weights": (i32, [i32, i32, i32, i32, i32, i32, c_vp, c_i64, c_vp, i32, c_vp, i32, c_vp,
+                                       c_vp, c_vp, c_vp, c_vp, c_vp]),
+        "ee_op_attention_weights": (i32, [i32, i32, i32, i32, i32, c_vp, c_vp, c_vp, i32, c_vp, i32, c_vp, c_vp,
+                                          c_vp, c_vp, c_vp]),
+        "ee_op_evict": (i32, [i32, i32, i32, i32, i32, i32, c_vp, c_vp, c_vp, i32, c_vp, i32, c_vp, i32, c_vp,
+                              c_vp, c_vp, c_vp, c_vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -501,3 +511,145 @@ def vocab_head(u, E, scratch=None, err=None, stream=None):
                                            _ptr(scratch), _ptr(err), _stream(stream)),
            "ee_op_vocab_head")
     return conf, arg
+
+
+# ------------------------------------------------- prompts and bounded caches
+
+class _Args:
+    """Checks of the cache operators' tensors, all before any launch: on one CUDA
+    device, of the right type and shape, contiguous (rows of q and out may be
+    strided).  Refusals raise EEError with EE_ERR_INVALID_ARG."""
+
+    def __init__(self, what: str, first):
+        import torch
+        self.what, self.torch = what, torch
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            self.refuse("the tensors have to be on a CUDA device")
+        self.device = first.device
+
+    def refuse(self, why: str):
+        raise EEError(1, "%s: %s" % (self.what, why))
+
+    def tensor(self, name: str, t, kinds: str, shape):
+        """t's address; kinds: 'half' (fp16, or its bits in 16-bit integers), 'f32' or 'i32';
+        shape: None where any size is taken."""
+        torch = self.torch
+        if not isinstance(t, torch.Tensor) or t.device != self.device:
+            self.refuse("%s has to be a tensor on %s" % (name, self.device))
+        ok = {"half": (torch.float16, torch.int16, torch.uint16), "f32": (torch.float32,),
+              "i32": (torch.int32,)}[kinds]
+        if t.dtype not in ok:
+            self.refuse("%s has type %s" % (name, t.dtype))
+        if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+            self.refuse("%s has shape %s, not %s" % (name, tuple(t.shape), tuple("any" if w is None else w for w in shape)))
+        if not t.is_contiguous():
+            self.refuse("%s has to be contiguous" % name)
+        return t.data_ptr()
+
+    def rows(self, name: str, t, width: int, rows=None):
+        """(address, row stride) of fp16 rows whose values lie side by side."""
+        torch = self.torch
+        if not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype not in (torch.float16, torch.int16, torch.uint16):
+            self.refuse("%s has to be fp16 (or its bits) on %s" % (name, self.device))
+        if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
+            self.refuse("%s has shape %s, not (%s, %d)" % (name, tuple(t.shape), "rows" if rows is None else rows, width))
+        if t.shape[0] <= 1:
+            stride = width
+        else:
+            stride = t.stride(0)
+        if (width > 1 and t.stride(1) != 1) or stride < width:
+            self.refuse("%s has strides %s" % (name, t.stride()))
+        return t.data_ptr(), stride
+
+    def cache(self, kcache, table, n_seqs, n_kv_heads, head_dim):
+        """(n_blocks, address of K, address of the table, its stride)"""
+        k = self.tensor("kcache", kcache, "half", (None, n_kv_heads, 16, head_dim))
+        return kcache.shape[0], k, self.tensor("block_table", table, "i32", (n_seqs, None)), table.shape[1]
+
+    def err(self, err):
+        return 0 if err is None else self.tensor("err", err, "i32", (1,))
+
+    def call(self, fn, stream, *args):
+        with self.torch.cuda.device(self.device):
+            st = (stream or self.torch.cuda.current_stream(self.device)).cuda_stream
+            _raise(fn(*args, st), self.what)
+
+
+def prompt_attention(q, kcache, vcache, block_table, cu_q, ctx, n_heads, n_kv_heads, head_dim, max_ctx,
+                     out=None, err=None, stream=None):
+    """Causal attention of packed prompt rows over the paged cache
+    (ee_op_prompt_attention).  q [T, Hq*hd] fp16 (rows may be strided by a
+    multiple of 8); caches [blocks, Hkv, 16, hd] fp16; block_table [S, W], cu_q
+    [S+1], ctx [S] int32.  Returns (o [T, Hq*hd] fp16, lse [Hq, T] fp32); rows of
+    no sequence are left unwritten."""
+    import torch
+    a = _Args("ee_op_prompt_attention", q)
+    qp, qs = a.rows("q", q, n_heads * head_dim)
+    T, S = q.shape[0], ctx.shape[0]
+    nb, kp, tp, ts = a.cache(kcache, block_table, S, n_kv_heads, head_dim)
+    vp = a.tensor("vcache", vcache, "half", tuple(kcache.shape))
+    cp, xp = a.tensor("cu_q", cu_q, "i32", (S + 1,)), a.tensor("ctx", ctx, "i32", (S,))
+    o = out if out is not None else torch.empty((T, n_heads * head_dim), dtype=torch.float16, device=q.device)
+    op, os_ = a.rows("out", o, n_heads * head_dim, T)
+    lse = torch.empty((n_heads, T), dtype=torch.float32, device=q.device)
+    a.call(load_library().ee_op_prompt_attention, stream, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs, kp,
+           vp, nb, tp, ts, cp, xp, op, os_, lse.data_ptr(), a.err(err))
+    return o, lse
+
+
+def prompt_weights(q, kcache, block_table, cu_q, ctx, lse, weights, n_heads, n_kv_heads, head_dim, max_ctx,
+                   err=None, stream=None):
+    """Adds to weights [blocks, Hkv, 16] fp32 what each cached token weighs in
+    prompt_attention's rows (ee_op_prompt_weights); lse as it returned it.
+    Returns weights."""
+    a = _Args("ee_op_prompt_weights", q)
+    qp, qs = a.rows("q", q, n_heads * head_dim)
+    T, S = q.shape[0], ctx.shape[0]
+    nb, kp, tp, ts = a.cache(kcache, block_table, S, n_kv_heads, head_dim)
+    cp, xp = a.tensor("cu_q", cu_q, "i32", (S + 1,)), a.tensor("ctx", ctx, "i32", (S,))
+    lp, wp = a.tensor("lse", lse, "f32", (n_heads, T)), a.tensor("weights", weights, "f32", (nb, n_kv_heads, 16))
+    a.call(load_library().ee_op_prompt_weights, stream, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs, kp, nb,
+           tp, ts, cp, xp, lp, wp, a.err(err))
+    return weights
+
+
+def attention_weights(q, kcache, vcache, block_table, pos, weights, n_heads, n_kv_heads, head_dim, max_ctx,
+                      out=None, err=None, stream=None):
+    """attention() that also adds each token's weight to weights [blocks, Hkv, 16]
+    fp32 (ee_op_attention_weights).  q [B, Hq*hd] fp32, pos [B] int32 (-1: an
+    empty sequence).  Returns o [B, Hq*hd] fp32."""
+    import torch
+    a = _Args("ee_op_attention_weights", q)
+    B = pos.shape[0]
+    qp, pp = a.tensor("q", q, "f32", (B, n_heads * head_dim)), a.tensor("pos", pos, "i32", (B,))
+    nb, kp, tp, ts = a.cache(kcache, block_table, B, n_kv_heads, head_dim)
+    vp = a.tensor("vcache", vcache, "half", tuple(kcache.shape))
+    wp = a.tensor("weights", weights, "f32", (nb, n_kv_heads, 16))
+    o = out if out is not None else torch.empty((B, n_heads * head_dim), dtype=torch.float32, device=q.device)
+    op = a.tensor("out", o, "f32", (B, n_heads * head_dim))
+    a.call(load_library().ee_op_attention_weights, stream, B, n_heads, n_kv_heads, head_dim, max_ctx, qp, kp, vp, nb,
+           tp, ts, pp, op, wp, a.err(err))
+    return o
+
+
+def evict(kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_table=None, err=None, stream=None):
+    """Cuts every sequence to `keep` tokens, the last `recent` and the heaviest
+    others, in place or into dst_table's blocks (ee_op_evict).  Returns (kept
+    [B, Hkv, keep] int32: the kept tokens' former indices, then -1; new_ctx [B]
+    int32)."""
+    import torch
+    a = _Args("ee_op_evict", kcache)
+    if kcache.dim() != 4:
+        a.refuse("kcache has shape %s" % (tuple(kcache.shape),))
+    B, hkv, hd = ctx.shape[0], kcache.shape[1], kcache.shape[3]
+    nb, kp, tp, ts = a.cache(kcache, block_table, B, hkv, hd)
+    vp = a.tensor("vcache", vcache, "half", tuple(kcache.shape))
+    wp, xp = a.tensor("weights", weights, "f32", (nb, hkv, 16)), a.tensor("ctx", ctx, "i32", (B,))
+    dp, ds = (0, 0) if dst_table is None else (a.tensor("dst_table", dst_table, "i32", (B, None)), dst_table.shape[1])
+    if keep < 1 or (dst_table is not None and ds * 16 < keep):
+        a.refuse("keep has to be at least 1 and to fit dst_table")
+    kept = torch.empty((B, hkv, keep), dtype=torch.int32, device=kcache.device)
+    new = torch.empty_like(ctx)
+    a.call(load_library().ee_op_evict, stream, B, hkv, hd, max_ctx, keep, recent, kp, vp, wp, nb, tp, ts, dp, ds, xp,
+           new.data_ptr(), kept.data_ptr(), a.err(err))
+    return kept, new

@@ -418,6 +418,99 @@ ee_status ee_op_attention_noalloc(int32_t B, int32_t n_heads, int32_t n_kv_heads
                                   const int32_t *block_table, int32_t bt_stride,
                                   const int32_t *pos, float *o, int32_t *err_flag, void *stream);
 
+/* ---- prompts in one call, and caches that are kept small -------------------
+ * Not part of the early-exit method: the pages have no counterpart.  Four
+ * operators on the paged cache of ee_op_attention, for callers whose prompts are
+ * long and whose caches are bounded: the attention of whole prompts, what every
+ * cached token weighs in it, one decode step that goes on weighing, and the
+ * eviction of the tokens that weigh least.
+ *
+ * Common to the four:
+ *  - kcache/vcache [n_blocks, Hkv, 16, hd] fp16 and weights [n_blocks, Hkv, 16]
+ *    fp32 (device); token t of sequence s sits in block
+ *    block_table[s * bt_stride + t / 16], slot t % 16.  Only the entries of
+ *    tokens that exist are read.  head_dim 64 or 128, Hq / Hkv in {1, 2, 4, 8},
+ *    at most EE_MAX_BATCH sequences, max_ctx <= 16384.  q, the caches and o
+ *    are 16-byte aligned, the other arrays by their element's size.
+ *  - They need no scratch, allocate nothing and keep nothing between calls: calls
+ *    on different streams, and captured ones, share no memory but the
+ *    caller's.
+ *  - Lengths and block ids are on the device, so a bad one is found by the
+ *    kernel: *err_flag (if given) becomes EE_DERR_LENGTH or EE_DERR_BLOCK and the
+ *    call stays inside the caller's arrays -- a length is cut to the range
+ *    [0, min(max_ctx, 16 * bt_stride)], a block id outside [0, n_blocks) is read
+ *    as some block and not written -- but the results of that sequence mean
+ *    nothing.  *err_flag is never cleared.
+ *  - A block may stand in the tables of several sequences (a shared prefix) where
+ *    a call only reads it.  Weights of a shared block get every sequence's part;
+ *    the order of these additions, and with it the last bit, is not
+ *    fixed.  All other results do not depend on timing.
+ * Asynchronous, on `stream`. */
+enum { EE_DERR_LENGTH = 16, EE_DERR_BLOCK = 17 };
+
+/* Causal attention of packed prompt rows.  Sequence s has the rows cu_q[s] ..
+ * cu_q[s+1]-1 (n of them; device, [n_seqs + 1], ascending, within
+ * [0, total_q]) and ctx[s] cached tokens (device, [n_seqs]), its rows' own
+ * K/V among them: row i stands at position p = ctx[s] - n + i, so a whole prompt
+ * has ctx = n and a chunk behind a cached prefix ctx > n.  For query head h of
+ * kv head floor(h * Hkv / Hq), with z_t = q . k_t / sqrt(hd),
+ *   lse[h, row] = log sum_{t <= p} exp z_t,
+ *   o[row, h]   = sum_{t <= p} exp(z_t - lse) v_t.
+ * A row with p < 0 sees nothing: o = 0, lse = -INF.  Rows of no sequence are
+ * left as they are.
+ *   q [total_q, q_stride] fp16 in natural order, head h at column h * hd;
+ *   o [total_q, o_stride] fp16 likewise, not overlapping q; strides multiples
+ *   of 8, at least Hq * hd; lse [Hq, total_q] fp32 or NULL.  total_q may be 0.
+ * Products are exact in fp32 accumulators and softmax statistics fp32; the
+ * probabilities are rounded to fp16 for the product with V. */
+ee_status ee_op_prompt_attention(int32_t n_seqs, int32_t total_q, int32_t n_heads, int32_t n_kv_heads,
+                                 int32_t head_dim, int32_t max_ctx, const uint16_t *q, int64_t q_stride,
+                                 const uint16_t *kcache, const uint16_t *vcache, int32_t n_blocks,
+                                 const int32_t *block_table, int32_t bt_stride, const int32_t *cu_q,
+                                 const int32_t *ctx, uint16_t *o, int64_t o_stride, float *lse,
+                                 int32_t *err_flag, void *stream);
+
+/* What each cached token weighs in that attention, added to `weights`:
+ *   weights[block(t), g, t % 16] += sum over rows with p >= t and over the query
+ *   heads h of kv head g of exp(z_t - lse[h, row]).
+ * Arguments as above; lse [Hq, total_q] as ee_op_prompt_attention wrote it (a
+ * row whose lse is -INF adds nothing). */
+ee_status ee_op_prompt_weights(int32_t n_seqs, int32_t total_q, int32_t n_heads, int32_t n_kv_heads,
+                               int32_t head_dim, int32_t max_ctx, const uint16_t *q, int64_t q_stride,
+                               const uint16_t *kcache, int32_t n_blocks, const int32_t *block_table,
+                               int32_t bt_stride, const int32_t *cu_q, const int32_t *ctx,
+                               const float *lse, float *weights, int32_t *err_flag, void *stream);
+
+/* The decode attention of ee_op_attention (same q, o, pos and results to
+ * rounding) that also adds what each token weighs:
+ *   weights[block(t), g, t % 16] += sum over the query heads of kv head g of
+ *   softmax_t(q_h . k_t / sqrt(hd)),  t <= pos[s].
+ * pos[s] = -1 is an empty sequence: o = 0, no weight is added. */
+ee_status ee_op_attention_weights(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                  int32_t max_ctx, const float *q, const uint16_t *kcache,
+                                  const uint16_t *vcache, int32_t n_blocks, const int32_t *block_table,
+                                  int32_t bt_stride, const int32_t *pos, float *o, float *weights,
+                                  int32_t *err_flag, void *stream);
+
+/* Cuts every sequence to `keep` tokens.  Where ctx[s] > keep, each kv head keeps
+ * the last `recent` tokens and, of the others, the keep - recent that weigh most
+ * (ties: the lower index; NaN weighs least, -0 as 0), moves their K, V and
+ * weights in token order to slots 0 .. keep-1 of dst_table's blocks, and
+ * new_ctx[s] = keep.  Where ctx[s] <= keep all are kept and new_ctx[s] = ctx[s].
+ * kept [B, Hkv, keep] (or NULL) gets the kept tokens' former indices, ascending,
+ * then -1.  Slots behind the kept ones are left as they are, and the caller
+ * may give away the blocks from ceil(new_ctx / 16) on.  1 <= keep <= max_ctx,
+ * 0 <= recent <= keep.
+ *   dst_table [B, dst_stride] with 16 * dst_stride >= keep: blocks that no row of
+ *   block_table names and that occur once in dst_table; NULL moves in
+ *   place (into block_table's own blocks, which then occur once).
+ *   new_ctx must not be ctx. */
+ee_status ee_op_evict(int32_t B, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx, int32_t keep,
+                      int32_t recent, uint16_t *kcache, uint16_t *vcache, float *weights, int32_t n_blocks,
+                      const int32_t *block_table, int32_t bt_stride, const int32_t *dst_table,
+                      int32_t dst_stride, const int32_t *ctx, int32_t *new_ctx, int32_t *kept,
+                      int32_t *err_flag, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
