@@ -41,6 +41,7 @@
 #include "ee_epilogue.cuh"
 #include "ee_head.cuh"
 #include "ee_kernels.cuh"
+#include "ee_tcgen05.cuh"
 
 namespace ee {
 
@@ -68,41 +69,6 @@ template <int MODE>
 constexpr size_t kTcSmem = (size_t)stage_count(MODE) * stage_bytes(MODE == 0 ? 2 * kCols : kCols) +
                            (MODE == 1 ? (size_t)kRawSlots * kQ4Block : 0) + 1024;
 static_assert(kTcSmem<1> <= kTcSmem<0>, "MODE 1 fits in MODE 0's shared memory");
-
-// Shared memory descriptor of a K-major tile with 128-byte rows and the
-// 128-byte swizzle: start address, stride between 8-row groups (1024 B),
-// descriptor version 1, swizzle mode 2 (leading offset unused: 1).
-EE_DEV uint64_t smem_desc_sw128(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// Instruction descriptor, kind::f16: fp32 accumulators, A and B of type
-// `ab` (0 = f16, 1 = bf16), both K-major, N and M given.
-constexpr uint32_t instr_desc(uint32_t ab, int n, int m) {
-  return (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
-// Byte offset of 16-byte chunk j (8 elements) of row r in a 128B-swizzled tile.
-EE_DEV uint32_t sw128(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
-
-EE_DEV void st_shared_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
-EE_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-EE_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
-}
 
 // x = hi + lo for two values: hi their bf16 roundings (one paired
 // conversion), lo the remainders, exact in bf16 for fp16 inputs.
@@ -591,29 +557,11 @@ cudaError_t gemm_tc_prepare() {
   return cudaFuncSetAttribute(k_gemm_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem<0>);
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 bool encode_weight_map(CUtensorMap* map, const uint16_t* w, int N, int K) {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !f)
-      return false;
-    fn = reinterpret_cast<EncodeTiledFn>(f);
-  }
   if (!w || (uintptr_t)w % 16 || K % kBK || N < 1) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)N};
-  const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)kBM};
-  const cuuint32_t es[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(w), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const uint64_t dims[2] = {(uint64_t)K, (uint64_t)N}, strides[1] = {(uint64_t)K * 2};
+  const uint32_t box[2] = {(uint32_t)kBK, (uint32_t)kBM};
+  return encode_tensor_map(map, true, 2, w, dims, strides, box);
 }
 
 cudaError_t launch_gemm_tc(const TcParams& tp, bool pdl, cudaStream_t st) {
