@@ -515,85 +515,78 @@ def vocab_head(u, E, scratch=None, err=None, stream=None):
 
 # ------------------------------------------------- prompts and bounded caches
 
-class _Args:
-    """Checks of the cache operators' tensors, all before any launch: on one CUDA
-    device, of the right type and shape, contiguous (rows of q and out may be
-    strided).  Refusals raise EEError with EE_ERR_INVALID_ARG."""
+def _cuda_tensor(what: str, name: str, t) -> int:
+    """The device index of a CUDA tensor; EE_ERR_INVALID_ARG for anything else."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise EEError(1, "%s: %s has to be a tensor on a CUDA device" % (what, name))
+    return t.get_device()
 
-    def __init__(self, what: str, first):
+
+def _kinds():
+    """Element types by kind: fp16 (or its bits in 16-bit integers), fp32, int32."""
+    global _KINDS
+    if _KINDS is None:
         import torch
-        self.what, self.torch = what, torch
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            self.refuse("the tensors have to be on a CUDA device")
-        self.device = first.device
+        _KINDS = (torch.float16, torch.int16, torch.uint16), (torch.float32,), (torch.int32,)
+    return _KINDS
 
-    def refuse(self, why: str):
-        raise EEError(1, "%s: %s" % (self.what, why))
 
-    def tensor(self, name: str, t, kinds: str, shape):
-        """t's address; kinds: 'half' (fp16, or its bits in 16-bit integers), 'f32' or 'i32';
-        shape: None where any size is taken."""
-        torch = self.torch
-        if not isinstance(t, torch.Tensor) or t.device != self.device:
-            self.refuse("%s has to be a tensor on %s" % (name, self.device))
-        ok = {"half": (torch.float16, torch.int16, torch.uint16), "f32": (torch.float32,),
-              "i32": (torch.int32,)}[kinds]
-        if t.dtype not in ok:
-            self.refuse("%s has type %s" % (name, t.dtype))
-        if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-            self.refuse("%s has shape %s, not %s" % (name, tuple(t.shape), tuple("any" if w is None else w for w in shape)))
-        if not t.is_contiguous():
-            self.refuse("%s has to be contiguous" % name)
-        return t.data_ptr()
+_KINDS = None
 
-    def rows(self, name: str, t, width: int, rows=None):
-        """(address, row stride) of fp16 rows whose values lie side by side."""
-        torch = self.torch
-        if not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype not in (torch.float16, torch.int16, torch.uint16):
-            self.refuse("%s has to be fp16 (or its bits) on %s" % (name, self.device))
-        if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
-            self.refuse("%s has shape %s, not (%s, %d)" % (name, tuple(t.shape), "rows" if rows is None else rows, width))
-        if t.shape[0] <= 1:
-            stride = width
-        else:
-            stride = t.stride(0)
-        if (width > 1 and t.stride(1) != 1) or stride < width:
-            self.refuse("%s has strides %s" % (name, t.stride()))
-        return t.data_ptr(), stride
 
-    def cache(self, kcache, table, n_seqs, n_kv_heads, head_dim):
-        """(n_blocks, address of K, address of the table, its stride)"""
-        k = self.tensor("kcache", kcache, "half", (None, n_kv_heads, 16, head_dim))
-        return kcache.shape[0], k, self.tensor("block_table", table, "i32", (n_seqs, None)), table.shape[1]
+def _addr(what: str, dev: int, name: str, t, kinds, shape) -> int:
+    """t's address; refused (EE_ERR_INVALID_ARG, before any launch) unless t is a
+    contiguous tensor of that shape and type on device dev."""
+    _cuda_tensor(what, name, t)
+    if t.get_device() != dev or t.dtype not in kinds or t.shape != shape or not t.is_contiguous():
+        raise EEError(1, "%s: %s has to be a contiguous %s tensor of shape %s on cuda:%d, not %s %s on %s"
+                      % (what, name, kinds[0], tuple(shape), dev, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
 
-    def err(self, err):
-        return 0 if err is None else self.tensor("err", err, "i32", (1,))
 
-    def call(self, fn, stream, *args):
-        with self.torch.cuda.device(self.device):
-            st = (stream or self.torch.cuda.current_stream(self.device)).cuda_stream
-            _raise(fn(*args, st), self.what)
+def _rows(what: str, dev: int, name: str, t, kinds, shape):
+    """(address, row stride) of fp16 rows that may lie apart, their values side by side."""
+    _cuda_tensor(what, name, t)
+    stride = t.stride(0) if t.dim() == 2 and shape[0] > 1 else shape[1]
+    if t.get_device() != dev or t.dtype not in kinds or t.shape != shape or t.stride(1) != 1 or stride < shape[1]:
+        raise EEError(1, "%s: %s has to be a %s tensor of shape %s on cuda:%d with side-by-side columns, not %s %s, strides %s on %s"
+                      % (what, name, kinds[0], tuple(shape), dev, t.dtype, tuple(t.shape), t.stride(), t.device))
+    return t.data_ptr(), stride
+
+
+def _launch(what: str, dev: int, fn, stream, *args):
+    """Calls fn on device dev and its current stream (or the given one)."""
+    import torch
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(what, dev, fn, stream, *args)
+    _raise(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream), what)
 
 
 def prompt_attention(q, kcache, vcache, block_table, cu_q, ctx, n_heads, n_kv_heads, head_dim, max_ctx,
                      out=None, err=None, stream=None):
     """Causal attention of packed prompt rows over the paged cache
-    (ee_op_prompt_attention).  q [T, Hq*hd] fp16 (rows may be strided by a
-    multiple of 8); caches [blocks, Hkv, 16, hd] fp16; block_table [S, W], cu_q
+    (ee_op_prompt_attention).  q [T, Hq*hd] fp16 (rows may lie apart by a multiple
+    of 8 values); caches [blocks, Hkv, 16, hd] fp16; block_table [S, W], cu_q
     [S+1], ctx [S] int32.  Returns (o [T, Hq*hd] fp16, lse [Hq, T] fp32); rows of
     no sequence are left unwritten."""
     import torch
-    a = _Args("ee_op_prompt_attention", q)
-    qp, qs = a.rows("q", q, n_heads * head_dim)
-    T, S = q.shape[0], ctx.shape[0]
-    nb, kp, tp, ts = a.cache(kcache, block_table, S, n_kv_heads, head_dim)
-    vp = a.tensor("vcache", vcache, "half", tuple(kcache.shape))
-    cp, xp = a.tensor("cu_q", cu_q, "i32", (S + 1,)), a.tensor("ctx", ctx, "i32", (S,))
-    o = out if out is not None else torch.empty((T, n_heads * head_dim), dtype=torch.float16, device=q.device)
-    op, os_ = a.rows("out", o, n_heads * head_dim, T)
+    what = "ee_op_prompt_attention"
+    dev = _cuda_tensor(what, "q", q)
+    _cuda_tensor(what, "kcache", kcache), _cuda_tensor(what, "block_table", block_table), _cuda_tensor(what, "ctx", ctx)
+    half, f32, i32 = _kinds()
+    T, S, nb, W = q.shape[0], ctx.numel(), kcache.shape[0], block_table.shape[-1]
+    cache, width = (nb, n_kv_heads, 16, head_dim), n_heads * head_dim
+    qp, qs = _rows(what, dev, "q", q, half, (T, width))
+    o = out if out is not None else torch.empty((T, width), dtype=torch.float16, device=q.device)
+    op, os_ = _rows(what, dev, "out", o, half, (T, width))
     lse = torch.empty((n_heads, T), dtype=torch.float32, device=q.device)
-    a.call(load_library().ee_op_prompt_attention, stream, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs, kp,
-           vp, nb, tp, ts, cp, xp, op, os_, lse.data_ptr(), a.err(err))
+    _launch(what, dev, load_library().ee_op_prompt_attention, stream, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs,
+            _addr(what, dev, "kcache", kcache, half, cache), _addr(what, dev, "vcache", vcache, half, cache), nb,
+            _addr(what, dev, "block_table", block_table, i32, (S, W)), W, _addr(what, dev, "cu_q", cu_q, i32, (S + 1,)),
+            _addr(what, dev, "ctx", ctx, i32, (S,)), op, os_, lse.data_ptr(),
+            0 if err is None else _addr(what, dev, "err", err, i32, (1,)))
     return o, lse
 
 
@@ -602,14 +595,18 @@ def prompt_weights(q, kcache, block_table, cu_q, ctx, lse, weights, n_heads, n_k
     """Adds to weights [blocks, Hkv, 16] fp32 what each cached token weighs in
     prompt_attention's rows (ee_op_prompt_weights); lse as it returned it.
     Returns weights."""
-    a = _Args("ee_op_prompt_weights", q)
-    qp, qs = a.rows("q", q, n_heads * head_dim)
-    T, S = q.shape[0], ctx.shape[0]
-    nb, kp, tp, ts = a.cache(kcache, block_table, S, n_kv_heads, head_dim)
-    cp, xp = a.tensor("cu_q", cu_q, "i32", (S + 1,)), a.tensor("ctx", ctx, "i32", (S,))
-    lp, wp = a.tensor("lse", lse, "f32", (n_heads, T)), a.tensor("weights", weights, "f32", (nb, n_kv_heads, 16))
-    a.call(load_library().ee_op_prompt_weights, stream, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs, kp, nb,
-           tp, ts, cp, xp, lp, wp, a.err(err))
+    what = "ee_op_prompt_weights"
+    dev = _cuda_tensor(what, "q", q)
+    _cuda_tensor(what, "kcache", kcache), _cuda_tensor(what, "block_table", block_table), _cuda_tensor(what, "ctx", ctx)
+    half, f32, i32 = _kinds()
+    T, S, nb, W = q.shape[0], ctx.numel(), kcache.shape[0], block_table.shape[-1]
+    qp, qs = _rows(what, dev, "q", q, half, (T, n_heads * head_dim))
+    _launch(what, dev, load_library().ee_op_prompt_weights, stream, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs,
+            _addr(what, dev, "kcache", kcache, half, (nb, n_kv_heads, 16, head_dim)), nb,
+            _addr(what, dev, "block_table", block_table, i32, (S, W)), W, _addr(what, dev, "cu_q", cu_q, i32, (S + 1,)),
+            _addr(what, dev, "ctx", ctx, i32, (S,)), _addr(what, dev, "lse", lse, f32, (n_heads, T)),
+            _addr(what, dev, "weights", weights, f32, (nb, n_kv_heads, 16)),
+            0 if err is None else _addr(what, dev, "err", err, i32, (1,)))
     return weights
 
 
@@ -619,16 +616,18 @@ def attention_weights(q, kcache, vcache, block_table, pos, weights, n_heads, n_k
     fp32 (ee_op_attention_weights).  q [B, Hq*hd] fp32, pos [B] int32 (-1: an
     empty sequence).  Returns o [B, Hq*hd] fp32."""
     import torch
-    a = _Args("ee_op_attention_weights", q)
-    B = pos.shape[0]
-    qp, pp = a.tensor("q", q, "f32", (B, n_heads * head_dim)), a.tensor("pos", pos, "i32", (B,))
-    nb, kp, tp, ts = a.cache(kcache, block_table, B, n_kv_heads, head_dim)
-    vp = a.tensor("vcache", vcache, "half", tuple(kcache.shape))
-    wp = a.tensor("weights", weights, "f32", (nb, n_kv_heads, 16))
-    o = out if out is not None else torch.empty((B, n_heads * head_dim), dtype=torch.float32, device=q.device)
-    op = a.tensor("out", o, "f32", (B, n_heads * head_dim))
-    a.call(load_library().ee_op_attention_weights, stream, B, n_heads, n_kv_heads, head_dim, max_ctx, qp, kp, vp, nb,
-           tp, ts, pp, op, wp, a.err(err))
+    what = "ee_op_attention_weights"
+    dev = _cuda_tensor(what, "q", q)
+    _cuda_tensor(what, "kcache", kcache), _cuda_tensor(what, "block_table", block_table), _cuda_tensor(what, "pos", pos)
+    half, f32, i32 = _kinds()
+    B, nb, W = pos.numel(), kcache.shape[0], block_table.shape[-1]
+    cache, rows = (nb, n_kv_heads, 16, head_dim), (B, n_heads * head_dim)
+    o = out if out is not None else torch.empty(rows, dtype=torch.float32, device=q.device)
+    _launch(what, dev, load_library().ee_op_attention_weights, stream, B, n_heads, n_kv_heads, head_dim, max_ctx,
+            _addr(what, dev, "q", q, f32, rows), _addr(what, dev, "kcache", kcache, half, cache),
+            _addr(what, dev, "vcache", vcache, half, cache), nb, _addr(what, dev, "block_table", block_table, i32, (B, W)), W,
+            _addr(what, dev, "pos", pos, i32, (B,)), _addr(what, dev, "out", o, f32, rows),
+            _addr(what, dev, "weights", weights, f32, cache[:3]), 0 if err is None else _addr(what, dev, "err", err, i32, (1,)))
     return o
 
 
@@ -638,18 +637,26 @@ def evict(kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_
     [B, Hkv, keep] int32: the kept tokens' former indices, then -1; new_ctx [B]
     int32)."""
     import torch
-    a = _Args("ee_op_evict", kcache)
+    what = "ee_op_evict"
+    dev = _cuda_tensor(what, "kcache", kcache)
+    _cuda_tensor(what, "block_table", block_table), _cuda_tensor(what, "ctx", ctx)
+    half, f32, i32 = _kinds()
     if kcache.dim() != 4:
-        a.refuse("kcache has shape %s" % (tuple(kcache.shape),))
-    B, hkv, hd = ctx.shape[0], kcache.shape[1], kcache.shape[3]
-    nb, kp, tp, ts = a.cache(kcache, block_table, B, hkv, hd)
-    vp = a.tensor("vcache", vcache, "half", tuple(kcache.shape))
-    wp, xp = a.tensor("weights", weights, "f32", (nb, hkv, 16)), a.tensor("ctx", ctx, "i32", (B,))
-    dp, ds = (0, 0) if dst_table is None else (a.tensor("dst_table", dst_table, "i32", (B, None)), dst_table.shape[1])
+        raise EEError(1, "%s: kcache has shape %s" % (what, tuple(kcache.shape)))
+    cache, B, W = kcache.shape, ctx.numel(), block_table.shape[-1]
+    hkv, hd = cache[1], cache[3]
+    dp = ds = 0
+    if dst_table is not None:
+        _cuda_tensor(what, "dst_table", dst_table)
+        ds = dst_table.shape[-1]
+        dp = _addr(what, dev, "dst_table", dst_table, i32, (B, ds))
     if keep < 1 or (dst_table is not None and ds * 16 < keep):
-        a.refuse("keep has to be at least 1 and to fit dst_table")
+        raise EEError(1, "%s: keep has to be at least 1 and to fit dst_table" % what)
     kept = torch.empty((B, hkv, keep), dtype=torch.int32, device=kcache.device)
-    new = torch.empty_like(ctx)
-    a.call(load_library().ee_op_evict, stream, B, hkv, hd, max_ctx, keep, recent, kp, vp, wp, nb, tp, ts, dp, ds, xp,
-           new.data_ptr(), kept.data_ptr(), a.err(err))
+    new = torch.empty((B,), dtype=torch.int32, device=kcache.device)
+    _launch(what, dev, load_library().ee_op_evict, stream, B, hkv, hd, max_ctx, keep, recent,
+            _addr(what, dev, "kcache", kcache, half, (cache[0], hkv, 16, hd)), _addr(what, dev, "vcache", vcache, half, cache),
+            _addr(what, dev, "weights", weights, f32, cache[:3]), cache[0],
+            _addr(what, dev, "block_table", block_table, i32, (B, W)), W, dp, ds, _addr(what, dev, "ctx", ctx, i32, (B,)),
+            new.data_ptr(), kept.data_ptr(), 0 if err is None else _addr(what, dev, "err", err, i32, (1,)))
     return kept, new

@@ -106,7 +106,7 @@ ee_status ee_op_prompt_weights(int32_t n_seqs, int32_t total_q, int32_t n_heads,
                             bt_stride, err_flag, &p.c);
   if (s == EE_OK) s = prompt_args(n_seqs, total_q, n_heads, n_kv_heads, head_dim, q, q_stride, cu_q, ctx, &p);
   if (s != EE_OK) return s;
-  if (!aligned(weights, 4)) return EE_ERR_INVALID_ARG;
+  if (!aligned(weights, 16)) return EE_ERR_INVALID_ARG;
   if (total_q == 0) return EE_OK;
   if (!aligned(lse, 4)) return EE_ERR_INVALID_ARG;
   p.lse_in = lse;
@@ -121,7 +121,7 @@ ee_status ee_op_attention_weights(int32_t B, int32_t n_heads, int32_t n_kv_heads
   const ee_status s = paged_cache(B, n_kv_heads, head_dim, max_ctx, kcache, vcache, weights, n_blocks, block_table,
                                   bt_stride, err_flag, &p.c);
   if (s != EE_OK) return s;
-  if (!group_ok(n_heads, n_kv_heads) || !aligned(vcache, 16) || !aligned(weights, 4) || !aligned(q, 16) ||
+  if (!group_ok(n_heads, n_kv_heads) || !aligned(vcache, 16) || !aligned(weights, 16) || !aligned(q, 16) ||
       !aligned(o, 16) || !aligned(pos, 4))
     return EE_ERR_INVALID_ARG;
   p.batch = B;
@@ -140,7 +140,7 @@ ee_status ee_op_evict(int32_t B, int32_t n_kv_heads, int32_t head_dim, int32_t m
   const ee_status s = paged_cache(B, n_kv_heads, head_dim, max_ctx, kcache, vcache, weights, n_blocks, block_table,
                                   bt_stride, err_flag, &p.c);
   if (s != EE_OK) return s;
-  if (!aligned(vcache, 16) || !aligned(weights, 4) || !aligned(ctx, 4) || !aligned(new_ctx, 4) || new_ctx == ctx ||
+  if (!aligned(vcache, 16) || !aligned(weights, 16) || !aligned(ctx, 4) || !aligned(new_ctx, 4) || new_ctx == ctx ||
       (kept && !aligned(kept, 4)))
     return EE_ERR_INVALID_ARG;
   if (keep < 1 || keep > max_ctx || recent < 0 || recent > keep) return EE_ERR_INVALID_ARG;

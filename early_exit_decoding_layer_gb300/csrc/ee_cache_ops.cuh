@@ -7,6 +7,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/ee.h"
@@ -61,6 +62,31 @@ struct EvictParams {
   int32_t* new_ctx = nullptr;
   int32_t* kept = nullptr;
 };
+
+// exp(z - x) of a score z = q . k / sqrt(hd), from the tensor core's sum s, as
+// 2^(c s - f x): c is log2(e) / sqrt(hd) rounded to fp32 and f c's counterpart in two
+// terms, so that c's rounding multiplies z - x and not z and x each (1e-6 at a
+// score of 10 otherwise).  unit is 1 / sqrt(hd) in two terms.
+//
+// The tensor core's accumulator is cut, not rounded, after each of the hd / 16 steps of
+// a product, so sums come out smaller by about 0.42 * 2^-23 of each partial
+// sum (hd 128: 2.1e-7 of s measured, hd 64: 1.4e-7; weights of tokens with
+// z = 6 were 1.2e-6 too small).  c, f and unit take that mean back.
+struct Exponent {
+  float c, f_hi, f_lo, unit_hi, unit_lo;
+};
+inline Exponent make_exponent(int head_dim) {
+  const double r = sqrt((double)head_dim);
+  const double grow = 1.0 + 0.42 * 0x1p-23 * (head_dim / 16 + 1) / 2;  // partial sums grow evenly
+  Exponent e;
+  e.c = (float)(1.4426950408889634074 * grow / r);
+  const double f = (double)e.c * r / grow, unit = grow / r;
+  e.f_hi = (float)f;
+  e.f_lo = (float)(f - e.f_hi);
+  e.unit_hi = (float)unit;
+  e.unit_lo = (float)(unit - e.unit_hi);
+  return e;
+}
 
 cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t st);
 cudaError_t launch_prompt_weights(const PromptParams& p, cudaStream_t st);

@@ -140,6 +140,12 @@ EE_DEV void tmem_pin(uint32_t* v) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
+// mbar_wait_bounded by a whole warp with one answer for all its lanes, which stay
+// together for the aligned instructions that follow.
+EE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, code));
+}
+
 EE_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -66,11 +66,17 @@ struct Shared {
   float m[kRows], l[kRows];
 };
 
+// log of the sum of exp(s / sqrt(hd)), from its sum l relative to the score m.
+EE_DEV float log_sum(float m, float l, const Exponent& ex) {
+  return l == 0.0f ? -INFINITY : fmaf(m, ex.unit_hi, fmaf(m, ex.unit_lo, logf(l)));
+}
+
 template <int HD, int G, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_prompt_attention(const PromptParams p, const __grid_constant__ Maps maps, const float c /* log2(e) / sqrt(hd) */) {
+    k_prompt_attention(const PromptParams p, const __grid_constant__ Maps maps, const Exponent ex) {
   using S = Shape<HD>;
   constexpr int kPos = kRows / G;  // positions per CTA
+  const float c = ex.c;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* tiles = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kv = 0; kv < 2; ++kv, ++issued) {
         const int st = issued % S::NST, pass = issued / S::NST;
         if (pass > 0)
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.kv_empty[st], (pass - 1) & 1, p.c.err, DERR_EMPTY_WAIT));
+          ok = warp_wait(&sh.kv_empty[st], (pass - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], (uint32_t)here * 16 * HD * 2);
         __syncwarp();
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      if (!(ok = mbar_wait_bounded(&sh.s_full[t], j & 1, p.c.err, DERR_FULL_WAIT))) break;
+      if (!(ok = warp_wait(&sh.s_full[t], j & 1, p.c.err, DERR_FULL_WAIT))) break;
       tc_fence_after();
       uint32_t s[kKeys];
 #pragma unroll
@@ -255,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float a = m == mn ? 1.0f : ex2((m - mn) * c);
         m = mn;
         l *= a;
-        if (!(ok = mbar_wait_bounded(&sh.o_done[t], (j - 1) & 1, p.c.err, DERR_FULL_WAIT))) break;
+        if (!(ok = warp_wait(&sh.o_done[t], (j - 1) & 1, p.c.err, DERR_FULL_WAIT))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int i = 0; i < HD; i += 16) {
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (masked) {
         // V values that are not finite become 0 before the product reads them
         const int it = 2 * j + 1;
-        if (!(ok = mbar_wait_bounded(&sh.kv_full[it % S::NST], (it / S::NST) & 1, p.c.err, DERR_FULL_WAIT))) break;
+        if (!(ok = warp_wait(&sh.kv_full[it % S::NST], (it / S::NST) & 1, p.c.err, DERR_FULL_WAIT))) break;
         uint8_t* vt = tiles + 2 * S::kTile + (it % S::NST) * S::kTile;
         bool fixed = false;
 #pragma unroll 4
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&sh.p_ready[t]);
     }
-    if (ok && n > 0) ok = mbar_wait_bounded(&sh.o_done[t], (n - 1) & 1, p.c.err, DERR_FULL_WAIT);
+    if (ok && n > 0) ok = warp_wait(&sh.o_done[t], (n - 1) & 1, p.c.err, DERR_FULL_WAIT);
     tc_fence_after();
     asm volatile("bar.sync 1, 256;" ::: "memory");  // bad_v of both tiles; the tiles' space is free
     const bool bad = sh.bad_v;
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.m[t * 128 + r] = m;
       sh.l[t * 128 + r] = l;
     } else if (valid && p.lse) {
-      p.lse[(size_t)head * p.total_q + tl.sq.first + row] = (m * c + log2f(l)) * 0.6931471805599453f;
+      p.lse[(size_t)head * p.total_q + tl.sq.first + row] = log_sum(m, l, ex);
     }
     tc_fence_before();
   }
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint2*>(p.o + (int64_t)(tl.sq.first + row) * p.o_stride + head * HD + col) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
         if (col == 0 && p.lse)
-          p.lse[(size_t)head * p.total_q + tl.sq.first + row] = (M * c + log2f(l)) * 0.6931471805599453f;
+          p.lse[(size_t)head * p.total_q + tl.sq.first + row] = log_sum(M, l, ex);
       }
     }
     cl.sync();  // nobody leaves while its memory is read
@@ -451,7 +457,7 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   if (!encode_tensor_map(&maps.q, false, 3, p.q, qd, qs, qb) || !encode_tensor_map(&maps.k, false, 2, p.c.k, cd, cs, cb) ||
       !encode_tensor_map(&maps.v, false, 2, p.c.v, cd, cs, cb))
     return cudaErrorInvalidValue;
-  const float c = 1.4426950408889634f / sqrtf((float)HD);
+  const Exponent ex = make_exponent(HD);
   // at most this many tiles: each sequence may leave one unfilled
   const int64_t units = ((int64_t)p.total_q * G / kRows + p.n_seqs) * p.c.n_kv_heads;
   int split = 1;
@@ -461,7 +467,7 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
-  if (split == 1) return cudaLaunchKernelEx(&cfg, k_prompt_attention<HD, G, false>, p, maps, c);
+  if (split == 1) return cudaLaunchKernelEx(&cfg, k_prompt_attention<HD, G, false>, p, maps, ex);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = split;
@@ -469,7 +475,7 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_prompt_attention<HD, G, true>, p, maps, c);
+  return cudaLaunchKernelEx(&cfg, k_prompt_attention<HD, G, true>, p, maps, ex);
 }
 
 }  // namespace

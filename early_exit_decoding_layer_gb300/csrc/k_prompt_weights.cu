@@ -1,48 +1,289 @@
-// What each cached token weighs in the attention of packed prompt rows: a warp
-// per (token, kv head) walks the rows that see it.
+// What each cached token weighs in the attention of packed prompt rows, on the
+// tensor cores: w[t] += sum over the rows (position, head of the group) that see
+// t of exp(z_t - lse).
+//
+// The keys are the MMA's rows: S = K_tile Q^T gives every thread of a softmax
+// warpgroup one key and, along its registers, 128 query rows, so the sum over
+// the rows stays in the thread: no shuffles, and no second pass over anything.
+// A CTA owns 128 keys of one kv head; K stays in shared memory, tiles of 128
+// query rows (128 / G positions x G heads) stream through a ring by TMA from
+// the first row that sees a key:
+//   warp 9 (one thread)  S_b = K Q_j^T into four tensor-memory buffers in turn
+//   warps 0-3, 4-7       tiles 0, 2, .. and 1, 3, ..: exp2(c S - lse log2 e), summed
+//   warp 8               TMA
+// Each tile's 128 terms are summed in four chains, and the tiles' sums with
+// compensation, so that the error does not grow with the prompt's length.
+//
+// Few keys: the query tiles are dealt to the CTAs of a cluster, whose
+// sums are joined through distributed shared memory in rank order.  A token's
+// weight is added once per sequence and call (red.add: a block that several
+// sequences share gets every part).
+#include <cooperative_groups.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "ee_cache_ops.cuh"
+#include "ee_tcgen05.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace ee {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kKeys = 128;
+constexpr int kCols = 128;     // query rows per tile
+constexpr int kThreads = 320;
+constexpr int kBuf = 4;        // S buffers of 128 tensor-memory columns
+constexpr int kMaxCluster = 8;
 
 template <int HD>
-__global__ void __launch_bounds__(kWarps * 32) k_prompt_weights(const PromptParams p) {
-  constexpr int E = HD / 32;
-  const int s = blockIdx.z, g = blockIdx.y, lane = threadIdx.x & 31, G = p.n_heads / p.c.n_kv_heads;
+struct Shape {
+  static constexpr int H = HD / 64;
+  static constexpr uint32_t kTile = 128 * HD * 2;
+  static constexpr uint32_t kHalf = 128 * 128;
+  static constexpr int NST = HD == 128 ? 4 : 6;
+  static constexpr size_t kSmem = 1024 + (1 + NST) * (size_t)kTile;
+};
+
+struct Maps {
+  CUtensorMap q, k;
+};
+
+struct Shared {
+  uint64_t k_full, q_full[8], q_empty[8], s_full[kBuf], s_free[kBuf];
+  uint32_t tmem;
+  alignas(16) float lse[2][2][kCols];  // by warpgroup, two tiles
+  float sum[2][kKeys];
+};
+
+template <int HD, int G, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_prompt_weights(const PromptParams p, const __grid_constant__ Maps maps, const Exponent ex) {
+  using S = Shape<HD>;
+  constexpr int kPos = kCols / G;  // positions per query tile
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* tiles = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nsplit = SPLIT ? (int)cg::this_cluster().num_blocks() : 1;
+  const int split = SPLIT ? (int)cg::this_cluster().block_rank() : 0;
+  // first keys first: most rows see them
+  const int unit = blockIdx.x / nsplit;
+  const int g = unit % p.c.n_kv_heads, s = unit / p.c.n_kv_heads % p.n_seqs;
+  const int key0 = unit / p.c.n_kv_heads / p.n_seqs * kKeys;
   const PromptSeq sq = prompt_seq(p, s);
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= sq.ctx) return;
-  bool ok;
-  const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, s, t, p.c.err, &ok);
-  const size_t slot = ((size_t)b * p.c.n_kv_heads + g) * 16 + (t & 15);
-  float k[E], w = 0.0f;
-  for (int e = 0; e < E; ++e) k[e] = __half2float(__ushort_as_half(p.c.k[slot * HD + lane * E + e])) * rsqrtf((float)HD);
-  for (int i = max(0, t - (sq.ctx - sq.n)); i < sq.n; ++i)
-    for (int h = g * G; h < (g + 1) * G; ++h) {
-      const int64_t row = sq.first + i;
-      float z = 0.0f;
-      for (int e = 0; e < E; ++e)
-        z = fmaf(k[e], __half2float(__ushort_as_half(p.q[row * p.q_stride + h * HD + lane * E + e])), z);
-      z = warp_sum(z);
-      const float lse = p.lse_in[(size_t)h * p.total_q + row];
-      if (lse != -INFINITY) w += expf(z - lse);
+  const int off = sq.ctx - sq.n;
+  const int first = max(0, key0 - off);  // first row that sees a key of the tile
+  if (key0 >= sq.ctx || first >= sq.n) return;  // the whole cluster
+  const int all = (sq.n - first + kPos - 1) / kPos;
+  const int nq = (all - split + nsplit - 1) / nsplit;  // this CTA's: tiles split, split + nsplit, ...
+  auto tile_row = [&](int j) { return first + (split + j * nsplit) * kPos; };
+
+  if (tid == 0) {
+    mbar_init(&sh.k_full, 1);
+    for (int i = 0; i < S::NST; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
     }
-  if (lane == 0 && ok) atomicAdd(p.c.weights + slot, w);
+    for (int i = 0; i < kBuf; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], 128);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(&sh.tmem, kBuf * kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t k_s = smem_addr(tiles), q_s = k_s + S::kTile;
+
+  if (warp == 8) {
+    const int here = min(8, ((sq.ctx + 15) >> 4) - key0 / 16);  // blocks of the key tile
+    const int b8 = lane & 7, half = lane >> 3;
+    if (nq > 0) {
+      int id = b8 < here ? p.c.table[(int64_t)s * p.c.table_stride + key0 / 16 + b8] : 0;
+      if (id < 0 || id >= p.c.n_blocks) {
+        report(p.c.err, EE_DERR_BLOCK);
+        id = 0;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&sh.k_full, (uint32_t)here * 16 * HD * 2);
+      __syncwarp();
+      if (half < S::H && b8 < here)
+        tma_load_2d(k_s + half * S::kHalf + b8 * 2048, &maps.k, half * 64, (id * p.c.n_kv_heads + g) * 16, &sh.k_full);
+    }
+    if (lane == 0) {
+      int issued = 0;
+      for (int j = 0; j < nq; ++j, ++issued) {
+        const int st = j % S::NST, pass = j / S::NST;
+        if (pass > 0 && !mbar_wait_bounded(&sh.q_empty[st], (pass - 1) & 1, p.c.err, DERR_EMPTY_WAIT)) break;
+        mbar_arrive_expect_tx(&sh.q_full[st], S::kTile);
+        for (int h = 0; h < S::H; ++h)
+          tma_load_3d(q_s + st * S::kTile + h * S::kHalf, &maps.q, h * 64, g * G, sq.first + tile_row(j), &sh.q_full[st]);
+      }
+      if (issued < nq)  // copies land before the CTA ends
+        for (int i = max(0, issued - S::NST); i < issued; ++i)
+          mbar_wait_bounded(&sh.q_full[i % S::NST], (i / S::NST) & 1, p.c.err, DERR_DRAIN_WAIT);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0 && nq > 0) {
+      constexpr uint32_t idesc = instr_desc(0, kCols, 128);
+      bool ok = mbar_wait_bounded(&sh.k_full, 0, p.c.err, DERR_FULL_WAIT);
+      for (int j = 0; j < nq && ok; ++j) {
+        const int st = j % S::NST, b = j % kBuf;
+        ok = mbar_wait_bounded(&sh.q_full[st], (j / S::NST) & 1, p.c.err, DERR_FULL_WAIT);
+        if (ok && j >= kBuf) ok = mbar_wait_bounded(&sh.s_free[b], (j / kBuf - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * S::kHalf + (kk & 3) * 32;
+          mma_f16(tmem + b * kCols, smem_desc_sw128(k_s + o), smem_desc_sw128(q_s + st * S::kTile + o), idesc, kk > 0);
+        }
+        mma_commit(&sh.q_empty[st]);
+        mma_commit(&sh.s_full[b]);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int t = warp >> 2, r = tid & 127;
+    const int key = key0 + r;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    // column r of a tile: its lse in the exponent's unit, +inf for a row that adds nothing
+    auto load_lse = [&](int j) {
+      if (j >= nq) return 0.0f;
+      const int row = tile_row(j) + r / G;
+      if (row >= sq.n) return INFINITY;
+      const float v = p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row];
+      return v == -INFINITY ? INFINITY : fmaf(v, ex.f_hi, v * ex.f_lo);
+    };
+    float sum = 0.0f, comp = 0.0f, next = load_lse(t);
+    const uint64_t c2 = pack2(ex.c, ex.c);
+    bool ok = true;
+    for (int j = t; j < nq; j += 2) {
+      float* ls = sh.lse[t][(j >> 1) & 1];
+      ls[r] = -next;
+      next = load_lse(j + 2);
+      // the other buffer was read two tiles ago, before the barrier of the last one
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+      const int b = j % kBuf, row0 = tile_row(j);
+      // after a wait that gave up the loop goes on without waiting: every thread
+      // still meets the warpgroup's barriers
+      if (ok) ok = warp_wait(&sh.s_full[b], (j / kBuf) & 1, p.c.err, DERR_FULL_WAIT);
+      tc_fence_after();
+      uint32_t v[kCols];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(tmem + b * kCols + lane_base + 32 * i, v + 32 * i);
+      tmem_wait_ld();
+      tmem_pin<kCols>(v);
+      tc_fence_before();
+      mbar_arrive(&sh.s_free[b]);
+      if (off + row0 < key0 + kKeys - 1 || row0 + kPos > sq.n) {
+        // rows before the key, rows of no one: -inf
+        const int lo = (key - off - row0) * G, hi = (sq.n - row0) * G;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+          if (i < lo || i >= hi) v[i] = 0xff800000u;
+      }
+      uint64_t acc[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < kCols; i += 4) {
+        const float4 l4 = *reinterpret_cast<const float4*>(ls + i);
+        const float2 x = unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, pack2(l4.x, l4.y)));
+        const float2 y = unpack2(fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), c2, pack2(l4.z, l4.w)));
+        acc[0] = add2(acc[0], pack2(ex2(x.x), ex2(x.y)));
+        acc[1] = add2(acc[1], pack2(ex2(y.x), ex2(y.y)));
+      }
+      const float2 a = unpack2(add2(acc[0], acc[1]));
+      const float y = (a.x + a.y) - comp, u = sum + y;  // compensated sum over the tiles
+      comp = (u - sum) - y;
+      sum = u;
+    }
+    sh.sum[t][r] = sum;
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, kBuf * kCols);
+  }
+  if (SPLIT) cg::this_cluster().sync();
+  if (split == 0 && tid < kKeys && key0 + tid < sq.ctx) {
+    float w = sh.sum[0][tid] + sh.sum[1][tid];
+    if (SPLIT)
+      for (int k = 1; k < nsplit; ++k) {
+        const Shared* o = cg::this_cluster().map_shared_rank(&sh, k);
+        w += o->sum[0][tid] + o->sum[1][tid];
+      }
+    bool ok;
+    const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, s, key0 + tid, nullptr, &ok);
+    if (ok) atomicAdd(p.c.weights + ((size_t)b * p.c.n_kv_heads + g) * 16 + (tid & 15), w);
+  }
+  if (SPLIT) cg::this_cluster().sync();  // nobody leaves while its sums are read
+}
+
+template <int HD, int G>
+cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
+  using S = Shape<HD>;
+  static std::atomic<uint64_t> prepared{0};  // a bit per device
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(k_prompt_weights<HD, G, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_prompt_weights<HD, G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) prepared.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  Maps maps;
+  const uint64_t qd[3] = {(uint64_t)HD, (uint64_t)p.n_heads, (uint64_t)p.total_q};
+  const uint64_t qs[2] = {(uint64_t)HD * 2, (uint64_t)p.q_stride * 2};
+  const uint32_t qb[3] = {64, (uint32_t)G, kCols / (uint32_t)G};
+  const uint64_t cd[2] = {(uint64_t)HD, (uint64_t)p.c.n_blocks * p.c.n_kv_heads * 16}, cs[1] = {(uint64_t)HD * 2};
+  const uint32_t cb[2] = {64, 16};
+  if (!encode_tensor_map(&maps.q, false, 3, p.q, qd, qs, qb) || !encode_tensor_map(&maps.k, false, 2, p.c.k, cd, cs, cb))
+    return cudaErrorInvalidValue;
+  const Exponent ex = make_exponent(HD);
+  const int64_t units = (int64_t)((p.c.max_ctx + kKeys - 1) / kKeys) * p.n_seqs * p.c.n_kv_heads;
+  int split = 1;
+  while (split < kMaxCluster && units * split * 2 <= sms) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  if (split == 1) return cudaLaunchKernelEx(&cfg, k_prompt_weights<HD, G, false>, p, maps, ex);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_prompt_weights<HD, G, true>, p, maps, ex);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_weights(const PromptParams& p, cudaStream_t st) {
-  const dim3 grid((p.c.max_ctx + kWarps - 1) / kWarps, p.c.n_kv_heads, p.n_seqs);
-  if (p.c.head_dim == 64)
-    k_prompt_weights<64><<<grid, kWarps * 32, 0, st>>>(p);
-  else
-    k_prompt_weights<128><<<grid, kWarps * 32, 0, st>>>(p);
-  return cudaGetLastError();
+  const int G = p.n_heads / p.c.n_kv_heads, hd = p.c.head_dim;
+#define EE_WEIGHTS_CASE(HD_, G_) \
+  if (hd == HD_ && G == G_) return launch_t<HD_, G_>(p, st);
+  EE_WEIGHTS_CASE(64, 1)
+  EE_WEIGHTS_CASE(64, 2)
+  EE_WEIGHTS_CASE(64, 4)
+  EE_WEIGHTS_CASE(64, 8)
+  EE_WEIGHTS_CASE(128, 1)
+  EE_WEIGHTS_CASE(128, 2)
+  EE_WEIGHTS_CASE(128, 4)
+  EE_WEIGHTS_CASE(128, 8)
+#undef EE_WEIGHTS_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace ee

@@ -430,8 +430,8 @@ ee_status ee_op_attention_noalloc(int32_t B, int32_t n_heads, int32_t n_kv_heads
  *    fp32 (device); token t of sequence s sits in block
  *    block_table[s * bt_stride + t / 16], slot t % 16.  Only the entries of
  *    tokens that exist are read.  head_dim 64 or 128, Hq / Hkv in {1, 2, 4, 8},
- *    at most EE_MAX_BATCH sequences, max_ctx <= 16384.  q, the caches and o
- *    are 16-byte aligned, the other arrays by their element's size.
+ *    at most EE_MAX_BATCH sequences, max_ctx <= 16384.  q, o, the caches and
+ *    the weights are 16-byte aligned, the other arrays by their element's size.
  *  - They need no scratch, allocate nothing and keep nothing between calls: calls
  *    on different streams, and captured ones, share no memory but the
  *    caller's.

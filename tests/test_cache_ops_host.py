@@ -57,7 +57,7 @@ def test_prompt_attention_refuses(lib, kw):
     assert prompt_attention(lib, **kw) == 1
 
 
-@pytest.mark.parametrize("kw", CACHE + GROUP + ROWS + [dict(lse=None), dict(weights=None), dict(weights=2)], ids=str)
+@pytest.mark.parametrize("kw", CACHE + GROUP + ROWS + [dict(lse=None), dict(weights=None), dict(weights=4)], ids=str)
 def test_prompt_weights_refuses(lib, kw):
     assert prompt_weights(lib, **kw) == 1
 
@@ -69,7 +69,7 @@ def test_attention_weights_refuses(lib, kw):
 
 
 @pytest.mark.parametrize("kw", CACHE + [dict(B=0), dict(B=65), dict(keep=0), dict(keep=65), dict(recent=-1), dict(recent=9),
-                                        dict(weights=None), dict(ctx=None), dict(new_ctx=None), dict(new_ctx=16), dict(kept=2),
+                                        dict(weights=None), dict(weights=24), dict(ctx=None), dict(new_ctx=None), dict(new_ctx=16), dict(kept=2),
                                         dict(dst=16, dst_stride=0), dict(dst=16, dst_stride=1, keep=17), dict(dst=2)], ids=str)
 def test_evict_refuses(lib, kw):
     assert evict(lib, **kw) == 1
