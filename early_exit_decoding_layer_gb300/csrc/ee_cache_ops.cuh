@@ -134,58 +134,65 @@ EE_DEV PromptSeq prompt_seq(const PromptParams& p, int s) {
 }
 
 // Tiles of `rows` rows of every sequence, numbered so that those with the most keys
-// come first (the grid starts them first): a tile's level is its last row's
+// come first (they are started first): a tile's level is its last row's
 // position over `rows`, levels count down, and within a level the sequences
-// count up.  A whole warp looks tile number `rank` up; s = -1: there is none.
+// count up.  A whole warp holds the index, two sequences per lane.
 struct PromptTile {
-  int s, i0;  // sequence, the tile's first row within it
+  int s, i0;  // sequence (-1: there is no such tile), the tile's first row within it
   PromptSeq sq;
 };
-EE_DEV PromptTile prompt_tile(const PromptParams& p, int rank, int rows) {
-  static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
-  const int lane = threadIdx.x & 31;
-  int base[2], nt[2], top = 0;
+struct PromptIndex {
   PromptSeq sq[2];
+  int base[2], end[2], top, rows;
+
+  EE_DEV void init(const PromptParams& p, int rows_) {
+    static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
+    rows = rows_;
+    top = 0;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int s = lane + 32 * u;
-    sq[u] = s < p.n_seqs ? prompt_seq(p, s) : PromptSeq{0, 0, 0};
-    nt[u] = (sq[u].n + rows - 1) / rows;
-    base[u] = max(0, sq[u].ctx - sq[u].n) / rows;
-    top = max(top, base[u] + nt[u]);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  // tiles at level l or above
-  auto above = [&](int l) {
-    const int c = min(max(base[0] + nt[0] - l, 0), nt[0]) + min(max(base[1] + nt[1] - l, 0), nt[1]);
-    return (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
-  };
-  PromptTile r = {-1, 0, {0, 0, 0}};
-  if (rank >= above(0)) return r;
-  int lo = 0, hi = top;  // above(lo) > rank >= above(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (above(mid) > rank) lo = mid;
-    else hi = mid;
-  }
-  int idx = rank - above(hi);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const unsigned m = __ballot_sync(0xffffffffu, base[u] <= lo && lo < base[u] + nt[u]);
-    const int c = __popc(m);
-    if (r.s < 0 && idx < c) {
-      const int src = __fns(m, 0, idx + 1);
-      r.s = src + 32 * u;
-      r.i0 = (lo - __shfl_sync(0xffffffffu, base[u], src)) * rows;
-      r.sq.first = __shfl_sync(0xffffffffu, sq[u].first, src);
-      r.sq.n = __shfl_sync(0xffffffffu, sq[u].n, src);
-      r.sq.ctx = __shfl_sync(0xffffffffu, sq[u].ctx, src);
-    } else {
-      idx -= c;
+    for (int u = 0; u < 2; ++u) {
+      const int s = (threadIdx.x & 31) + 32 * u;
+      sq[u] = s < p.n_seqs ? prompt_seq(p, s) : PromptSeq{0, 0, 0};
+      base[u] = max(0, sq[u].ctx - sq[u].n) / rows;
+      end[u] = base[u] + (sq[u].n + rows - 1) / rows;
+      top = max(top, end[u]);
     }
+    top = __reduce_max_sync(0xffffffffu, top);
   }
-  return r;
-}
+  // tiles at level l or above
+  EE_DEV int above(int l) const {
+    const int c = max(end[0] - max(base[0], l), 0) + max(end[1] - max(base[1], l), 0);
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
+  }
+  EE_DEV PromptTile find(int rank) const {
+    PromptTile r = {-1, 0, {0, 0, 0}};
+    if (rank >= above(0)) return r;
+    int lo = 0, hi = top;  // above(lo) > rank >= above(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (above(mid) > rank) lo = mid;
+      else hi = mid;
+    }
+    int idx = rank - above(hi);  // the idx-th sequence with a tile at level lo
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool has = base[u] <= lo && lo < end[u];
+      const unsigned m = __ballot_sync(0xffffffffu, has);
+      const int lane = threadIdx.x & 31;
+      const unsigned hit = __ballot_sync(0xffffffffu, has && __popc(m & ((1u << lane) - 1u)) == idx);
+      if (hit && r.s < 0) {
+        const int src = __ffs(hit) - 1;
+        r.s = src + 32 * u;
+        r.i0 = (lo - __shfl_sync(0xffffffffu, base[u], src)) * rows;
+        r.sq.first = __shfl_sync(0xffffffffu, sq[u].first, src);
+        r.sq.n = __shfl_sync(0xffffffffu, sq[u].n, src);
+        r.sq.ctx = __shfl_sync(0xffffffffu, sq[u].ctx, src);
+      }
+      idx -= __popc(m);
+    }
+    return r;
+  }
+};
 #endif
 
 }  // namespace ee

@@ -54,6 +54,12 @@ EE_DEV void st_shared_v4(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+EE_DEV void st_global_v8(void* p, const uint32_t* v) {  // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 EE_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 EE_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -149,6 +155,12 @@ EE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code
 EE_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+EE_DEV float max3(float a, float b, float c) {  // NaN only if all three are
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 

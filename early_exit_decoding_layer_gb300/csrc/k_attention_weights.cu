@@ -18,6 +18,7 @@
 // everything is fp32 but the fp16 cache.
 #include <cooperative_groups.h>
 #include <math.h>
+#include <stdlib.h>
 
 #include <atomic>
 
@@ -29,9 +30,9 @@ namespace cg = cooperative_groups;
 namespace ee {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;      // blocks in flight per warp
+constexpr int kStages = 2;  // blocks of a warp in shared memory
 constexpr int kMaxCluster = 16;
 
 struct Maps {
@@ -42,8 +43,8 @@ template <int HD, int G>
 struct Layout {
   static constexpr uint32_t kTile = 16 * HD * 2;  // K or V of one block and kv head
   static constexpr uint32_t kRing = kWarps * kStages * 2 * kTile;
-  // what the warps join, in the ring's space: acc [warp][G][HD]
-  static_assert(kWarps * G * HD * 4 <= kRing, "join space");
+  // what is joined, in the ring's space: acc [warp][G][HD], then the CTA's [G][HD]
+  static_assert((kWarps + 1) * G * HD * 4 <= kRing, "join space");
 };
 
 template <int HD, int G>
@@ -51,10 +52,11 @@ struct Shared {
   uint64_t full[kWarps][kStages];
   alignas(16) float q[G][HD];
   alignas(16) float p[kWarps][16][G];
-  alignas(16) float acc[G][HD];   // of the CTA, relative to m
   float wm[kWarps][G], wl[kWarps][G];
-  float m[G], l[G];               // of the CTA
-  float M[G], inv[G];             // of the whole sequence
+  float m[G], l[G];                      // of the CTA
+  float cm[kMaxCluster][G], cl[kMaxCluster][G];  // of every rank
+  float f[kMaxCluster][G];               // what a rank's acc counts in the whole
+  float M[G], inv[G];                    // of the whole sequence
 };
 
 template <int HD, int G>
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int e = 0; e < E; ++e) wacc[(warp * G + h) * HD + d0 + e] = acc[h][e];
   __syncthreads();
+  float* cacc = wacc + kWarps * G * HD;
   for (int i = tid; i < G * HD; i += kThreads) {
     const int h = i / HD;
     float mm = -INFINITY, a = 0.0f, ll = 0.0f;
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads)
         ll = fmaf(f, sh.wl[w][h], ll);
       }
     }
-    sh.acc[h][i % HD] = a;
+    cacc[i] = a;
     if (i % HD == 0) {
       sh.m[h] = mm;
       sh.l[h] = ll;
@@ -263,24 +266,33 @@ __global__ void __launch_bounds__(kThreads)
   }
   cl.sync();
   // the CTAs join: every rank finds M and L, rank r a share of the outputs
+  for (int i = tid; i < C * G; i += kThreads) {
+    const Shared<HD, G>* o = cl.map_shared_rank(&sh, i / G);
+    sh.cm[i / G][i % G] = o->m[i % G];
+    sh.cl[i / G][i % G] = o->l[i % G];
+  }
+  __syncthreads();
   if (tid < G) {
     float mm = -INFINITY, ll = 0.0f;
-    for (int k = 0; k < C; ++k) mm = fmaxf(mm, cl.map_shared_rank(&sh, k)->m[tid]);
+    for (int k = 0; k < C; ++k) mm = fmaxf(mm, sh.cm[k][tid]);
     for (int k = 0; k < C; ++k) {
-      const Shared<HD, G>* o = cl.map_shared_rank(&sh, k);
-      if (o->l[tid] != 0.0f) ll = fmaf(o->m[tid] == mm ? 1.0f : ex2(o->m[tid] - mm), o->l[tid], ll);
+      const float f = sh.cl[k][tid] == 0.0f ? 0.0f : sh.cm[k][tid] == mm ? 1.0f : ex2(sh.cm[k][tid] - mm);
+      sh.f[k][tid] = f;
+      if (f != 0.0f) ll = fmaf(f, sh.cl[k][tid], ll);
     }
     sh.M[tid] = mm;
     sh.inv[tid] = ll == 0.0f ? 0.0f : 1.0f / ll;
   }
   __syncthreads();
-  for (int i = rank * kThreads + tid; i < G * HD; i += C * kThreads) {
+  const int share = (G * HD + C - 1) / C;
+  for (int i = rank * share + tid; i < min(G * HD, (rank + 1) * share); i += kThreads) {
     const int h = i / HD;
-    float a = 0.0f;
-    for (int k = 0; k < C; ++k) {
-      const Shared<HD, G>* o = cl.map_shared_rank(&sh, k);
-      if (o->l[h] != 0.0f) a = fmaf(o->m[h] == sh.M[h] ? 1.0f : ex2(o->m[h] - sh.M[h]), o->acc[h][i % HD], a);
-    }
+    float v[kMaxCluster], a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) v[k] = k < C ? cl.map_shared_rank(cacc, k)[i] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k)
+      if (k < C && sh.f[k][h] != 0.0f) a = fmaf(sh.f[k][h], v[k], a);
     p.o[((size_t)s * p.n_heads + g * G) * HD + i] = a * sh.inv[h];
   }
   // the weights of this CTA's tokens
@@ -322,6 +334,8 @@ cudaError_t launch_t(const DecodeWeightsParams& p, cudaStream_t st) {
   const int units = p.batch * p.c.n_kv_heads, nb = (p.c.max_ctx + 15) / 16;
   auto smem = [&](int C) { return 1024 + (size_t)Lay::kRing + (size_t)G * ((nb + C - 1) / C) * 16 * 4; };
   int C = 1;
+  const char* ec = getenv("EE_C");
+  if (ec) C = atoi(ec); else
   while (C < kMaxCluster && (smem(C) > (size_t)kMaxSmem || (units * C < 2 * sms && nb > C * kWarps))) C *= 2;
   if (smem(C) > (size_t)kMaxSmem) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};

@@ -6,9 +6,12 @@
 // serves the whole group.  The rows are two M = 128 tiles with a softmax
 // warpgroup each; while one is busy with its probabilities the tensor core works
 // for the other:
-//   warp 9 (one thread)  S_t = Q_t K_j^T, then O_t += P_t V_j, for t = 0, 1 in turn
+//   warp 9 (one thread)  O_t += P_t V_j, then S_t = Q_t K_{j + 1}^T, t = 0, 1 in turn
 //   warps 4t .. 4t + 3   a thread per row: S_t to registers, the running maximum
-//                        and sum, P_t = exp2(c S - c m) as fp16 over S_t's columns
+//                        and sum, P_t = exp2(c S - c m) as fp16 over S_t's columns;
+//                        S_t of a step also says that the K and V before are free
+//   warp 10              waits for K and V tiles in warp 9's place
+//   warp 11              finds the CTA's next units of work
 //   warp 8               K and V tiles of 128 keys by TMA, one copy per 16-slot
 //                        block and 64 columns, into a ring of NST tiles
 // The running maximum may lag behind by up to 8 (in log2): then P is at most 2^8
@@ -41,8 +44,10 @@ namespace {
 
 constexpr int kRows = 256;     // rows of S per CTA: two tiles of 128
 constexpr int kKeys = 128;     // keys per step
-constexpr int kThreads = 320;  // two softmax warpgroups, TMA, MMA
+constexpr int kThreads = 384;  // two softmax warpgroups, TMA, MMA, landed tiles, units
 constexpr int kMaxCluster = 8;
+constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsSingle = 88;  // at launch, and after
+static_assert(256 * kRegsSoftmax + 128 * kRegsSingle <= kThreads * kRegs, "no more than the launch has");
 
 template <int HD>
 struct Shape {
@@ -59,16 +64,50 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
-struct Shared {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_ready[2], o_done[2];
-  uint32_t tmem;
-  int bad_v;            // a non-finite V value was replaced
-  float m[kRows], l[kRows];
-};
-
 // log of the sum of exp(s / sqrt(hd)), from its sum l relative to the score m.
 EE_DEV float log_sum(float m, float l, const Exponent& ex) {
   return l == 0.0f ? -INFINITY : fmaf(m, ex.unit_hi, fmaf(m, ex.unit_lo, logf(l)));
+}
+
+// The work of one CTA on one (tile of rows, kv head): key tiles [ka, kb) of 128,
+// of which row tile t takes the first n[t]; those from jm[t] on are not seen whole by
+// every row of it.
+struct Unit {
+  PromptTile tl;
+  int g, off, ka, kb, n[2], jm[2];
+};
+
+constexpr int kUnits = 4;  // units known ahead
+
+struct Shared {
+  uint64_t q_full, q_free, kv_full[8], kv_empty[8], s_full[2], p_ready[2], o_done[2];
+  uint64_t unit_full[kUnits], unit_free[kUnits];
+  Unit unit[kUnits];
+  uint32_t tmem;
+  int bad_v[8];  // [unit & 7]: the last unit in which a non-finite V value was replaced
+  float m[kRows], l[kRows];
+};
+
+template <int G>
+EE_DEV Unit make_unit(const PromptTile& tl, int g, int split, int nsplit) {
+  constexpr int kPos = kRows / G;
+  Unit u;
+  u.tl = tl;
+  u.g = g;
+  u.off = tl.sq.ctx - tl.sq.n;  // position of row 0
+  int nt[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int r0 = tl.i0 + t * (kPos / 2), r1 = min(tl.sq.n, r0 + kPos / 2);
+    nt[t] = r1 > r0 ? max(0, u.off + r1 + kKeys - 1) / kKeys : 0;
+    u.jm[t] = max(0, u.off + r0 + 1) / kKeys;
+  }
+  const int all = max(nt[0], nt[1]), each = (all + nsplit - 1) / nsplit;
+  u.ka = min(all, split * each);
+  u.kb = min(all, u.ka + each);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) u.n[t] = max(0, min(nt[t], u.kb) - u.ka);
+  return u;
 }
 
 template <int HD, int G, bool SPLIT>
@@ -83,41 +122,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nsplit = SPLIT ? (int)cg::this_cluster().num_blocks() : 1;
   const int split = SPLIT ? (int)cg::this_cluster().block_rank() : 0;
-  const int unit = blockIdx.x / nsplit;
-  const int g = unit % p.c.n_kv_heads;
-  const PromptTile tl = prompt_tile(p, unit / p.c.n_kv_heads, kPos);
-  if (tl.s < 0) return;  // the whole cluster
-  const int off = tl.sq.ctx - tl.sq.n;  // position of row 0
-
-  // keys that tile t's rows see, in tiles: [0, nt[t]); those from jm[t] on are
-  // not seen whole by every row
-  int ka = 0, kb, nt[2], jm[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int r0 = tl.i0 + t * (kPos / 2), r1 = min(tl.sq.n, r0 + kPos / 2);
-    nt[t] = r1 > r0 ? max(0, off + r1 + kKeys - 1) / kKeys : 0;
-    jm[t] = max(0, off + r0 + 1) / kKeys;
-  }
-  kb = max(nt[0], nt[1]);
-  if (SPLIT) {
-    const int each = (kb + nsplit - 1) / nsplit;
-    ka = min(kb, split * each);
-    kb = min(kb, ka + each);
-  }
-  const int n0 = max(0, min(nt[0], kb) - ka), n1 = max(0, min(nt[1], kb) - ka), nk = kb - ka;
-
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_free, 2);  // a thread of each warpgroup
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_ready[t], 128);
+      mbar_init(&sh.p_ready[t], 129);  // its warpgroup, and V and K landed
       mbar_init(&sh.o_done[t], 1);
     }
-    sh.bad_v = 0;
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&sh.unit_full[i], 1);
+      mbar_init(&sh.unit_free[i], 11);  // every warp but the one that finds them
+    }
+    for (int i = 0; i < 8; ++i) sh.bad_v[i] = -1;
     fence_mbar_init();
   }
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
@@ -129,256 +150,377 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tensor memory: S_t (128 columns, P_t over its first 64), then O_t
   auto s_col = [&](int t) { return tmem + t * 128; };
   auto o_col = [&](int t) { return tmem + 256 + t * HD; };
+  // Ring items count on over the units: item base + 2 j is K of the unit's key tile
+  // ka + j, item base + 2 j + 1 its V.
+  auto stage = [&](int i) { return i % S::NST; };
+  auto phase = [&](int i) { return (uint32_t)(i / S::NST) & 1; };
 
-  if (warp == 8) {
-    // ring item 2 j is K of key tile ka + j, item 2 j + 1 its V
-    const int ntok = tl.sq.ctx, nblk = (ntok + 15) >> 4;
-    const int32_t* bt = p.c.table + (int64_t)tl.s * p.c.table_stride;
-    if (lane == 0 && nk > 0) {
-      mbar_arrive_expect_tx(&sh.q_full, (n0 > 0 ? S::kTile : 0) + (n1 > 0 ? S::kTile : 0));
-      for (int t = 0; t < 2; ++t)
-        if ((t ? n1 : n0) > 0)
-          for (int h = 0; h < S::H; ++h)
-            tma_load_3d(q_s + t * S::kTile + h * S::kHalf, &maps.q, h * 64, g * G,
-                        tl.sq.first + tl.i0 + t * (kPos / 2), &sh.q_full);
+  // Unit i of this CTA, found by warp 11; s = -1: no more.
+  auto unit_at = [&](int i) {
+    Unit u;
+    u.tl.s = -1;
+    if (warp_wait(&sh.unit_full[i % kUnits], (i / kUnits) & 1, p.c.err, DERR_FULL_WAIT)) {
+      u = sh.unit[i % kUnits];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.unit_free[i % kUnits]);
     }
+    return u;
+  };
+
+  // Registers go from the four single warps to the softmax warps, which hold a row of
+  // S: 128 x 88 + 256 x 208 is what 384 threads are launched with at 168 each
+  // (launch_t checks that).
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSingle));
+  if (warp == 11) {
+    // Not split: a CTA takes units until there are none, every second round in the
+    // opposite order, which evens out what the falling sizes leave uneven.
+    // Split: a cluster has one.
+    PromptIndex index;
+    index.init(p, kPos);
+    for (int i = 0;; ++i) {
+      int at = blockIdx.x / nsplit;
+      if (!SPLIT) at = i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      PromptTile tl = {-1, 0, {0, 0, 0}};
+      if (!SPLIT || i == 0) tl = index.find(at / p.c.n_kv_heads);
+      const Unit u = make_unit<G>(tl, at % p.c.n_kv_heads, split, nsplit);
+      if (i >= kUnits && !warp_wait(&sh.unit_free[i % kUnits], (i / kUnits - 1) & 1, p.c.err, DERR_EMPTY_WAIT)) break;
+      if (lane == 0) {
+        sh.unit[i % kUnits] = u;
+        mbar_arrive(&sh.unit_full[i % kUnits]);
+      }
+      __syncwarp();
+      if (tl.s < 0) break;
+    }
+  } else if (warp == 8) {
+    Unit u = unit_at(0);
     const int b8 = lane & 7, half = lane >> 3;
-    auto block_id = [&](int j) {  // of block b8 of key tile j
-      const int b = j * 8 + b8;
-      int id = b < nblk && j < kb ? bt[b] : 0;
-      if (id < 0 || id >= p.c.n_blocks) {
-        report(p.c.err, EE_DERR_BLOCK);
-        id = 0;
-      }
-      return id;
-    };
-    int id = block_id(ka), issued = 0;
+    int issued = 0, loads = 0;
     bool ok = true;
-    for (int j = ka; j < kb && ok; ++j) {
-      const int next = block_id(j + 1), here = min(8, nblk - j * 8);
-      for (int kv = 0; kv < 2; ++kv, ++issued) {
-        const int st = issued % S::NST, pass = issued / S::NST;
-        if (pass > 0)
-          ok = warp_wait(&sh.kv_empty[st], (pass - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], (uint32_t)here * 16 * HD * 2);
+    for (int i = 0; u.tl.s >= 0 && ok; u = unit_at(++i)) {
+      const int nblk = (u.tl.sq.ctx + 15) >> 4;
+      const int32_t* bt = p.c.table + (int64_t)u.tl.s * p.c.table_stride;
+      auto block_id = [&](int j) {  // of block b8 of key tile j
+        const int b = j * 8 + b8;
+        int id = b < nblk && j < u.kb ? bt[b] : 0;
+        if (id < 0 || id >= p.c.n_blocks) {
+          report(p.c.err, EE_DERR_BLOCK);
+          id = 0;
+        }
+        return id;
+      };
+      int id = block_id(u.ka);
+      // a unit whose rows see anything has its Q loaded; q_free: the products of the
+      // one before have read theirs
+      if (u.kb > u.ka) {
+        if (loads > 0) ok = warp_wait(&sh.q_free, (loads - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+        ++loads;
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&sh.q_full, (u.n[0] > 0 ? S::kTile : 0) + (u.n[1] > 0 ? S::kTile : 0));
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (u.n[t] > 0)
+              for (int h = 0; h < S::H; ++h)
+                tma_load_3d(q_s + t * S::kTile + h * S::kHalf, &maps.q, h * 64, u.g * G,
+                            u.tl.sq.first + u.tl.i0 + t * (kPos / 2), &sh.q_full);
+        }
         __syncwarp();
-        if (half < S::H && b8 < here)
-          tma_load_2d(kv_s + st * S::kTile + half * S::kHalf + b8 * 2048, kv ? &maps.v : &maps.k, half * 64,
-                      (id * p.c.n_kv_heads + g) * 16, &sh.kv_full[st]);
       }
-      id = next;
+      for (int j = u.ka; j < u.kb && ok; ++j) {
+        const int next = block_id(j + 1), here = min(8, nblk - j * 8);
+        for (int kv = 0; kv < 2; ++kv, ++issued) {
+          const int st = stage(issued);
+          if (issued >= S::NST) ok = warp_wait(&sh.kv_empty[st], phase(issued - S::NST), p.c.err, DERR_EMPTY_WAIT);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], (uint32_t)here * 16 * HD * 2);
+          __syncwarp();
+          if (half < S::H && b8 < here)
+            tma_load_2d(kv_s + st * S::kTile + half * S::kHalf + b8 * 2048, kv ? &maps.v : &maps.k, half * 64,
+                        (id * p.c.n_kv_heads + u.g) * 16, &sh.kv_full[st]);
+        }
+        id = next;
+      }
     }
     if (!ok)  // copies land before the CTA ends
       for (int i = max(0, issued - S::NST); i < issued; ++i)
-        mbar_wait_bounded(&sh.kv_full[i % S::NST], (i / S::NST) & 1, p.c.err, DERR_DRAIN_WAIT);
+        mbar_wait_bounded(&sh.kv_full[stage(i)], phase(i), p.c.err, DERR_DRAIN_WAIT);
   } else if (warp == 9) {
-    if (lane == 0 && nk > 0) {
-      constexpr uint32_t id_qk = instr_desc(0, kKeys, 128), id_pv = instr_desc(0, HD, 128, true);
-      auto item = [&](int i) { return kv_s + (i % S::NST) * S::kTile; };
-      auto landed = [&](int i) {
-        const bool r = mbar_wait_bounded(&sh.kv_full[i % S::NST], (i / S::NST) & 1, p.c.err, DERR_FULL_WAIT);
-        tc_fence_after();
-        return r;
-      };
-      auto qk = [&](int t, int j) {
-        const uint32_t a = q_s + t * S::kTile, b = item(2 * j);
+    // One thread issues every MMA.  The tensor core takes an MMA from it when it
+    // starts on it, so what the thread does between two products costs the
+    // tensor core time: a step's O and next S products of a tile go out together,
+    // each wait that can be left to another warp is, and commits are few.  The
+    // commit behind S_t(j + 1) also says that O_t has P_t V_j.
+    Unit u = unit_at(0);
+    constexpr uint32_t id_qk = instr_desc(0, kKeys, 128), id_pv = instr_desc(0, HD, 128, true);
+    int base = 0, steps[2] = {0, 0}, loads = 0;
+    bool ok = true;
+    for (int i = 0; u.tl.s >= 0 && ok; u = unit_at(++i)) {
+      const int nk = u.kb - u.ka;
+      if (lane == 0 && nk > 0) {
+        auto qk = [&](int t, int j) {
+          const uint32_t a = q_s + t * S::kTile, b = kv_s + stage(base + 2 * j) * S::kTile;
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * S::kHalf + (kk & 3) * 32;
-          mma_f16(s_col(t), smem_desc_sw128(a + o), smem_desc_sw128(b + o), id_qk, kk > 0);
-        }
-        mma_commit(&sh.s_full[t]);
-      };
-      auto pv = [&](int t, int j) {
-        const uint32_t b = item(2 * j + 1);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_f16_ta(o_col(t), s_col(t) + kk * 8, smem_desc_sw128_mn(b + kk * 2048, S::kHalf), id_pv, j > 0 || kk > 0);
-        mma_commit(&sh.o_done[t]);
-      };
-      bool ok = mbar_wait_bounded(&sh.q_full, 0, p.c.err, DERR_FULL_WAIT) && landed(0);
-      if (ok) {
-        if (n0 > 0) qk(0, 0);
-        if (n1 > 0) qk(1, 0);
-        mma_commit(&sh.kv_empty[0]);
-      }
-      for (int j = 0; j < nk && ok; ++j) {
-        ok = landed(2 * j + 1);
-        for (int t = 0; t < 2 && ok; ++t) {
-          const int n = t ? n1 : n0;
-          if (j < n) {
-            ok = mbar_wait_bounded(&sh.p_ready[t], j & 1, p.c.err, DERR_FULL_WAIT);
-            tc_fence_after();
-            if (ok) pv(t, j);
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * S::kHalf + (kk & 3) * 32;
+            mma_f16(s_col(t), smem_desc_sw128(a + o), smem_desc_sw128(b + o), id_qk, kk > 0);
           }
-          if (t == 1) mma_commit(&sh.kv_empty[(2 * j + 1) % S::NST]);
-          if (t == 0 && j + 1 < nk && ok) ok = landed(2 * j + 2);
-          if (j + 1 < n && ok) qk(t, j + 1);
-          if (t == 1 && j + 1 < nk) mma_commit(&sh.kv_empty[(2 * j + 2) % S::NST]);
+          mma_commit(&sh.s_full[t]);
+        };
+        ok = mbar_wait_bounded(&sh.q_full, loads & 1, p.c.err, DERR_FULL_WAIT) &&
+             mbar_wait_bounded(&sh.kv_full[stage(base)], phase(base), p.c.err, DERR_FULL_WAIT);
+        tc_fence_after();
+        if (ok && u.n[0] > 0) qk(0, 0);
+        if (ok && u.n[1] > 0) qk(1, 0);
+        for (int j = 0; j < nk && ok; ++j) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int n = u.n[t];
+            if (j < n) {
+              // P_t(j) is in tensor memory, V_j and K_{j + 1} have landed
+              if (!(ok = mbar_wait_bounded(&sh.p_ready[t], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
+              ++steps[t];
+              tc_fence_after();
+              const uint32_t b = kv_s + stage(base + 2 * j + 1) * S::kTile;
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_f16_ta(o_col(t), s_col(t) + kk * 8, smem_desc_sw128_mn(b + kk * 2048, S::kHalf), id_pv,
+                           j > 0 || kk > 0);
+              if (j + 1 < n) qk(t, j + 1);
+              else mma_commit(&sh.o_done[t]);
+            }
+          }
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
+      base += 2 * nk;
+      loads += nk > 0;
     }
-    __syncwarp();
+  } else if (warp == 10) {
+    // Waits for V_j and K_{j + 1} on behalf of the MMA thread: P_t(j)'s barriers
+    // count this warp's arrival too.  In tiles that are masked for some row, V
+    // values that are not finite become 0 before the product reads them.
+    Unit u = unit_at(0);
+    int base = 0, steps[2] = {0, 0};
+    bool ok = true;
+    for (int i = 0; u.tl.s >= 0 && ok; u = unit_at(++i)) {
+      const int nk = u.kb - u.ka;
+      for (int j = 0; j < nk && ok; ++j) {
+        const int v = base + 2 * j + 1;
+        ok = warp_wait(&sh.kv_full[stage(v)], phase(v), p.c.err, DERR_FULL_WAIT);
+        if (ok && u.ka + j >= min(u.jm[0], u.jm[1])) {
+          uint8_t* vt = tiles + 2 * S::kTile + stage(v) * S::kTile;
+          const int chunks = (int)(S::kTile / 16) / 32;  // 16-byte chunks per lane
+          uint32_t any = 0;
+#pragma unroll 8
+          for (int k = 0; k < chunks; ++k) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vt + (k * 32 + lane) * 16);
+            any |= ((x.x & 0x7c007c00u) + 0x04000400u) | ((x.y & 0x7c007c00u) + 0x04000400u) |
+                   ((x.z & 0x7c007c00u) + 0x04000400u) | ((x.w & 0x7c007c00u) + 0x04000400u);
+          }
+          if (__any_sync(0xffffffffu, any & 0x80008000u)) {
+            bool fixed = false;
+            for (int k = 0; k < chunks; ++k) {
+              const int at = (k * 32 + lane) * 16;
+              uint32_t w[4];
+              *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(vt + at);
+              bool hit = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7c00u) == 0x7c00u) w[e] &= 0xffff0000u, hit = true;
+                if ((w[e] & 0x7c000000u) == 0x7c000000u) w[e] &= 0x0000ffffu, hit = true;
+              }
+              if (hit) {
+                *reinterpret_cast<uint4*>(vt + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                // rows of the tile are 128 bytes in each half
+                if ((u.ka + j) * kKeys + (at % (int)S::kHalf) / 128 < u.tl.sq.ctx) fixed = true;
+              }
+            }
+            if (__any_sync(0xffffffffu, fixed) && lane == 0) sh.bad_v[i & 7] = i;
+            fence_proxy_async();
+            __syncwarp();
+          }
+        }
+        if (ok && j + 1 < nk) ok = warp_wait(&sh.kv_full[stage(v + 1)], phase(v + 1), p.c.err, DERR_FULL_WAIT);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || j >= u.n[t]) continue;
+          // one phase of p_ready per step: the one before has to be over
+          if (steps[t] > 0) ok = warp_wait(&sh.p_ready[t], (steps[t] - 1) & 1, p.c.err, DERR_FULL_WAIT);
+          if (ok && lane == 0) mbar_arrive(&sh.p_ready[t]);
+          ++steps[t];
+        }
+      }
+      base += 2 * nk;
+    }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2, r = tid & 127;  // tile and row
-    const int n = t ? n1 : n0;
-    const int row = tl.i0 + t * (kPos / 2) + r / G;
-    const bool valid = row < tl.sq.n;
-    const int pos = valid ? off + row : -1;  // last key this row sees
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = s_col(t) + lane_base, o_at = o_col(t) + lane_base;
-    float m = -INFINITY, l = 0.0f;
+    Unit u = unit_at(0);
+    int base = 0, steps = 0, ends = 0;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = warp_wait(&sh.s_full[t], j & 1, p.c.err, DERR_FULL_WAIT))) break;
-      tc_fence_after();
-      uint32_t s[kKeys];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
-      tmem_wait_ld();
-      tmem_pin<kKeys>(s);
-      const bool masked = ka + j >= jm[t];
-      if (masked) {
-        const int lim = pos - (ka + j) * kKeys;
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i)
-          if (i > lim) s[i] = 0xff800000u;  // -inf
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < kKeys; i += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          mx[u] = fmaxf(mx[u], fmaxf(__uint_as_float(s[i + u]), __uint_as_float(s[i + 4 + u])));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (j == 0) {
-        m = mt;
-      } else if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
-        // some row's maximum has grown too far: this warp's rows of O and l go
-        // over to the new maxima, once the product before has been added
-        const float mn = fmaxf(m, mt);
-        const float a = m == mn ? 1.0f : ex2((m - mn) * c);
-        m = mn;
-        l *= a;
-        if (!(ok = warp_wait(&sh.o_done[t], (j - 1) & 1, p.c.err, DERR_FULL_WAIT))) break;
+    for (int i = 0; u.tl.s >= 0 && ok; u = unit_at(++i)) {
+      const int n = u.n[t], nk = u.kb - u.ka;
+      const int row = u.tl.i0 + t * (kPos / 2) + r / G;
+      const bool valid = row < u.tl.sq.n;
+      const int pos = valid ? u.off + row : -1;  // last key this row sees
+      // the tile whose products come last in a step: n[1] >= n[0] or n[1] = 0
+      const bool frees = r == 0 && t == (u.n[1] > 0 ? 1 : 0);
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < n && ok; ++j) {
+        if (!(ok = warp_wait(&sh.s_full[t], steps & 1, p.c.err, DERR_FULL_WAIT))) break;
+        ++steps;
         tc_fence_after();
-#pragma unroll 1
-        for (int i = 0; i < HD; i += 16) {
-          uint32_t o[16];
-          tmem_ld16(o_at + i, o);
+        if (frees) {  // the tiles of the products before are free
+          if (j > 0) mbar_arrive(&sh.kv_empty[stage(base + 2 * j - 1)]);
+          mbar_arrive(&sh.kv_empty[stage(base + 2 * j)]);
+        }
+        if (r == 0 && j == n - 1) mbar_arrive(&sh.q_free);  // the last product with this Q tile
+        const bool masked = u.ka + j >= u.jm[t];
+        uint32_t s[kKeys], ph[kKeys / 2];
+        auto load = [&]() {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
           tmem_wait_ld();
-          tmem_pin<16>(o);
+          tmem_pin<kKeys>(s);
+          if (masked) {
+            const int lim = pos - (u.ka + j) * kKeys;
 #pragma unroll
-          for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * a);
-          tmem_st16(o_at + i, o);
-        }
-      }
-      // a row that has seen nothing yet has m = -inf: its P is 0
-      const float mc = m == -INFINITY ? 0.0f : m * c;
-      const uint64_t c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
-      uint64_t sum[2] = {0, 0};
+            for (int i = 0; i < kKeys; ++i)
+              if (i > lim) s[i] = 0xff800000u;  // -inf
+          }
+        };
+        auto maximum = [&]() {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < kKeys; i += 32) {
-        uint32_t ph[16];
+          for (int i = 0; i < kKeys; i += 8)
 #pragma unroll
-        for (int u = 0; u < 32; u += 2) {
-          const float2 x =
-              unpack2(fma2(pack2(__uint_as_float(s[i + u]), __uint_as_float(s[i + u + 1])), c2, nm2));
-          const float e0 = ex2(x.x), e1 = ex2(x.y);
-          sum[(u >> 1) & 1] = add2(sum[(u >> 1) & 1], pack2(e0, e1));
-          const __half2 h = __floats2half2_rn(e0, e1);
-          ph[u >> 1] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        tmem_st16(s_at + i / 2, ph);
-      }
-      const float2 st = unpack2(add2(sum[0], sum[1]));
-      l += st.x + st.y;
-      if (masked) {
-        // V values that are not finite become 0 before the product reads them
-        const int it = 2 * j + 1;
-        if (!(ok = warp_wait(&sh.kv_full[it % S::NST], (it / S::NST) & 1, p.c.err, DERR_FULL_WAIT))) break;
-        uint8_t* vt = tiles + 2 * S::kTile + (it % S::NST) * S::kTile;
-        bool fixed = false;
-#pragma unroll 4
-        for (int i = r; i < (int)(S::kTile / 16); i += 128) {
-          uint4 v = *reinterpret_cast<uint4*>(vt + i * 16);
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-          bool any = false;
+            for (int w = 0; w < 4; ++w)
+              mx[w] = max3(mx[w], __uint_as_float(s[i + 2 * w]), __uint_as_float(s[i + 2 * w + 1]));
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        // P of all keys into ph, returns their sum
+        auto exponentials = [&]() {
+          // a row that has seen nothing yet has m = -inf: its P is 0
+          const float mc = m == -INFINITY ? 0.0f : m * c;
+          const uint64_t c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) any |= ((w[u] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-          if (any) {
+          for (int i = 0; i < kKeys; i += 2) {
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2));
+            const float e0 = ex2(x.x), e1 = ex2(x.y);
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(e0, e1));
+            const __half2 h = __floats2half2_rn(e0, e1);
+            ph[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          const float2 st = unpack2(add2(sum[0], sum[1]));
+          return st.x + st.y;
+        };
+        load();
+        const float mt = maximum();
+        float sum;
+        if (j == 0) {
+          m = mt;
+          sum = exponentials();
+        } else {
+          // with the maximum of the steps before, which need not wait for this step's
+          sum = exponentials();
+          if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
+            // some row's maximum has grown too far: this warp's rows of O and l go
+            // over to the new maxima (O has every product before: S_t(j) came after)
+            const float mn = fmaxf(m, mt);
+            const float a = m == mn ? 1.0f : ex2((m - mn) * c);
+            m = mn;
+            l *= a;
+#pragma unroll 1
+            for (int i = 0; i < HD; i += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + i, o);
+              tmem_wait_ld();
+              tmem_pin<16>(o);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              if ((w[u] & 0x7c00u) == 0x7c00u) w[u] &= 0xffff0000u;
-              if ((w[u] & 0x7c000000u) == 0x7c000000u) w[u] &= 0x0000ffffu;
+              for (int w = 0; w < 16; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * a);
+              tmem_st16(o_at + i, o);
             }
-            *reinterpret_cast<uint4*>(vt + i * 16) = v;
-            // rows of the tile are 128 bytes in each half
-            if ((ka + j) * kKeys + (int)((i * 16) % S::kHalf) / 128 < tl.sq.ctx) fixed = true;
+            load();
+            sum = exponentials();
           }
         }
-        if (fixed) sh.bad_v = 1;
-        fence_proxy_async();
+        l += sum;
+#pragma unroll
+        for (int i = 0; i < kKeys / 2; i += 16) tmem_st16(s_at + i, ph + i);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.p_ready[t]);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&sh.p_ready[t]);
-    }
-    if (ok && n > 0) ok = warp_wait(&sh.o_done[t], (n - 1) & 1, p.c.err, DERR_FULL_WAIT);
-    tc_fence_after();
-    asm volatile("bar.sync 1, 256;" ::: "memory");  // bad_v of both tiles; the tiles' space is free
-    const bool bad = sh.bad_v;
-    const int head = g * G + r % G;
-    const float il = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays
-    uint16_t* orow = p.o + (int64_t)(tl.sq.first + row) * p.o_stride + head * HD;
-    float* jrow = reinterpret_cast<float*>(tiles) + (size_t)(t * 128 + r) * S::kPad;
+      if (r == 0 && n == 0 && nk > 0) mbar_arrive(&sh.q_free);
+      if (ok && n > 0) ok = warp_wait(&sh.o_done[t], ends & 1, p.c.err, DERR_FULL_WAIT);
+      ends += n > 0;
+      tc_fence_after();
+      if (frees && nk > 0) mbar_arrive(&sh.kv_empty[stage(base + 2 * nk - 1)]);
+      // for the join, which reuses the tiles' space, the other row tile has to be done too
+      if (SPLIT && ok && u.n[1 - t] > 0) ok = warp_wait(&sh.o_done[1 - t], 0, p.c.err, DERR_FULL_WAIT);
+      const bool bad = sh.bad_v[i & 7] == i;
+      const int jm = min(u.jm[0], u.jm[1]);
+      const int head = u.g * G + r % G;
+      const float il = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays
+      uint16_t* orow = p.o + (int64_t)(u.tl.sq.first + row) * p.o_stride + head * HD;
+      const bool wide = ((uintptr_t)p.o & 31) == 0 && (p.o_stride & 15) == 0;
+      float* jrow = reinterpret_cast<float*>(tiles) + (size_t)(t * 128 + r) * S::kPad;
 #pragma unroll 1
-    for (int i = 0; i < HD; i += 32) {
-      uint32_t o[32];
-      tmem_ld32(o_at + i, o);
-      tmem_wait_ld();
-      tmem_pin<32>(o);
-      if (n == 0) {
+      for (int i = 0; i < HD; i += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_at + i, o);
+        tmem_wait_ld();
+        tmem_pin<32>(o);
+        if (n == 0) {
 #pragma unroll
-        for (int u = 0; u < 32; ++u) o[u] = 0;
-      }
-      if (bad) {  // the values taken out above, for the rows that see them
-        const int end = min(pos, kb * kKeys - 1);
-        for (int tok = max(min(jm[0], jm[1]), ka) * kKeys; tok <= end; ++tok) {
-          bool bok;
-          const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, tl.s, tok, nullptr, &bok);
-          const uint16_t* v = p.c.v + (((size_t)b * p.c.n_kv_heads + g) * 16 + (tok & 15)) * HD + i;
+          for (int w = 0; w < 32; ++w) o[w] = 0;
+        }
+        if (bad) {  // the values taken out above, for the rows that see them
+          const int end = min(pos, u.kb * kKeys - 1);
+          for (int tok = max(jm, u.ka) * kKeys; tok <= end; ++tok) {
+            bool bok;
+            const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, u.tl.s, tok, nullptr, &bok);
+            const uint16_t* v = p.c.v + (((size_t)b * p.c.n_kv_heads + u.g) * 16 + (tok & 15)) * HD + i;
 #pragma unroll
-          for (int u = 0; u < 32; ++u)
-            if ((v[u] & 0x7c00u) == 0x7c00u)
-              o[u] = __float_as_uint(__uint_as_float(o[u]) + __half2float(__ushort_as_half(v[u])));
+            for (int w = 0; w < 32; ++w)
+              if ((v[w] & 0x7c00u) == 0x7c00u)
+                o[w] = __float_as_uint(__uint_as_float(o[w]) + __half2float(__ushort_as_half(v[w])));
+          }
+        }
+        if (SPLIT) {
+#pragma unroll
+          for (int w = 0; w < 32; w += 4)
+            *reinterpret_cast<uint4*>(jrow + i + w) = make_uint4(o[w], o[w + 1], o[w + 2], o[w + 3]);
+        } else if (valid && ok) {
+          uint32_t h[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const __half2 x = __floats2half2_rn(__uint_as_float(o[2 * k]) * il, __uint_as_float(o[2 * k + 1]) * il);
+            h[k] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          if (wide) {  // whole 32-byte sectors
+            st_global_v8(orow + i, h);
+            st_global_v8(orow + i + 16, h + 8);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(orow + i + 8 * k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+          }
         }
       }
       if (SPLIT) {
-#pragma unroll
-        for (int u = 0; u < 32; u += 4)
-          *reinterpret_cast<uint4*>(jrow + i + u) = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
-      } else if (valid) {
-#pragma unroll
-        for (int u = 0; u < 32; u += 8) {
-          uint32_t h[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const __half2 x = __floats2half2_rn(__uint_as_float(o[u + 2 * w]) * il, __uint_as_float(o[u + 2 * w + 1]) * il);
-            h[w] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          *reinterpret_cast<uint4*>(orow + i + u) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+        sh.m[t * 128 + r] = m;
+        sh.l[t * 128 + r] = l;
+      } else if (valid && ok && p.lse) {
+        p.lse[(size_t)head * p.total_q + u.tl.sq.first + row] = log_sum(m, l, ex);
       }
+      tc_fence_before();
+      base += 2 * nk;
     }
-    if (SPLIT) {
-      sh.m[t * 128 + r] = m;
-      sh.l[t * 128 + r] = l;
-    } else if (valid && p.lse) {
-      p.lse[(size_t)head * p.total_q + tl.sq.first + row] = log_sum(m, l, ex);
-    }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == 9) {
@@ -388,31 +530,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (SPLIT) {
     // rank r joins rows r, r + nsplit, ...: every rank's (O, m, l) in rank order
     cg::cluster_group cl = cg::this_cluster();
+    const Unit u = sh.unit[0];
     cl.sync();
     constexpr int L = HD / 4;  // threads per row
-    const int rows = min(kRows, (tl.sq.n - tl.i0) * G);
+    const int rows = u.tl.s < 0 ? 0 : min(kRows, (u.tl.sq.n - u.tl.i0) * G);
     if (tid < 256) {
       for (int r = split + nsplit * (tid / L); r < rows; r += nsplit * (256 / L)) {
-        const int row = tl.i0 + r / G, head = g * G + r % G, col = (tid % L) * 4;
+        const int row = u.tl.i0 + r / G, head = u.g * G + r % G, col = (tid % L) * 4;
         float M = -INFINITY;
         float mr[kMaxCluster], lr[kMaxCluster];
         float4 x[kMaxCluster];
 #pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) {
-          if (k >= nsplit) break;
-          const Shared* o = cl.map_shared_rank(&sh, k);
+        for (int k = 0; k < kMaxCluster; ++k) {  // all reads first
+          const int from = k < nsplit ? k : split;
+          const Shared* o = cl.map_shared_rank(&sh, from);
           mr[k] = o->m[r];
           lr[k] = o->l[r];
-          x[k] = *reinterpret_cast<const float4*>(cl.map_shared_rank(reinterpret_cast<float*>(tiles), k) +
+          x[k] = *reinterpret_cast<const float4*>(cl.map_shared_rank(reinterpret_cast<float*>(tiles), from) +
                                                   (size_t)r * S::kPad + col);
-          M = fmaxf(M, mr[k]);
         }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < nsplit) M = fmaxf(M, mr[k]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.0f;
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {
-          if (k >= nsplit) break;
-          if (lr[k] == 0.0f) continue;  // saw nothing (NaN is not 0)
+          if (k >= nsplit || lr[k] == 0.0f) continue;  // saw nothing (NaN is not 0)
           const float a = mr[k] == M ? 1.0f : ex2((mr[k] - M) * c);
           l += a * lr[k];
           o.x += a * x[k].x;
@@ -422,10 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float il = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
         const __half2 h0 = __floats2half2_rn(o.x * il, o.y * il), h1 = __floats2half2_rn(o.z * il, o.w * il);
-        *reinterpret_cast<uint2*>(p.o + (int64_t)(tl.sq.first + row) * p.o_stride + head * HD + col) =
+        *reinterpret_cast<uint2*>(p.o + (int64_t)(u.tl.sq.first + row) * p.o_stride + head * HD + col) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
         if (col == 0 && p.lse)
-          p.lse[(size_t)head * p.total_q + tl.sq.first + row] = log_sum(M, l, ex);
+          p.lse[(size_t)head * p.total_q + u.tl.sq.first + row] = log_sum(M, l, ex);
       }
     }
     cl.sync();  // nobody leaves while its memory is read
@@ -443,6 +587,12 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
     e = cudaFuncSetAttribute(k_prompt_attention<HD, G, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k_prompt_attention<HD, G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    // the exchange of registers above counts on the launch's share
+    for (const void* f : {(const void*)k_prompt_attention<HD, G, false>, (const void*)k_prompt_attention<HD, G, true>}) {
+      cudaFuncAttributes at;
+      if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, f);
+      if (e == cudaSuccess && at.numRegs != kRegs) e = cudaErrorInvalidConfiguration;
+    }
     if (e != cudaSuccess) return e;
     if (dev < 64) prepared.fetch_or(1ull << dev, std::memory_order_release);
   }
@@ -463,7 +613,7 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   int split = 1;
   while (split < kMaxCluster && units * split * 2 <= sms && split * 2 * kKeys < p.c.max_ctx) split *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * split));
+  cfg.gridDim = dim3((unsigned)(split > 1 ? units * split : units < sms ? units : sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
