@@ -76,6 +76,11 @@ EE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int 
       : "memory");
 }
 
+// The same box to L2 only.
+EE_DEV void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
 // D[tmem] (+)= A * B, both operands in shared memory.
 EE_DEV void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),

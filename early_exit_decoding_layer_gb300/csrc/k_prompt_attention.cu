@@ -420,35 +420,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         load();
         const float mt = maximum();
-        float sum;
         if (j == 0) {
           m = mt;
-          sum = exponentials();
-        } else {
-          // with the maximum of the steps before, which need not wait for this step's
-          sum = exponentials();
-          if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
-            // some row's maximum has grown too far: this warp's rows of O and l go
-            // over to the new maxima (O has every product before: S_t(j) came after)
-            const float mn = fmaxf(m, mt);
-            const float a = m == mn ? 1.0f : ex2((m - mn) * c);
-            m = mn;
-            l *= a;
+        } else if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
+          // some row's maximum has grown too far: this warp's rows of O and l go over to
+          // the new maxima (O has every product before: S_t(j) came after)
+          const float mn = fmaxf(m, mt);
+          const float a = m == mn ? 1.0f : ex2((m - mn) * c);
+          m = mn;
+          l *= a;
 #pragma unroll 1
-            for (int i = 0; i < HD; i += 16) {
-              uint32_t o[16];
-              tmem_ld16(o_at + i, o);
-              tmem_wait_ld();
-              tmem_pin<16>(o);
+          for (int i = 0; i < HD; i += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_at + i, o);
+            tmem_wait_ld();
+            tmem_pin<16>(o);
 #pragma unroll
-              for (int w = 0; w < 16; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * a);
-              tmem_st16(o_at + i, o);
-            }
-            load();
-            sum = exponentials();
+            for (int w = 0; w < 16; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * a);
+            tmem_st16(o_at + i, o);
           }
         }
-        l += sum;
+        l += exponentials();
 #pragma unroll
         for (int i = 0; i < kKeys / 2; i += 16) tmem_st16(s_at + i, ph + i);
         tmem_wait_st();

@@ -8,7 +8,8 @@
 // A CTA owns 128 keys of one kv head; K stays in shared memory, tiles of 128
 // query rows (128 / G positions x G heads) stream through a ring by TMA from
 // the first row that sees a key:
-//   warp 9 (one thread)  S_b = K Q_j^T into four tensor-memory buffers in turn
+//   warps 9, 10          (a thread of each) S_b = K Q_j^T, j even and odd, into two
+//                        tensor-memory buffers each
 //   warps 0-3, 4-7       tiles 0, 2, .. and 1, 3, ..: exp2(c S - lse log2 e), summed
 //   warp 8               TMA
 // Each tile's 128 terms are summed in four chains, and the tiles' sums with
@@ -33,7 +34,7 @@ namespace {
 
 constexpr int kKeys = 128;
 constexpr int kCols = 128;     // query rows per tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kBuf = 4;        // S buffers of 128 tensor-memory columns
 constexpr int kMaxCluster = 8;
 
@@ -127,22 +128,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_bounded(&sh.q_full[i % S::NST], (i / S::NST) & 1, p.c.err, DERR_DRAIN_WAIT);
     }
     __syncwarp();
-  } else if (warp == 9) {
-    if (lane == 0 && nq > 0) {
+  } else if (warp >= 9) {
+    // an issuing thread per warpgroup: what one does between two products falls into
+    // the other's
+    const int t = warp - 9;
+    if (lane == 0 && t < nq) {
       constexpr uint32_t idesc = instr_desc(0, kCols, 128);
+      const uint64_t a = smem_desc_sw128(k_s);
       bool ok = mbar_wait_bounded(&sh.k_full, 0, p.c.err, DERR_FULL_WAIT);
-      for (int j = 0; j < nq && ok; ++j) {
+      for (int j = t; j < nq && ok; j += 2) {
         const int st = j % S::NST, b = j % kBuf;
+        const uint64_t q = smem_desc_sw128(q_s + st * S::kTile);
         ok = mbar_wait_bounded(&sh.q_full[st], (j / S::NST) & 1, p.c.err, DERR_FULL_WAIT);
         if (ok && j >= kBuf) ok = mbar_wait_bounded(&sh.s_free[b], (j / kBuf - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * S::kHalf + (kk & 3) * 32;
-          mma_f16(tmem + b * kCols, smem_desc_sw128(k_s + o), smem_desc_sw128(q_s + st * S::kTile + o), idesc, kk > 0);
+          const uint32_t o = ((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4;
+          mma_f16(tmem + b * kCols, a + o, q + o, idesc, kk > 0);
         }
-        mma_commit(&sh.q_empty[st]);
         mma_commit(&sh.s_full[b]);
       }
     }
@@ -173,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // still meets the warpgroup's barriers
       if (ok) ok = warp_wait(&sh.s_full[b], (j / kBuf) & 1, p.c.err, DERR_FULL_WAIT);
       tc_fence_after();
+      if (r == 0) mbar_arrive(&sh.q_empty[j % S::NST]);  // the product has read its queries
       uint32_t v[kCols];
 #pragma unroll
       for (int i = 0; i < 4; ++i) tmem_ld32(tmem + b * kCols + lane_base + 32 * i, v + 32 * i);
