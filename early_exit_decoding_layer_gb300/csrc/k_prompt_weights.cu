@@ -8,10 +8,10 @@
 // A CTA owns 128 keys of one kv head; K stays in shared memory, tiles of 128
 // query rows (128 / G positions x G heads) stream through a ring by TMA from
 // the first row that sees a key:
-//   warps 9, 10          (a thread of each) S_b = K Q_j^T, j even and odd, into two
-//                        tensor-memory buffers each
-//   warps 0-3, 4-7       tiles 0, 2, .. and 1, 3, ..: exp2(c S - lse log2 e), summed
-//   warp 8               TMA
+//   warpgroups 0-3       tiles 0, 4, .. and 1, 5, .. and so on: exp2(c S - f lse),
+//                        summed; each has an S buffer in tensor memory
+//   warp 16              TMA
+//   warps 17, 18         (a thread of each) S = K Q_j^T, j even and odd
 // Each tile's 128 terms are summed in four chains, and the tiles' sums with
 // compensation, so that the error does not grow with the prompt's length.
 //
@@ -34,8 +34,10 @@ namespace {
 
 constexpr int kKeys = 128;
 constexpr int kCols = 128;     // query rows per tile
-constexpr int kThreads = 352;
-constexpr int kBuf = 4;        // S buffers of 128 tensor-memory columns
+constexpr int kGroups = 4;     // softmax warpgroups, each with an S buffer of 128 tensor-memory columns
+constexpr int kThreads = kGroups * 128 + 96;  // and TMA and two MMA warps
+constexpr int kBuf = kGroups;
+constexpr int kTma = kGroups * 4;  // warp; the two behind it issue the MMAs
 constexpr int kMaxCluster = 8;
 
 template <int HD>
@@ -54,8 +56,8 @@ struct Maps {
 struct Shared {
   uint64_t k_full, q_full[8], q_empty[8], s_full[kBuf], s_free[kBuf];
   uint32_t tmem;
-  alignas(16) float lse[2][2][kCols];  // by warpgroup, two tiles
-  float sum[2][kKeys];
+  alignas(16) float lse[kGroups][2][kCols];  // by warpgroup, two tiles
+  float sum[kGroups][kKeys];
 };
 
 template <int HD, int G, bool SPLIT>
@@ -93,14 +95,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(&sh.tmem, kBuf * kCols);
+  if (warp == kTma + 1) tmem_alloc(&sh.tmem, kBuf * kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t k_s = smem_addr(tiles), q_s = k_s + S::kTile;
 
-  if (warp == 8) {
+  if (warp == kTma) {
     const int here = min(8, ((sq.ctx + 15) >> 4) - key0 / 16);  // blocks of the key tile
     const int b8 = lane & 7, half = lane >> 3;
     if (nq > 0) {
@@ -128,10 +130,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_bounded(&sh.q_full[i % S::NST], (i / S::NST) & 1, p.c.err, DERR_DRAIN_WAIT);
     }
     __syncwarp();
-  } else if (warp >= 9) {
+  } else if (warp > kTma) {
     // an issuing thread per warpgroup: what one does between two products falls into
     // the other's
-    const int t = warp - 9;
+    const int t = warp - kTma - 1;
     if (lane == 0 && t < nq) {
       constexpr uint32_t idesc = instr_desc(0, kCols, 128);
       const uint64_t a = smem_desc_sw128(k_s);
@@ -156,51 +158,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, r = tid & 127;
     const int key = key0 + r;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    // column r of a tile: its lse in the exponent's unit, +inf for a row that adds nothing
+    // column r of a tile: its lse, -inf for a row of nobody.  What becomes of it waits
+    // until the next tile, when the load is over.
     auto load_lse = [&](int j) {
-      if (j >= nq) return 0.0f;
-      const int row = tile_row(j) + r / G;
-      if (row >= sq.n) return INFINITY;
-      const float v = p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row];
-      return v == -INFINITY ? INFINITY : fmaf(v, ex.f_hi, v * ex.f_lo);
+      const int row = j < nq ? tile_row(j) + r / G : sq.n;
+      return row < sq.n ? p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row] : -INFINITY;
     };
     float sum = 0.0f, comp = 0.0f, next = load_lse(t);
     const uint64_t c2 = pack2(ex.c, ex.c);
     bool ok = true;
-    for (int j = t; j < nq; j += 2) {
-      float* ls = sh.lse[t][(j >> 1) & 1];
-      ls[r] = -next;
-      next = load_lse(j + 2);
+    for (int j = t; j < nq; j += kGroups) {
+      float* ls = sh.lse[t][(j / kGroups) & 1];
+      // in the exponent's unit; a row that adds nothing has an lse of +inf here
+      ls[r] = next == -INFINITY ? -INFINITY : -fmaf(next, ex.f_hi, next * ex.f_lo);
+      next = load_lse(j + kGroups);
       // the other buffer was read two tiles ago, before the barrier of the last one
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
       const int b = j % kBuf, row0 = tile_row(j);
+      const uint32_t at = tmem + b * kCols + lane_base;
       // after a wait that gave up the loop goes on without waiting: every thread
       // still meets the warpgroup's barriers
       if (ok) ok = warp_wait(&sh.s_full[b], (j / kBuf) & 1, p.c.err, DERR_FULL_WAIT);
       tc_fence_after();
       if (r == 0) mbar_arrive(&sh.q_empty[j % S::NST]);  // the product has read its queries
-      uint32_t v[kCols];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(tmem + b * kCols + lane_base + 32 * i, v + 32 * i);
-      tmem_wait_ld();
-      tmem_pin<kCols>(v);
-      tc_fence_before();
-      mbar_arrive(&sh.s_free[b]);
-      if (off + row0 < key0 + kKeys - 1 || row0 + kPos > sq.n) {
-        // rows before the key, rows of no one: -inf
-        const int lo = (key - off - row0) * G, hi = (sq.n - row0) * G;
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (i < lo || i >= hi) v[i] = 0xff800000u;
-      }
+      const bool masked = off + row0 < key0 + kKeys - 1 || row0 + kPos > sq.n;
+      const int lo = (key - off - row0) * G, hi = (sq.n - row0) * G;
+      // 32 columns at a time, the next ones on their way
+      uint32_t v[2][32];
       uint64_t acc[2] = {0, 0};
+      tmem_ld32(at, v[0]);
 #pragma unroll
-      for (int i = 0; i < kCols; i += 4) {
-        const float4 l4 = *reinterpret_cast<const float4*>(ls + i);
-        const float2 x = unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, pack2(l4.x, l4.y)));
-        const float2 y = unpack2(fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), c2, pack2(l4.z, l4.w)));
-        acc[0] = add2(acc[0], pack2(ex2(x.x), ex2(x.y)));
-        acc[1] = add2(acc[1], pack2(ex2(y.x), ex2(y.y)));
+      for (int k = 0; k < kCols / 32; ++k) {
+        tmem_wait_ld();
+        tmem_pin<32>(v[k & 1]);
+        if (k < kCols / 32 - 1) {
+          tmem_ld32(at + 32 * (k + 1), v[(k + 1) & 1]);
+        } else {
+          tc_fence_before();
+          mbar_arrive(&sh.s_free[b]);
+        }
+        uint32_t* x = v[k & 1];
+        if (masked) {  // rows before the key, rows of no one: -inf
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * k + i < lo || 32 * k + i >= hi) x[i] = 0xff800000u;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * k + i);
+          const float2 y = unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, pack2(l4.x, l4.y)));
+          const float2 z = unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), c2, pack2(l4.z, l4.w)));
+          acc[0] = add2(acc[0], pack2(ex2(y.x), ex2(y.y)));
+          acc[1] = add2(acc[1], pack2(ex2(z.x), ex2(z.y)));
+        }
       }
       const float2 a = unpack2(add2(acc[0], acc[1]));
       const float y = (a.x + a.y) - comp, u = sum + y;  // compensated sum over the tiles
@@ -211,17 +221,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kTma + 1) {
     tc_fence_after();
     tmem_free(tmem, kBuf * kCols);
   }
   if (SPLIT) cg::this_cluster().sync();
   if (split == 0 && tid < kKeys && key0 + tid < sq.ctx) {
-    float w = sh.sum[0][tid] + sh.sum[1][tid];
+    float w = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kGroups; ++t) w += sh.sum[t][tid];
     if (SPLIT)
       for (int k = 1; k < nsplit; ++k) {
         const Shared* o = cg::this_cluster().map_shared_rank(&sh, k);
-        w += o->sum[0][tid] + o->sum[1][tid];
+        for (int t = 0; t < kGroups; ++t) w += o->sum[t][tid];
       }
     bool ok;
     const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, s, key0 + tid, nullptr, &ok);
