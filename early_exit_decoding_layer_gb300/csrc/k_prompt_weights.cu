@@ -5,10 +5,11 @@
 // The keys are the MMA's rows: S = K_tile Q^T gives every thread of a softmax
 // warpgroup one key and, along its registers, 128 query rows, so the sum over
 // the rows stays in the thread: no shuffles, and no second pass over anything.
-// A CTA owns 128 keys of one kv head; K stays in shared memory, tiles of 128
-// query rows (128 / G positions x G heads) stream through a ring by TMA from
-// the first row that sees a key:
-//   warpgroups 0-3       tiles 0, 4, .. and 1, 5, .. and so on: exp2(c S - f lse),
+// A CTA owns 256 keys of one kv head, two M = 128 tiles that stay in shared memory
+// (one read of the queries serves both: with one tile their way from L2 was the
+// limit); tiles of 128 query rows (128 / G positions x G heads) stream through
+// a ring by TMA from the first row that sees a key:
+//   warpgroup t          key tile t & 1, query tiles of parity t / 2: exp2(c S - f lse),
 //                        summed; each has an S buffer in tensor memory
 //   warp 16              TMA
 //   warps 17, 18         (a thread of each) S = K Q_j^T, j even and odd
@@ -32,13 +33,13 @@ namespace cg = cooperative_groups;
 namespace ee {
 namespace {
 
-constexpr int kKeys = 128;
+constexpr int kKeys = 256;     // per CTA: two MMA tiles of 128
 constexpr int kCols = 128;     // query rows per tile
 constexpr int kGroups = 4;     // softmax warpgroups, each with an S buffer of 128 tensor-memory columns
 constexpr int kThreads = kGroups * 128 + 96;  // and TMA and two MMA warps
 constexpr int kBuf = kGroups;
 constexpr int kTma = kGroups * 4;  // warp; the two behind it issue the MMAs
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
 
 template <int HD>
 struct Shape {
@@ -46,7 +47,7 @@ struct Shape {
   static constexpr uint32_t kTile = 128 * HD * 2;
   static constexpr uint32_t kHalf = 128 * 128;
   static constexpr int NST = HD == 128 ? 4 : 6;
-  static constexpr size_t kSmem = 1024 + (1 + NST) * (size_t)kTile;
+  static constexpr size_t kSmem = 1024 + (2 + NST) * (size_t)kTile;
 };
 
 struct Maps {
@@ -57,7 +58,7 @@ struct Shared {
   uint64_t k_full, q_full[8], q_empty[8], s_full[kBuf], s_free[kBuf];
   uint32_t tmem;
   alignas(16) float lse[kGroups][2][kCols];  // by warpgroup, two tiles
-  float sum[kGroups][kKeys];
+  float sum[kGroups][128];
 };
 
 template <int HD, int G, bool SPLIT>
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int off = sq.ctx - sq.n;
   const int first = max(0, key0 - off);  // first row that sees a key of the tile
   if (key0 >= sq.ctx || first >= sq.n) return;  // the whole cluster
+  const int nh = key0 + 128 < sq.ctx ? 2 : 1;  // key tiles
   const int all = (sq.n - first + kPos - 1) / kPos;
   const int nq = (all - split + nsplit - 1) / nsplit;  // this CTA's: tiles split, split + nsplit, ...
   auto tile_row = [&](int j) { return first + (split + j * nsplit) * kPos; };
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.k_full, 1);
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_empty[i], nh);  // a warpgroup per key tile
     }
     for (int i = 0; i < kBuf; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -100,21 +102,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const uint32_t k_s = smem_addr(tiles), q_s = k_s + S::kTile;
+  const uint32_t k_s = smem_addr(tiles), q_s = k_s + 2 * S::kTile;
 
   if (warp == kTma) {
-    const int here = min(8, ((sq.ctx + 15) >> 4) - key0 / 16);  // blocks of the key tile
-    const int b8 = lane & 7, half = lane >> 3;
+    const int here = min(kKeys / 16, ((sq.ctx + 15) >> 4) - key0 / 16);  // blocks of the keys
+    const int b16 = lane & 15, half = lane >> 4;
     if (nq > 0) {
-      int id = b8 < here ? p.c.table[(int64_t)s * p.c.table_stride + key0 / 16 + b8] : 0;
+      int id = b16 < here ? p.c.table[(int64_t)s * p.c.table_stride + key0 / 16 + b16] : 0;
       if (id < 0 || id >= p.c.n_blocks) {
         report(p.c.err, EE_DERR_BLOCK);
         id = 0;
       }
       if (lane == 0) mbar_arrive_expect_tx(&sh.k_full, (uint32_t)here * 16 * HD * 2);
       __syncwarp();
-      if (half < S::H && b8 < here)
-        tma_load_2d(k_s + half * S::kHalf + b8 * 2048, &maps.k, half * 64, (id * p.c.n_kv_heads + g) * 16, &sh.k_full);
+      if (half < S::H && b16 < here)
+        tma_load_2d(k_s + (b16 >> 3) * S::kTile + half * S::kHalf + (b16 & 7) * 2048, &maps.k, half * 64,
+                    (id * p.c.n_kv_heads + g) * 16, &sh.k_full);
     }
     if (lane == 0) {
       int issued = 0;
@@ -136,27 +139,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp - kTma - 1;
     if (lane == 0 && t < nq) {
       constexpr uint32_t idesc = instr_desc(0, kCols, 128);
-      const uint64_t a = smem_desc_sw128(k_s);
       bool ok = mbar_wait_bounded(&sh.k_full, 0, p.c.err, DERR_FULL_WAIT);
       for (int j = t; j < nq && ok; j += 2) {
-        const int st = j % S::NST, b = j % kBuf;
+        const int st = j % S::NST;
         const uint64_t q = smem_desc_sw128(q_s + st * S::kTile);
         ok = mbar_wait_bounded(&sh.q_full[st], (j / S::NST) & 1, p.c.err, DERR_FULL_WAIT);
-        if (ok && j >= kBuf) ok = mbar_wait_bounded(&sh.s_free[b], (j / kBuf - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
-        if (!ok) break;
-        tc_fence_after();
+#pragma unroll 1
+        for (int h = 0; h < nh && ok; ++h) {
+          const int b = 2 * t + h;
+          const uint64_t a = smem_desc_sw128(k_s + h * S::kTile);
+          if (j >= 2) ok = mbar_wait_bounded(&sh.s_free[b], (j / 2 - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4;
-          mma_f16(tmem + b * kCols, a + o, q + o, idesc, kk > 0);
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t o = ((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4;
+            mma_f16(tmem + b * kCols, a + o, q + o, idesc, kk > 0);
+          }
+          mma_commit(&sh.s_full[b]);
         }
-        mma_commit(&sh.s_full[b]);
       }
     }
     __syncwarp();
   } else {
-    const int t = warp >> 2, r = tid & 127;
-    const int key = key0 + r;
+    // warpgroup t: key tile t & 1, query tiles j = t / 2, t / 2 + 2, ..
+    const int t = warp >> 2, r = tid & 127, keys = key0 + (t & 1) * 128, key = keys + r;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // column r of a tile: its lse, -inf for a row of nobody.  What becomes of it waits
     // until the next tile, when the load is over.
@@ -164,24 +171,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = j < nq ? tile_row(j) + r / G : sq.n;
       return row < sq.n ? p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row] : -INFINITY;
     };
-    float sum = 0.0f, comp = 0.0f, next = load_lse(t);
+    float sum = 0.0f, comp = 0.0f, next = load_lse(t >> 1);
     const uint64_t c2 = pack2(ex.c, ex.c);
     bool ok = true;
-    for (int j = t; j < nq; j += kGroups) {
-      float* ls = sh.lse[t][(j / kGroups) & 1];
+    for (int j = t >> 1; j < ((t & 1) < nh ? nq : 0); j += 2) {
+      float* ls = sh.lse[t][(j >> 1) & 1];
       // in the exponent's unit; a row that adds nothing has an lse of +inf here
       ls[r] = next == -INFINITY ? -INFINITY : -fmaf(next, ex.f_hi, next * ex.f_lo);
-      next = load_lse(j + kGroups);
+      next = load_lse(j + 2);
       // the other buffer was read two tiles ago, before the barrier of the last one
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
-      const int b = j % kBuf, row0 = tile_row(j);
-      const uint32_t at = tmem + b * kCols + lane_base;
+      const int row0 = tile_row(j);
+      const uint32_t at = tmem + t * kCols + lane_base;
       // after a wait that gave up the loop goes on without waiting: every thread
       // still meets the warpgroup's barriers
-      if (ok) ok = warp_wait(&sh.s_full[b], (j / kBuf) & 1, p.c.err, DERR_FULL_WAIT);
+      if (ok) ok = warp_wait(&sh.s_full[t], (j >> 1) & 1, p.c.err, DERR_FULL_WAIT);
       tc_fence_after();
       if (r == 0) mbar_arrive(&sh.q_empty[j % S::NST]);  // the product has read its queries
-      const bool masked = off + row0 < key0 + kKeys - 1 || row0 + kPos > sq.n;
+      const bool masked = off + row0 < keys + 127 || row0 + kPos > sq.n;
       const int lo = (key - off - row0) * G, hi = (sq.n - row0) * G;
       // 32 columns at a time, the next ones on their way
       uint32_t v[2][32];
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(at + 32 * (k + 1), v[(k + 1) & 1]);
         } else {
           tc_fence_before();
-          mbar_arrive(&sh.s_free[b]);
+          mbar_arrive(&sh.s_free[t]);
         }
         uint32_t* x = v[k & 1];
         if (masked) {  // rows before the key, rows of no one: -inf
@@ -227,13 +234,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (SPLIT) cg::this_cluster().sync();
   if (split == 0 && tid < kKeys && key0 + tid < sq.ctx) {
-    float w = 0.0f;
-#pragma unroll
-    for (int t = 0; t < kGroups; ++t) w += sh.sum[t][tid];
+    const int h = tid >> 7, r = tid & 127;
+    float w = sh.sum[h][r] + sh.sum[2 + h][r];
     if (SPLIT)
       for (int k = 1; k < nsplit; ++k) {
         const Shared* o = cg::this_cluster().map_shared_rank(&sh, k);
-        for (int t = 0; t < kGroups; ++t) w += o->sum[t][tid];
+        w += o->sum[h][r] + o->sum[2 + h][r];
       }
     bool ok;
     const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, s, key0 + tid, nullptr, &ok);
