@@ -45,7 +45,7 @@ namespace {
 constexpr int kRows = 256;     // rows of S per CTA: two tiles of 128
 constexpr int kKeys = 128;     // keys per step
 constexpr int kThreads = 384;  // two softmax warpgroups, TMA, MMA, landed tiles, units
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 6;
 constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsSingle = 88;  // at launch, and after
 static_assert(256 * kRegsSoftmax + 128 * kRegsSingle <= kThreads * kRegs, "no more than the launch has");
 
@@ -85,7 +85,8 @@ struct Shared {
   Unit unit[kUnits];
   uint32_t tmem;
   int bad_v[8];  // [unit & 7]: the last unit in which a non-finite V value was replaced
-  float m[kRows], l[kRows];
+  float m[kRows], l[kRows];              // split: of the CTA's share of the keys
+  float fac[kMaxCluster][kRows / 2];     // split: what a rank's O counts in a row
 };
 
 template <int G>
@@ -520,49 +521,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_free(tmem, 512);
   }
   if (SPLIT) {
-    // rank r joins rows r, r + nsplit, ...: every rank's (O, m, l) in rank order
+    // Rank r joins rows r, r + nsplit, ...: every rank's (O, m, l) in rank order.
+    // First what each rank's O counts in a row (eight lanes per row, one per
+    // rank), then the rows.  Short code rather than many reads in flight: it runs
+    // once, and fetching it counts.
     cg::cluster_group cl = cg::this_cluster();
     const Unit u = sh.unit[0];
     cl.sync();
-    constexpr int L = HD / 4;  // threads per row
     const int rows = u.tl.s < 0 ? 0 : min(kRows, (u.tl.sq.n - u.tl.i0) * G);
-    if (tid < 256) {
-      for (int r = split + nsplit * (tid / L); r < rows; r += nsplit * (256 / L)) {
-        const int row = u.tl.i0 + r / G, head = u.g * G + r % G, col = (tid % L) * 4;
-        float M = -INFINITY;
-        float mr[kMaxCluster], lr[kMaxCluster];
-        float4 x[kMaxCluster];
+    const int mine = rows > split ? (rows - split + nsplit - 1) / nsplit : 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < mine; i0 += kThreads / 8) {
+      const int i = i0 + tid / 8, k = tid & 7, r = split + nsplit * i;
+      const Shared* o = cl.map_shared_rank(&sh, k < nsplit ? k : split);
+      const bool has = k < nsplit && i < mine;
+      const float m = has ? o->m[r] : -INFINITY, l = has ? o->l[r] : 0.0f;
+      float M = m;
 #pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) {  // all reads first
-          const int from = k < nsplit ? k : split;
-          const Shared* o = cl.map_shared_rank(&sh, from);
-          mr[k] = o->m[r];
-          lr[k] = o->l[r];
-          x[k] = *reinterpret_cast<const float4*>(cl.map_shared_rank(reinterpret_cast<float*>(tiles), from) +
-                                                  (size_t)r * S::kPad + col);
-        }
+      for (int x = 1; x < 8; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+      const float a = l == 0.0f ? 0.0f : m == M ? 1.0f : ex2((m - M) * c);  // 0: saw nothing
+      float sum = a == 0.0f ? 0.0f : a * l;
 #pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k)
-          if (k < nsplit) M = fmaxf(M, mr[k]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) {
-          if (k >= nsplit || lr[k] == 0.0f) continue;  // saw nothing (NaN is not 0)
-          const float a = mr[k] == M ? 1.0f : ex2((mr[k] - M) * c);
-          l += a * lr[k];
-          o.x += a * x[k].x;
-          o.y += a * x[k].y;
-          o.z += a * x[k].z;
-          o.w += a * x[k].w;
-        }
-        const float il = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        const __half2 h0 = __floats2half2_rn(o.x * il, o.y * il), h1 = __floats2half2_rn(o.z * il, o.w * il);
-        *reinterpret_cast<uint2*>(p.o + (int64_t)(u.tl.sq.first + row) * p.o_stride + head * HD + col) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-        if (col == 0 && p.lse)
-          p.lse[(size_t)head * p.total_q + u.tl.sq.first + row] = log_sum(M, l, ex);
+      for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      if (has) {
+        sh.fac[k][i] = a * (sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum));  // NaN stays
+        const int row = u.tl.i0 + r / G, head = u.g * G + r % G;
+        if (k == 0 && p.lse) p.lse[(size_t)head * p.total_q + u.tl.sq.first + row] = log_sum(M, sum, ex);
       }
+    }
+    __syncthreads();
+    constexpr int L = HD / 4;  // threads per row
+    const int col = (tid % L) * 4;
+#pragma unroll 1
+    for (int i = tid / L; i < mine; i += kThreads / L) {
+      const int r = split + nsplit * i;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int k0 = 0; k0 < nsplit; k0 += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[k] = *reinterpret_cast<const float4*>(
+              cl.map_shared_rank(reinterpret_cast<float*>(tiles), k0 + k < nsplit ? k0 + k : split) + (size_t)r * S::kPad + col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = k0 + k < nsplit ? sh.fac[k0 + k][i] : 0.0f;
+          if (a != 0.0f) {  // (NaN is not 0)
+            o.x = fmaf(a, x[k].x, o.x);
+            o.y = fmaf(a, x[k].y, o.y);
+            o.z = fmaf(a, x[k].z, o.z);
+            o.w = fmaf(a, x[k].w, o.w);
+          }
+        }
+      }
+      const int row = u.tl.i0 + r / G, head = u.g * G + r % G;
+      const __half2 h0 = __floats2half2_rn(o.x, o.y), h1 = __floats2half2_rn(o.z, o.w);
+      *reinterpret_cast<uint2*>(p.o + (int64_t)(u.tl.sq.first + row) * p.o_stride + head * HD + col) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
     }
     cl.sync();  // nobody leaves while its memory is read
   }
@@ -600,10 +615,16 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
       !encode_tensor_map(&maps.v, false, 2, p.c.v, cd, cs, cb))
     return cudaErrorInvalidValue;
   const Exponent ex = make_exponent(HD);
-  // at most this many tiles: each sequence may leave one unfilled
+  // At most this many tiles: each sequence may leave one unfilled.  Where they leave
+  // SMs idle the keys are split, as long as a CTA keeps some 2.5 key tiles: 60 rows
+  // of 64/8 heads, hd 128, behind 16000 tokens take 236 us on 16 CTAs and 53 us on
+  // 96; 512 rows of 32/8 heads, hd 64, 12.3 us unsplit and 14.5 us split in two.
+  // Clusters of 8 were slower than of 6 (84 us): a GPC's 18 or 19 free SMs hold
+  // three of 6 and only two of 8.
   const int64_t units = ((int64_t)p.total_q * G / kRows + p.n_seqs) * p.c.n_kv_heads;
+  const int steps = (p.c.max_ctx + kKeys - 1) / kKeys;
   int split = 1;
-  while (split < kMaxCluster && units * split * 2 <= sms && split * 2 * kKeys < p.c.max_ctx) split *= 2;
+  while (split < kMaxCluster && units * (split + 1) <= sms && 2 * steps >= 5 * (split + 1)) ++split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? units * split : units < sms ? units : sms));
   cfg.blockDim = dim3(kThreads);
