@@ -7,13 +7,14 @@
 //
 // Selection: the keep - recent heaviest of the tokens before the last `recent`, by
 // radix selection on the weights' bits, mapped to unsigned integers of the same
-// order: four passes of 8 bits, each a histogram, its suffix sums and the digit in
-// which the wanted rank falls.  Accumulated weights are of similar size, so
-// most keys fall into a few bins of the first pass: the histogram has a
-// copy per lane, which keeps the lanes of a warp off each other's counters.
-// Tokens above the resulting key stay, and of those equal to it the first ones, so
-// ties go to the lower index.  Each thread owns a run of tokens, so two prefix sums
-// (equal ones, then kept ones) give every kept token its slot.
+// order: up to four passes of 8 bits, each a histogram, its sums from the top and
+// the digit in which the wanted rank falls; a digit whose keys all stay ends
+// it.  Accumulated weights are of similar size, so most keys fall into a few bins
+// of the first pass: the histogram has eight copies, which leaves four lanes of a
+// warp on a counter (32 copies: clearing and adding them cost 2600 cycles a
+// pass, with 500 keys as with 16000).  Tokens above the resulting key stay, and of
+// those equal to it the first ones, so ties go to the lower index.  Warps own runs
+// of tokens and walk them twice in order, counting and then placing by ballots.
 //
 // Moving: a kept token's slot is never above the token, so rows move in place in
 // ascending order: the cluster reads a chunk of rows into registers (K, V and
@@ -43,40 +44,17 @@ EE_DEV uint32_t order_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum of one value per thread.
-EE_DEV int block_scan(int v, int* warps) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // warps is free again
-  if (lane == 31) warps[warp] = x;
-  __syncthreads();
-  int base = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (w < warp) base += warps[w];
-  return base + x - v;
-}
+constexpr int kCopies = 8;
 
-// A thread's run of tokens lies apart from the next one's by an odd number of words.
-EE_DEV int pad(int t) { return t + (t >> 5); }
-
-// Shared memory: keys (padded), then the histograms; the kept tokens (16 bits: below
-// 2^14) over the histograms; the two block tables.
+// Shared memory: keys, histograms, kept tokens (16 bits: below 2^14), block tables.
 struct Layout {
-  int keys, kept, src, dst, bytes;
+  int hist, kept, src, dst, bytes;
 };
 __host__ __device__ inline Layout layout(int max_ctx, int keep) {
   Layout l;
-  l.keys = 0;
-  l.kept = (max_ctx + max_ctx / 32 + 1) * 4;
-  l.kept = (l.kept + 15) / 16 * 16;
-  const int hist = 256 * 32 * 4, list = (max_ctx * 2 + 15) / 16 * 16;
-  l.src = l.kept + (hist > list ? hist : list);
+  l.hist = (max_ctx + 3) / 4 * 16;
+  l.kept = l.hist + 256 * kCopies * 4;
+  l.src = l.kept + (max_ctx * 2 + 15) / 16 * 16;
   l.dst = l.src + (max_ctx + 15) / 16 * 4;
   l.bytes = l.dst + (keep + 15) / 16 * 4;
   return l;
@@ -85,15 +63,14 @@ __host__ __device__ inline Layout layout(int max_ctx, int keep) {
 template <int HD>
 __global__ void __launch_bounds__(kThreads) k_evict(const EvictParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int warps[kWarps], s_digit, s_above;
-  __shared__ int bins[256];
+  __shared__ int sums[2][kWarps], s_digit, s_above, s_count;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, hkv = p.c.n_kv_heads;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hkv = p.c.n_kv_heads;
   const int unit = blockIdx.x / C, g = unit % hkv, s = unit / hkv;
   const Layout lay = layout(p.c.max_ctx, p.keep);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + lay.keys);
-  int* hist = reinterpret_cast<int*>(smem + lay.kept);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+  int* hist = reinterpret_cast<int*>(smem + lay.hist);
   uint16_t* kept = reinterpret_cast<uint16_t*>(smem + lay.kept);
   int* src = reinterpret_cast<int*>(smem + lay.src);
   int* dst = reinterpret_cast<int*>(smem + lay.dst);
@@ -122,79 +99,102 @@ __global__ void __launch_bounds__(kThreads) k_evict(const EvictParams p) {
   } else {
     const int m = n - p.recent;          // candidates
     const int need = p.keep - p.recent;  // of them, fewer than m
-    for (int i = tid; i < (m + 3) / 4; i += kThreads) {
-      const float4 w = *reinterpret_cast<const float4*>(p.c.weights + ((size_t)max(src[i >> 2], 0) * hkv + g) * 16 + (i & 3) * 4);
-      const float f[4] = {w.x, w.y, w.z, w.w};
+    constexpr int kFly = 4;  // quarter blocks in flight per thread
+    for (int i0 = tid; i0 < (m + 3) / 4; i0 += kFly * kThreads) {
+      float4 w[kFly];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (4 * i + u < m) keys[pad(4 * i + u)] = order_key(f[u]);
+      for (int u = 0; u < kFly; ++u) {
+        const int i = min(i0 + u * kThreads, (m + 3) / 4 - 1);
+        w[u] = *reinterpret_cast<const float4*>(p.c.weights + ((size_t)max(src[i >> 2], 0) * hkv + g) * 16 + (i & 3) * 4);
+      }
+#pragma unroll
+      for (int u = 0; u < kFly; ++u)
+        if (i0 + u * kThreads < (m + 3) / 4)
+          reinterpret_cast<uint4*>(keys)[i0 + u * kThreads] =
+              make_uint4(order_key(w[u].x), order_key(w[u].y), order_key(w[u].z), order_key(w[u].w));
     }
     uint32_t prefix = 0, mask = 0;
     int rest = need;  // rank of the key looked for, among those that match the prefix
+#pragma unroll 1
     for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-      for (int i = tid; i < 256 * 32; i += kThreads) hist[i] = 0;
+      for (int i = tid; i < 256 * kCopies; i += kThreads) hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int t = tid; t < m; t += kThreads) {
-        const uint32_t k = keys[pad(t)];
-        if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255) * 32 + lane], 1);
+        const uint32_t k = keys[t];
+        if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255) * kCopies + lane % kCopies], 1);
       }
       __syncthreads();
-      for (int b = tid >> 5; b < 256; b += kWarps) {
-        const int c = (int)__reduce_add_sync(0xffffffffu, (unsigned)hist[b * 32 + lane]);
-        if (lane == 0) bins[b] = c;
-      }
-      __syncthreads();
-      if (tid < 32) {  // lane l: bins 8 l .. 8 l + 7, from the top
-        int c[8], sum = 0;
+      // thread tid < 256: bin 255 - tid, and the keys in the bins above it
+      int c = 0, above = 0;
+      if (tid < 256) {
 #pragma unroll
-        for (int u = 7; u >= 0; --u) sum += (c[u] = bins[(31 - lane) * 8 + u]);
-        int above = sum;
+        for (int u = 0; u < kCopies; ++u) c += hist[(255 - tid) * kCopies + u];
+        above = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, above, o);
           if (lane >= o) above += y;
         }
-        above -= sum;  // keys in higher lanes' bins
-        if (above < rest && above + sum >= rest) {
-#pragma unroll
-          for (int u = 7; u >= 0; --u) {
-            if (above < rest && above + c[u] >= rest) {
-              s_digit = (31 - lane) * 8 + u;
-              s_above = above;
-            }
-            above += c[u];
-          }
+        if (lane == 31) sums[0][warp] = above;
+        above -= c;
+      }
+      __syncthreads();
+      if (tid < 256) {
+        for (int w = 0; w < warp; ++w) above += sums[0][w];
+        if (above < rest && above + c >= rest) {
+          s_digit = 255 - tid;
+          s_above = above;
+          s_count = c;
         }
       }
       __syncthreads();
       rest -= s_above;
       prefix |= (uint32_t)s_digit << shift;
       mask |= 255u << shift;
+      if (s_count == rest) break;  // the same for all: every key with this prefix stays
     }
-    // tokens [t0, t1) are this thread's; keys above prefix stay, and the first `rest`
-    // equal ones, and the recent tokens
-    const int each = (n + kThreads - 1) / kThreads;
-    const int t0 = min(n, tid * each), t1 = min(n, t0 + each);
+    __syncthreads();
+    // Masked keys above prefix stay, the first `rest` equal ones, and the recent
+    // tokens.  Warp w owns tokens [t0, t1).
+    const int each = (n + kThreads - 1) / kThreads * 32;
+    const int t0 = min(n, warp * each), t1 = min(n, t0 + each);
+    auto look = [&](int t, bool* eq) {
+      const bool cand = t < m && need > 0;
+      const uint32_t k = cand ? keys[t] & mask : 0u;
+      *eq = cand && k == prefix;
+      return (t >= m && t < t1) || (cand && t < t1 && k > prefix);
+    };
     int equal = 0, more = 0;
-    for (int t = t0; t < t1; ++t) {
-      const bool cand = t < m && need > 0;
-      const uint32_t k = cand ? keys[pad(t)] : 0u;
-      equal += cand && k == prefix;
-      more += t >= m || (cand && k > prefix);
+#pragma unroll 4
+    for (int t = t0 + lane; t < t1 + lane; t += 32) {
+      bool eq;
+      more += look(t, &eq);
+      equal += eq && t < t1;
     }
-    const int before = block_scan(equal, warps);
-    const int ties = max(0, min(equal, rest - before));
-    int slot = block_scan(more + ties, warps);
-    int taken = 0;
-    for (int t = t0; t < t1; ++t) {  // the histograms are no longer read
-      const bool cand = t < m && need > 0;
-      const uint32_t k = cand ? keys[pad(t)] : 0u;
-      bool stay = t >= m || (cand && k > prefix);
-      if (cand && k == prefix && taken < ties) {
-        stay = true;
-        ++taken;
-      }
-      if (stay) kept[slot++] = (uint16_t)t;
+    more = __reduce_add_sync(0xffffffffu, (unsigned)more);
+    equal = __reduce_add_sync(0xffffffffu, (unsigned)equal);
+    if (lane == 0) {
+      sums[0][warp] = more;
+      sums[1][warp] = equal;
+    }
+    __syncthreads();
+    int slot = 0, seen = 0;  // kept tokens and equal keys before
+    for (int w = 0; w < warp; ++w) {
+      slot += sums[0][w];
+      seen += sums[1][w];
+    }
+    slot += min(seen, rest);
+#pragma unroll 4
+    for (int t = t0 + lane; t < t1 + lane; t += 32) {
+      bool eq;
+      const bool above = look(t, &eq);
+      const unsigned below = (1u << lane) - 1u, e = __ballot_sync(0xffffffffu, eq && t < t1);
+      const bool stay = above || (eq && t < t1 && seen + __popc(e & below) < rest);
+      const unsigned k = __ballot_sync(0xffffffffu, stay);
+      if (stay) kept[slot + __popc(k & below)] = (uint16_t)t;
+      slot += __popc(k);
+      seen += __popc(e);
     }
   }
   __syncthreads();
@@ -254,7 +254,7 @@ cudaError_t launch_t(const EvictParams& p, cudaStream_t st) {
   // CTAs for every SM, as long as each has a chunk of rows to move
   const int units = p.batch * p.c.n_kv_heads, chunk = kThreads * kPieces / (HD / 8);
   int C = 1;
-  while (C < kMaxCluster && units * C < sms && C * chunk < p.keep) C *= 2;
+  while (C < kMaxCluster && units * C < 2 * sms && C * chunk < p.keep) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * C));
   cfg.blockDim = dim3(kThreads);
