@@ -40,10 +40,10 @@ EE_DEV uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t half) {
 }
 
 // Instruction descriptor, kind::f16: fp32 accumulators, A and B of type
-// `ab` (0 = f16, 1 = bf16), A K-major, B K-major (or MN-major), N and M given.
-constexpr uint32_t instr_desc(uint32_t ab, int n, int m, bool b_mn = false) {
-  return (1u << 4) | (ab << 7) | (ab << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
-         ((uint32_t)(m >> 4) << 24);
+// `ab` (0 = f16, 1 = bf16), each K-major or MN-major, N and M given.
+constexpr uint32_t instr_desc(uint32_t ab, int n, int m, bool b_mn = false, bool a_mn = false) {
+  return (1u << 4) | (ab << 7) | (ab << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Byte offset of 16-byte chunk j (8 elements) of row r in a 128B-swizzled tile.
