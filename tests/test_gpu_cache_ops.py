@@ -442,3 +442,122 @@ def test_refusals_on_device_tensors():
     with pytest.raises(ee.EEError):
         ee.prompt_weights(d["q"], d["k"], d["table"], d["cu"], d["ctx"], torch.zeros(4, 19, device="cuda"), w, *c.shape)
     torch.cuda.synchronize()
+
+
+def far_caches(h, shift):
+    """h's caches with every block `shift` ids further on, in arrays whose elements before
+    are left as the allocator gave them."""
+    out = []
+    for a in (h.k, h.v, h.w):
+        x = torch.empty((shift + h.n_blocks,) + a.shape[1:], dtype=torch.from_numpy(a).dtype, device="cuda")
+        x[shift:] = dev(a)
+        out.append(x)
+    return out + [dev(np.where(h.table == 0x7FFFFFF0, h.table, h.table + shift))]
+
+
+def test_offsets_beyond_32_bits():
+    """Blocks whose elements lie behind 2^32 bytes and 2^31 elements: the same bits as
+    near the start."""
+    hq, hkv, hd = 32, 8, 128
+    c = Prompt(71, hq, hkv, hd, [70, 9], [70, 200])
+    shift = (1 << 31) // (hkv * 16 * hd) + 1000
+    near = [dev(c.h.k), dev(c.h.v), dev(c.h.w), dev(c.h.table)]
+    far = far_caches(c.h, shift)
+    d = c.args()
+    qd = dev(c.h.rng.standard_normal((2, hq * hd)).astype(np.float32))
+    got = []
+    for k, v, w, table in (near, far):
+        o, lse = ee.prompt_attention(d["q"], k, v, table, d["cu"], d["ctx"], *c.shape)
+        ee.prompt_weights(d["q"], k, table, d["cu"], d["ctx"], lse, w, *c.shape)
+        x = ee.attention_weights(qd, k, v, table, d["ctx"] - 1, w, *c.shape)
+        kept, new = ee.evict(k, v, w, table, d["ctx"], 33, 5, c.max_ctx)
+        n = c.h.n_blocks
+        got.append([o, lse, x, kept, new, k[-n:].clone(), v[-n:].clone(), w[-n:].clone()])
+    for a, b in zip(*got):
+        assert torch.equal(torch.nan_to_num(a.float(), nan=777.0), torch.nan_to_num(b.float(), nan=777.0))
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(8, 2, 128), (8, 1, 64)])
+def test_longest_prompt(hq, hkv, hd):
+    """16384 tokens: rows from all over against 64 bits, every row's weights adding up to
+    one, the last row as a decode step, and the eviction to half."""
+    n, T = 16384, torch.float64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    nb = n // 16
+    k, v = (torch.randn(nb, hkv, 16, hd, generator=g, device="cuda").half() for _ in range(2))
+    table = torch.randperm(nb, generator=g, device="cuda").to(torch.int32).view(1, nb)
+    q = torch.randn(n, hq * hd, generator=g, device="cuda").half()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    w = torch.zeros(nb, hkv, 16, device="cuda")
+    shape = (hq, hkv, hd, n)
+    o, lse = ee.prompt_attention(q, k, v, table, i32(0, n), i32(n), *shape)
+    ee.prompt_weights(q, k, table, i32(0, n), i32(n), lse, w, *shape)
+    flat = lambda x: x[table[0].long()].transpose(1, 2).reshape(n, hkv, -1)  # noqa: E731
+    K, V, W = flat(k).to(T), flat(v).to(T), flat(w)[..., 0]
+    G = hq // hkv
+    for r in (0, 1, 63, 64, 127, 128, 255, 4095, 8191, 16320, 16383):
+        z = torch.einsum("hgd,thd->hgt", q[r].view(hkv, G, hd).to(T), K[: r + 1]) / math.sqrt(hd)
+        p = torch.softmax(z, -1)
+        ref = torch.einsum("hgt,thd->hgd", p, V[: r + 1])
+        mag = torch.einsum("hgt,thd->hgd", p, V[: r + 1].abs())
+        # as in prompt_reference: fp16 probabilities (2^-11 relative, 2^-25 absolute) and result
+        bound = (2.0 ** -11 + 1e-4) * mag + 2.0 ** -25 * V[: r + 1].abs().sum(0)[:, None] + 2.0 ** -11 * ref.abs() * 1.001 + 2.0 ** -25
+        assert torch.all((o[r].view(hkv, G, hd).to(T) - ref).abs() <= bound), r
+        # sums of r + 1 terms in fp32 and a score's error, as in prompt_reference
+        assert torch.all((lse[:, r].view(hkv, G).to(T) - torch.logsumexp(z, -1)).abs() <= 1e-4), r
+    # every row gives one weight per head of the group: n G per kv head, each to 2e-5
+    assert torch.all((W.to(T).sum(0) - n * G).abs() <= 2e-5 * n * G)
+    # the last tokens' weights come from few rows
+    rows = slice(n - 40, n)
+    z = torch.einsum("rhgd,thd->hgrt", q[rows].view(40, hkv, G, hd).to(T), K) / math.sqrt(hd)
+    seen = torch.arange(n, device="cuda") <= torch.arange(n - 40, n, device="cuda")[:, None]
+    p = torch.softmax(z.masked_fill(~seen, -math.inf), -1).sum((1, 2))
+    assert torch.allclose(W[n - 40:].T.to(T), p[:, n - 40:], rtol=1e-4, atol=0)
+    # decode: the same row from fp32 queries
+    before = w.clone()
+    x = ee.attention_weights(q[-1:].float(), k, v, table, i32(n - 1), w, *shape)
+    assert torch.all((x[0].view(hkv, G, hd).to(T) - ref).abs() <= 1e-4 * mag)
+    add = (flat(w)[..., 0] - flat(before)[..., 0]).to(T)
+    assert torch.all((add.sum(0) - G).abs() <= 1e-2)   # added to sums of up to 10^4, rounded there
+    # eviction: ties at the border go to the lower index
+    flat_w = torch.round(flat(w)[..., 0] * 4) / 4
+    wq = torch.empty_like(w)
+    wq[table[0].long()] = flat_w.view(nb, 16, hkv).transpose(1, 2)
+    kept, new = ee.evict(k, v, wq, table, i32(n), n // 2, 100, n)
+    want = oracle.evict_indices(flat_w.cpu().numpy(), n // 2, 100)
+    assert new.item() == n // 2 and np.array_equal(kept[0].cpu().numpy(), want)
+    moved = flat(k)[: n // 2].cpu()
+    for h in range(hkv):
+        assert torch.equal(moved[:, h], K[want[h], h].half().cpu())
+
+
+def test_full_batch():
+    """64 sequences, some without rows or tokens: every operator, each sequence as its own."""
+    hq, hkv, hd = 8, 2, 64
+    rng = np.random.default_rng(81)
+    ctxs = [int(x) for x in rng.integers(0, 90, 64)]
+    ctxs[3] = ctxs[63] = 0
+    rows = [int(min(c, x)) for c, x in zip(ctxs, rng.integers(0, 60, 64))]
+    c = Prompt(82, hq, hkv, hd, rows, ctxs, lead=1, tail=1)
+    d = c.args()
+    w = torch.zeros(c.h.n_blocks, hkv, 16, device="cuda")
+    o, lse = ee.prompt_attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+    ee.prompt_weights(d["q"], d["k"], d["table"], d["cu"], d["ctx"], lse, w, *c.shape)
+    qd = c.h.rng.standard_normal((64, hq, hd)).astype(np.float32)
+    x = ee.attention_weights(dev(qd.reshape(64, -1)), d["k"], d["v"], d["table"], d["ctx"] - 1, w, *c.shape)
+    kept, new = ee.evict(d["k"], d["v"], dev(c.h.w), d["table"], d["ctx"], 20, 4, c.max_ctx)
+    o, lse, x, w, kept, new = (t.cpu().numpy() for t in (o, lse, x, w, kept, new))
+    o = o.astype(np.float64).reshape(c.T, hq, hd)
+    for s in range(64):
+        r = c.seq_rows(s)
+        ro, rl, rw, bo, bl, bw = prompt_reference(c.h, s, c.q[r])
+        assert np.all(np.abs(o[r] - ro) <= bo) and np.all(np.abs(lse[:, r] - rl) <= bl), s
+        n = min(ctxs[s], 20)
+        assert new[s] == n
+        if ctxs[s] == 0:
+            assert np.all(x[s] == 0)
+            continue
+        xo, _, p = oracle.prompt_attention(qd[s][None].astype(np.float64), c.h.K[s].astype(np.float64), c.h.V[s].astype(np.float64))
+        assert np.allclose(x[s].reshape(hq, hd), xo[0], rtol=1e-4, atol=1e-5), s
+        assert np.all(np.abs(c.h.gather(w, s) - rw - p) <= bw + 1e-4 * (rw + p) + 1e-6), s
+        assert np.array_equal(kept[s, :, :n], oracle.evict_indices(c.h.W[s], 20, 4)), s
