@@ -151,6 +151,15 @@ EE_DEV void tmem_pin(uint32_t* v) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
+// mbar_wait_bounded with the wait itself out of line: where a thread's loop has to
+// stay in the instruction cache, only the first look is part of it.
+static __device__ __noinline__ bool bar_wait_slow(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code) {
+  return mbar_wait_bounded(bar, parity, err, code);
+}
+EE_DEV bool bar_wait(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code) {
+  return mbar_try_wait(bar, parity) || bar_wait_slow(bar, parity, err, code);
+}
+
 // mbar_wait_bounded by a whole warp with one answer for all its lanes, which stay
 // together for the aligned instructions that follow.
 EE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code) {

@@ -49,15 +49,17 @@ constexpr int kMaxCluster = 6;
 constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsSingle = 88;  // at launch, and after
 static_assert(256 * kRegsSoftmax + 128 * kRegsSingle <= kThreads * kRegs, "no more than the launch has");
 
-template <int HD>
+template <int HD, bool SPLIT>
 struct Shape {
   static constexpr int H = HD / 64;                       // 64-column halves
   static constexpr uint32_t kTile = 128 * HD * 2;         // a Q, K or V tile
   static constexpr uint32_t kHalf = 128 * 128;            // one 64-column half of it
-  static constexpr int NST = HD == 128 ? 4 : 6;           // ring tiles
+  // ring tiles: as many as fit.  A tile's way from L2 takes about as long as a step, and
+  // with four of them one step in two waited for V some 500 cycles.
+  static constexpr int NST = HD == 128 ? (SPLIT ? 4 : 5) : 9;
   static constexpr size_t kSmem = 1024 + (2 + NST) * (size_t)kTile;
   static constexpr int kPad = HD + 4;                     // floats per joined row
-  static_assert((size_t)kRows * kPad * 4 <= (2 + NST) * (size_t)kTile, "the join reuses the tiles' space");
+  static_assert(!SPLIT || (size_t)kRows * kPad * 4 <= (2 + NST) * (size_t)kTile, "the join reuses the tiles' space");
 };
 
 struct Maps {
@@ -79,14 +81,23 @@ struct Unit {
 
 constexpr int kUnits = 4;  // units known ahead
 
-struct Shared {
-  uint64_t q_full, q_free, kv_full[8], kv_empty[8], s_full[2], p_ready[2], o_done[2];
+// What only the join needs.
+template <bool SPLIT>
+struct Join {};
+template <>
+struct Join<true> {
+  float m[kRows], l[kRows];           // of the CTA's share of the keys
+  float fac[kMaxCluster][kRows / 2];  // what a rank's O counts in a row
+};
+
+template <int HD, bool SPLIT>
+struct Shared : Join<SPLIT> {
+  static constexpr int NST = Shape<HD, SPLIT>::NST;
+  uint64_t q_full, q_free, kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
   uint64_t unit_full[kUnits], unit_free[kUnits];
   Unit unit[kUnits];
   uint32_t tmem;
   int bad_v[8];  // [unit & 7]: the last unit in which a non-finite V value was replaced
-  float m[kRows], l[kRows];              // split: of the CTA's share of the keys
-  float fac[kMaxCluster][kRows / 2];     // split: what a rank's O counts in a row
 };
 
 template <int G>
@@ -114,11 +125,11 @@ EE_DEV Unit make_unit(const PromptTile& tl, int g, int split, int nsplit) {
 template <int HD, int G, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_prompt_attention(const PromptParams p, const __grid_constant__ Maps maps, const Exponent ex) {
-  using S = Shape<HD>;
+  using S = Shape<HD, SPLIT>;
   constexpr int kPos = kRows / G;  // positions per CTA
   const float c = ex.c;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Shared sh;
+  __shared__ Shared<HD, SPLIT> sh;
   uint8_t* tiles = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nsplit = SPLIT ? (int)cg::this_cluster().num_blocks() : 1;
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (SPLIT) {
+      if constexpr (SPLIT) {
         sh.m[t * 128 + r] = m;
         sh.l[t * 128 + r] = l;
       } else if (valid && ok && p.lse) {
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_free(tmem, 512);
   }
-  if (SPLIT) {
+  if constexpr (SPLIT) {
     // Rank r joins rows r, r + nsplit, ...: every rank's (O, m, l) in rank order.
     // First what each rank's O counts in a row (eight lanes per row, one per
     // rank), then the rows.  Short code rather than many reads in flight: it runs
@@ -533,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int i0 = 0; i0 < mine; i0 += kThreads / 8) {
       const int i = i0 + tid / 8, k = tid & 7, r = split + nsplit * i;
-      const Shared* o = cl.map_shared_rank(&sh, k < nsplit ? k : split);
+      const Shared<HD, SPLIT>* o = cl.map_shared_rank(&sh, k < nsplit ? k : split);
       const bool has = k < nsplit && i < mine;
       const float m = has ? o->m[r] : -INFINITY, l = has ? o->l[r] : 0.0f;
       float M = m;
@@ -585,15 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int HD, int G>
 cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
-  using S = Shape<HD>;
   static std::atomic<uint64_t> prepared{0};  // a bit per device
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_prompt_attention<HD, G, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    e = cudaFuncSetAttribute(k_prompt_attention<HD, G, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<HD, false>::kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_prompt_attention<HD, G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      e = cudaFuncSetAttribute(k_prompt_attention<HD, G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Shape<HD, true>::kSmem);
     // the exchange of registers above counts on the launch's share
     for (const void* f : {(const void*)k_prompt_attention<HD, G, false>, (const void*)k_prompt_attention<HD, G, true>}) {
       cudaFuncAttributes at;
@@ -628,7 +640,7 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? units * split : units < sms ? units : sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.dynamicSmemBytes = split > 1 ? Shape<HD, true>::kSmem : Shape<HD, false>::kSmem;
   cfg.stream = st;
   if (split == 1) return cudaLaunchKernelEx(&cfg, k_prompt_attention<HD, G, false>, p, maps, ex);
   cudaLaunchAttribute attr[1];
