@@ -483,18 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 32; ++w) o[w] = 0;
         }
-        if (bad) {  // the values taken out above, for the rows that see them
-          const int end = min(pos, u.kb * kKeys - 1);
-          for (int tok = max(jm, u.ka) * kKeys; tok <= end; ++tok) {
-            bool bok;
-            const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, u.tl.s, tok, nullptr, &bok);
-            const uint16_t* v = p.c.v + (((size_t)b * p.c.n_kv_heads + u.g) * 16 + (tok & 15)) * HD + i;
-#pragma unroll
-            for (int w = 0; w < 32; ++w)
-              if ((v[w] & 0x7c00u) == 0x7c00u)
-                o[w] = __float_as_uint(__uint_as_float(o[w]) + __half2float(__ushort_as_half(v[w])));
-          }
-        }
         if (SPLIT) {
 #pragma unroll
           for (int w = 0; w < 32; w += 4)
@@ -513,6 +501,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               *reinterpret_cast<uint4*>(orow + i + 8 * k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+          }
+        }
+      }
+      if (bad && ok) {
+        // the values taken out of V, for the rows that see them (rare: kept out of the
+        // loop above, whose code is fetched anew for every unit)
+        const int end = min(pos, u.kb * kKeys - 1);
+#pragma unroll 1
+        for (int tok = max(jm, u.ka) * kKeys; tok <= end; ++tok) {
+          bool bok;
+          const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, u.tl.s, tok, nullptr, &bok);
+          const uint16_t* v = p.c.v + (((size_t)b * p.c.n_kv_heads + u.g) * 16 + (tok & 15)) * HD;
+#pragma unroll 1
+          for (int w = 0; w < HD; ++w) {
+            if ((v[w] & 0x7c00u) != 0x7c00u) continue;
+            const float x = __half2float(__ushort_as_half(v[w]));
+            if (SPLIT) jrow[w] += x;
+            else orow[w] = float_to_half_bits(__half2float(__ushort_as_half(orow[w])) + x);
           }
         }
       }
