@@ -471,40 +471,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = u.g * G + r % G;
       const float il = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays
       uint16_t* orow = p.o + (int64_t)(u.tl.sq.first + row) * p.o_stride + head * HD;
-      const bool wide = ((uintptr_t)p.o & 31) == 0 && (p.o_stride & 15) == 0;
       float* jrow = reinterpret_cast<float*>(tiles) + (size_t)(t * 128 + r) * S::kPad;
+      if (SPLIT) {
 #pragma unroll 1
-      for (int i = 0; i < HD; i += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_at + i, o);
-        tmem_wait_ld();
-        tmem_pin<32>(o);
-        if (n == 0) {
-#pragma unroll
-          for (int w = 0; w < 32; ++w) o[w] = 0;
-        }
-        if (SPLIT) {
+        for (int i = 0; i < HD; i += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_at + i, o);
+          tmem_wait_ld();
+          tmem_pin<32>(o);
 #pragma unroll
           for (int w = 0; w < 32; w += 4)
-            *reinterpret_cast<uint4*>(jrow + i + w) = make_uint4(o[w], o[w + 1], o[w + 2], o[w + 3]);
-        } else if (valid && ok) {
-          uint32_t h[16];
+            *reinterpret_cast<uint4*>(jrow + i + w) =
+                n > 0 ? make_uint4(o[w], o[w + 1], o[w + 2], o[w + 3]) : make_uint4(0, 0, 0, 0);
+        }
+      } else if (ok) {
+        // Four lanes share a row here, eight rows of 64 columns per store: a thread that
+        // stores its own row touches 32 lines per instruction, and that took 4000
+        // cycles a unit.  Lane a has columns 8 k + 2 a, + 1 of every k; the four
+        // exchange pairs of k so that lane a gets all of k = 2 a and 2 a + 1.
+        const bool wide = ((uintptr_t)p.o & 31) == 0 && (p.o_stride & 15) == 0;
+        const int a = lane & 3;
+#pragma unroll 1
+        for (int i = 0; i < 2 * S::H; ++i) {
+          const int hf = i & 1, cb = i >> 1;  // 16 rows, 64 columns
+          uint32_t v[32];
+          tmem_ld_rows16(o_at + ((uint32_t)(16 * hf) << 16) + 64 * cb, v);
+          tmem_wait_ld();
+          tmem_pin<32>(v);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const __half2 x = __floats2half2_rn(__uint_as_float(o[2 * k]) * il, __uint_as_float(o[2 * k + 1]) * il);
-            h[k] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          if (wide) {  // whole 32-byte sectors
-            st_global_v8(orow + i, h);
-            st_global_v8(orow + i + 16, h + 8);
-          } else {
+          for (int q = 0; q < 2; ++q) {
+            const int rl = 16 * hf + 8 * q + (lane >> 2), rr = (warp & 3) * 32 + rl;  // row of the warp, of the tile
+            const float f = __shfl_sync(0xffffffffu, il, rl);
+            uint32_t e[4][2];  // [k / 2][k % 2]
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(orow + i + 8 * k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+            for (int k = 0; k < 8; ++k) {
+              const __half2 x = __floats2half2_rn(__uint_as_float(v[4 * k + 2 * q]) * f, __uint_as_float(v[4 * k + 2 * q + 1]) * f);
+              e[k >> 1][k & 1] = n > 0 ? *reinterpret_cast<const uint32_t*>(&x) : 0;
+            }
+#pragma unroll
+            for (int x = 1; x < 4; x <<= 1)
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                if (b & x) continue;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, (a & x) ? e[b][w] : e[b | x][w], x);
+                  if (a & x) e[b][w] = got;
+                  else e[b | x][w] = got;
+                }
+              }
+            const uint32_t h[8] = {e[0][0], e[1][0], e[2][0], e[3][0], e[0][1], e[1][1], e[2][1], e[3][1]};
+            const int at = u.tl.i0 + t * (kPos / 2) + rr / G;
+            uint16_t* to = p.o + (int64_t)(u.tl.sq.first + at) * p.o_stride + (u.g * G + rr % G) * HD + cb * 64 + a * 16;
+            if (at < u.tl.sq.n) {
+              if (wide) {
+                st_global_v8(to, h);
+              } else {
+                *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(to + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+              }
+            }
           }
         }
+        __syncwarp();
       }
-      if (bad && ok) {
+      if (bad && ok && valid) {
         // the values taken out of V, for the rows that see them (rare: kept out of the
         // loop above, whose code is fetched anew for every unit)
         const int end = min(pos, u.kb * kKeys - 1);
