@@ -407,44 +407,72 @@ cudaError_t launch_t(const DecodeWeightsParams& p, cudaStream_t st) {
   using Lay = Layout<HD>;
   constexpr int kMaxSmem = 226 * 1024 - (int)sizeof(Shared<HD, G>);  // of 227 KB, in whole KB
   static std::atomic<uint64_t> prepared{0};  // a bit per device
+  static std::atomic<int> held[64][kMaxCluster + 1];  // CTAs that the device holds, one per SM, by cluster size
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (!(prepared.load(std::memory_order_acquire) >> dev & 1)) {
     e = cudaFuncSetAttribute(k_attention_weights<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k_attention_weights<HD, G>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int k = 1; k <= kMaxCluster && e == cudaSuccess; ++k) {
+      int clusters = 0;
+      attr[0].val.clusterDim.x = k;
+      cfg.gridDim = dim3(1024 * k);
+      cfg.dynamicSmemBytes = kMaxSmem;
+      e = cudaOccupancyMaxActiveClusters(&clusters, k_attention_weights<HD, G>, &cfg);
+      held[dev][k].store(clusters * k, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) return e;
-    if (dev < 64) prepared.fetch_or(1ull << dev, std::memory_order_release);
+    prepared.fetch_or(1ull << dev, std::memory_order_release);
   }
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   Maps maps;
   const uint64_t cd[2] = {(uint64_t)HD, (uint64_t)p.c.n_blocks * p.c.n_kv_heads * 16}, cs[1] = {(uint64_t)HD * 2};
   const uint32_t cb[2] = {64, 16};
   if (!encode_tensor_map(&maps.k, false, 2, p.c.k, cd, cs, cb) || !encode_tensor_map(&maps.v, false, 2, p.c.v, cd, cs, cb))
     return cudaErrorInvalidValue;
-  // Two CTAs per SM, shares of at least a tile, and the scores of a share in shared
-  // memory.  One sequence of 2113 tokens, 8 kv heads of 128: 36 us with C = 1, 13.8
-  // with 4, 10.5 with 8, 8.7 with 12, 10.2 with 16 (too large for some GPCs);
-  // 32 sequences of up to 2176: 46 us with one, 39 with two, 55 with four.
+  // The cluster size with the least estimated time: waves of CTAs, each a fixed part
+  // (launch, first loads, join: 6 us measured) and its tiles, which take 0.87 us one
+  // after another, or their bytes at an SM's share of the memory's bandwidth (44.5
+  // GB/s) times the CTAs that share it.  The scores of a share decide how many CTAs
+  // an SM holds, the GPCs (of up to 20 SMs) how many clusters fit.  Estimated
+  // and measured, 8 kv heads of 128, 4 query heads each: 32 sequences of 2176
+  // tokens with C = 1, 2, 3, 4: 71, 62, 66, 74 and 78, 59, 68, 74 us; 8 of 16384
+  // with 2, 4, 6, 9, 12: 117, 123, 130, 156, 106 and 126, 129, 136, 163, 102; one of
+  // 2113 with 1, 4, 8, 12: 36, 14, 10, 9 and 36, 13.8, 10.5, 8.7.
   const int units = p.batch * p.c.n_kv_heads, nb = (p.c.max_ctx + 15) / 16;
   auto smem = [&](int C) { return 1024 + (size_t)Lay::kFixed + ((nb + C - 1) / C) * (size_t)(G * 16 + 1) * 4; };
-  int C = std::max(1, std::min({kMaxCluster, (2 * sms + units - 1) / units, nb / 4}));
-  while (C < kMaxCluster && smem(C) > (size_t)kMaxSmem) ++C;
-  if (smem(C) > (size_t)kMaxSmem) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
+  int C = 0;
+  double least = 0.0;
+  for (int k = 1; k <= kMaxCluster; ++k) {
+    const int one = held[dev][k].load(std::memory_order_relaxed);
+    if (one < 1 || smem(k) > (size_t)kMaxSmem || (C > 0 && nb <= 4 * (k - 1))) continue;
+    const int fit = std::max<int>(1, std::min<int>(4, 228 * 1024 / (int)(smem(k) + sizeof(Shared<HD, G>) + 1024)));
+    const int ctas = units * k, slots = one * fit, waves = (ctas + slots - 1) / slots;
+    const double live = (double)std::min(ctas, slots) / sms;
+    const int tiles = ((nb + k - 1) / k + 3) / 4;
+    const double t = waves * (6.0 + tiles * std::max(0.87, live * (2.0 * Lay::kTile / 44.5e3)));
+    if (C == 0 || t < least) {
+      C = k;
+      least = t;
+    }
+  }
+  if (C == 0) return cudaErrorInvalidValue;
   cfg.gridDim = dim3((unsigned)(units * C));
-  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem(C);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k_attention_weights<HD, G>, p, maps, make_exponent(HD).c);
 }
 
