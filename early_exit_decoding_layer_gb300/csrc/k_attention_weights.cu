@@ -435,7 +435,10 @@ cudaError_t launch_t(const DecodeWeightsParams& p, cudaStream_t st) {
       attr[0].val.clusterDim.x = k;
       cfg.gridDim = dim3(1024 * k);
       cfg.dynamicSmemBytes = kMaxSmem;
-      e = cudaOccupancyMaxActiveClusters(&clusters, k_attention_weights<HD, G>, &cfg);
+      if (cudaOccupancyMaxActiveClusters(&clusters, k_attention_weights<HD, G>, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // a size that this device does not take is not used
+        clusters = 0;
+      }
       held[dev][k].store(clusters * k, std::memory_order_relaxed);
     }
     if (e != cudaSuccess) return e;

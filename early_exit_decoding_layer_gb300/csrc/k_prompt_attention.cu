@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = SPLIT ? (int)cg::this_cluster().block_rank() : 0;
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_free, 2);  // a thread of each warpgroup
+    mbar_init(&sh.q_free, 1);
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 1);
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > 0) mbar_arrive(&sh.kv_empty[stage(base + 2 * j - 1)]);
           mbar_arrive(&sh.kv_empty[stage(base + 2 * j)]);
         }
-        if (r == 0 && j == n - 1) mbar_arrive(&sh.q_free);  // the last product with this Q tile
+        if (frees && j == n - 1) mbar_arrive(&sh.q_free);  // the last product with Q, of both tiles
         const bool masked = u.ka + j >= u.jm[t];
         uint32_t s[kKeys], ph[kKeys / 2];
         auto load = [&]() {
@@ -469,7 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&sh.p_ready[t]);
       }
-      if (r == 0 && n == 0 && nk > 0) mbar_arrive(&sh.q_free);
       if (ok && n > 0) ok = warp_wait(&sh.o_done[t], ends & 1, p.c.err, DERR_FULL_WAIT);
       ends += n > 0;
       tc_fence_after();

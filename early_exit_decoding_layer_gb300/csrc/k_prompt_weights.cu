@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = t >> 1; j < ((t & 1) < nh ? nq : 0); j += 2) {
       float* ls = sh.lse[t][(j >> 1) & 1];
-      // in the exponent's unit; a row that adds nothing has an lse of +inf here
-      ls[r] = next == -INFINITY ? -INFINITY : -fmaf(next, ex.f_hi, next * ex.f_lo);
+      // in the exponent's unit; a row with an infinite lse adds nothing
+      ls[r] = isinf(next) ? -INFINITY : -fmaf(next, ex.f_hi, next * ex.f_lo);
       next = load_lse(j + 2);
       // the other buffer was read two tiles ago, before the barrier of the last one
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");

@@ -561,3 +561,67 @@ def test_full_batch():
         assert np.allclose(x[s].reshape(hq, hd), xo[0], rtol=1e-4, atol=1e-5), s
         assert np.all(np.abs(c.h.gather(w, s) - rw - p) <= bw + 1e-4 * (rw + p) + 1e-6), s
         assert np.array_equal(kept[s, :, :n], oracle.evict_indices(c.h.W[s], 20, 4)), s
+
+
+@pytest.mark.parametrize("hq,hkv,hd,most", [(32, 32, 64, 100), (64, 16, 128, 31), (16, 16, 128, 140)])
+def test_many_small_units(hq, hkv, hd, most):
+    """More (row tile, kv head) pairs than SMs, most of them with one row tile of two, some
+    whose first rows see nothing: every CTA goes through several of them."""
+    rng = np.random.default_rng(hq + hd)
+    rows = [int(x) for x in rng.integers(1, most, 64)]
+    rows[::7] = [2 * most] * len(rows[::7])
+    ctxs = [max(0, r + int(x)) for r, x in zip(rows, rng.integers(-most // 2, 40, 64))]
+    c = Prompt(91, hq, hkv, hd, rows, ctxs)
+    d = c.args()
+    w = torch.zeros(c.h.n_blocks, hkv, 16, device="cuda")
+    first = None
+    for _ in range(3):
+        o, lse = ee.prompt_attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+        first = (o, lse) if first is None else first
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    ee.prompt_weights(d["q"], d["k"], d["table"], d["cu"], d["ctx"], lse, w, *c.shape)
+    o, lse, w = (t.cpu().numpy() for t in (o, lse, w))
+    o = o.astype(np.float64).reshape(c.T, hq, hd)
+    G = hq // hkv
+    for s in range(0, 64, 5):
+        r = c.seq_rows(s)
+        for g in (0, hkv // 2, hkv - 1):   # a kv head's group at a time: the oracle's loops stay short
+            one = History.__new__(History)
+            one.K, one.V = [c.h.K[s][:, g:g + 1]], [c.h.V[s][:, g:g + 1]]
+            heads = slice(g * G, (g + 1) * G)
+            ro, rl, rw, bo, bl, bw = prompt_reference(one, 0, c.q[r][:, heads])
+            assert np.all(np.abs(o[r, heads] - ro) <= bo), (s, g)
+            got, seen = lse[heads, r], ~np.isneginf(rl)
+            assert np.array_equal(~np.isneginf(got), seen) and np.all(np.abs(got[seen] - rl[seen]) <= bl[seen]), (s, g)
+            assert np.all(np.abs(c.h.gather(w, s)[:, g] - rw[:, 0]) <= bw[:, 0] + U32 * rw[:, 0]), (s, g)
+
+
+def test_first_call_may_be_captured():
+    """The first call of each operator in a process, made while a stream is captured."""
+    import subprocess
+    import sys
+    from tests.conftest import ROOT
+    code = """
+import torch
+import early_exit_decoding_layer_gb300 as ee
+d = "cuda"
+q = torch.randn(20, 256, device=d).half()
+k, v = (torch.randn(4, 2, 16, 64, device=d).half() for _ in range(2))
+w = torch.zeros(4, 2, 16, device=d)
+t = torch.arange(4, dtype=torch.int32, device=d).view(1, 4)
+cu, n = torch.tensor([0, 20], dtype=torch.int32, device=d), torch.tensor([20], dtype=torch.int32, device=d)
+q1, pos = q[-1:].float().contiguous(), n - 1
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g, stream=s):
+    o, lse = ee.prompt_attention(q, k, v, t, cu, n, 4, 2, 64, 64)
+    ee.prompt_weights(q, k, t, cu, n, lse, w, 4, 2, 64, 64)
+    x = ee.attention_weights(q1, k, v, t, pos, w, 4, 2, 64, 64)
+    kept, new = ee.evict(k, v, w, t, n, 8, 2, 64)
+g.replay()
+torch.cuda.synchronize()
+assert new.item() == 8 and torch.allclose(x[0], o[-1].float(), atol=5e-3), (x[0] - o[-1].float()).abs().max()
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
