@@ -494,51 +494,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n > 0 ? make_uint4(o[w], o[w + 1], o[w + 2], o[w + 3]) : make_uint4(0, 0, 0, 0);
         }
       } else if (ok) {
-        // Four lanes share a row here, eight rows of 64 columns per store: a thread that
-        // stores its own row touches 32 lines per instruction, and that took 4000
-        // cycles a unit.  Lane a has columns 8 k + 2 a, + 1 of every k; the four
-        // exchange pairs of k so that lane a gets all of k = 2 a and 2 a + 1.
-        const bool wide = ((uintptr_t)p.o & 31) == 0 && (p.o_stride & 15) == 0;
-        const int a = lane & 3;
+        // Two neighbouring lanes write their rows together, 32 bytes each side by side: a
+        // thread that stores its own row alone touches a line per lane.
+        const bool wide = ((uintptr_t)p.o & 31) == 0 && (p.o_stride & 15) == 0, odd = lane & 1;
+        uint16_t* other = reinterpret_cast<uint16_t*>(__shfl_xor_sync(0xffffffffu, (unsigned long long)orow, 1));
+        const bool other_valid = __shfl_xor_sync(0xffffffffu, valid, 1);
+        uint16_t* row_a = (odd ? other : orow) + (odd ? 16 : 0);  // of the even lane
+        uint16_t* row_b = (odd ? orow : other) + (odd ? 16 : 0);
+        const bool a_valid = odd ? other_valid : valid, b_valid = odd ? valid : other_valid;
+        const uint64_t il2 = pack2(il, il);
 #pragma unroll 1
-        for (int i = 0; i < 2 * S::H; ++i) {
-          const int hf = i & 1, cb = i >> 1;  // 16 rows, 64 columns
-          uint32_t v[32];
-          tmem_ld_rows16(o_at + ((uint32_t)(16 * hf) << 16) + 64 * cb, v);
+        for (int i = 0; i < HD; i += 32) {
+          uint32_t o[32], h[16], x[8];
+          tmem_ld32(o_at + i, o);
           tmem_wait_ld();
-          tmem_pin<32>(v);
+          tmem_pin<32>(o);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int rl = 16 * hf + 8 * q + (lane >> 2), rr = (warp & 3) * 32 + rl;  // row of the warp, of the tile
-            const float f = __shfl_sync(0xffffffffu, il, rl);
-            uint32_t e[4][2];  // [k / 2][k % 2]
+          for (int k = 0; k < 16; ++k) {
+            const float2 y = unpack2(mul2(pack2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), il2));
+            const __half2 z = __floats2half2_rn(y.x, y.y);
+            h[k] = n > 0 ? *reinterpret_cast<const uint32_t*>(&z) : 0;
+          }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const __half2 x = __floats2half2_rn(__uint_as_float(v[4 * k + 2 * q]) * f, __uint_as_float(v[4 * k + 2 * q + 1]) * f);
-              e[k >> 1][k & 1] = n > 0 ? *reinterpret_cast<const uint32_t*>(&x) : 0;
-            }
+          for (int k = 0; k < 8; ++k) x[k] = __shfl_xor_sync(0xffffffffu, odd ? h[k] : h[8 + k], 1);
+          uint32_t ra[8], rb[8];
 #pragma unroll
-            for (int x = 1; x < 4; x <<= 1)
+          for (int k = 0; k < 8; ++k) {
+            ra[k] = odd ? x[k] : h[k];
+            rb[k] = odd ? h[8 + k] : x[k];
+          }
+          if (wide) {
+            if (a_valid) st_global_v8(row_a + i, ra);
+            if (b_valid) st_global_v8(row_b + i, rb);
+          } else {
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                if (b & x) continue;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                  const uint32_t got = __shfl_xor_sync(0xffffffffu, (a & x) ? e[b][w] : e[b | x][w], x);
-                  if (a & x) e[b][w] = got;
-                  else e[b | x][w] = got;
-                }
-              }
-            const uint32_t h[8] = {e[0][0], e[1][0], e[2][0], e[3][0], e[0][1], e[1][1], e[2][1], e[3][1]};
-            const int at = u.tl.i0 + t * (kPos / 2) + rr / G;
-            uint16_t* to = p.o + (int64_t)(u.tl.sq.first + at) * p.o_stride + (u.g * G + rr % G) * HD + cb * 64 + a * 16;
-            if (at < u.tl.sq.n) {
-              if (wide) {
-                st_global_v8(to, h);
-              } else {
-                *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(to + 8) = make_uint4(h[4], h[5], h[6], h[7]);
-              }
+            for (int k = 0; k < 8; k += 4) {
+              if (a_valid) *reinterpret_cast<uint4*>(row_a + i + 2 * k) = make_uint4(ra[k], ra[k + 1], ra[k + 2], ra[k + 3]);
+              if (b_valid) *reinterpret_cast<uint4*>(row_b + i + 2 * k) = make_uint4(rb[k], rb[k + 1], rb[k + 2], rb[k + 3]);
             }
           }
         }
