@@ -2,7 +2,9 @@
 
 Argument marshalling only: every step of the decode path runs in the CUDA
 kernels behind the C ABI of ``include/ee.h``.  PyTorch provides device
-memory (the arena and op buffers) and streams.  There is no CPU fallback:
+memory (the arena and op buffers) and streams.  The operators on the paged cache
+(prompt_attention and the functions behind it) go through _binding.so, which
+looks their tensors over in C++.  There is no CPU fallback:
 importing works without a GPU, but every call needs the built library and
 a CUDA device and raises otherwise.
 """
@@ -515,64 +517,23 @@ def vocab_head(u, E, scratch=None, err=None, stream=None):
 
 # ------------------------------------------------- prompts and bounded caches
 
-# A decode step calls these once per layer: the checks are kept to about 0.3 us a
-# tensor, and PyTorch is looked up once.
-_torch = None
+_native = None
 
 
-def _device(what: str, name: str, t) -> int:
-    """The device index of a CUDA tensor; EE_ERR_INVALID_ARG for anything else."""
-    global _torch, _HALF, _F32, _I32
-    if _torch is None:
-        import torch
-        # element types by kind: fp16 (or its bits in 16-bit integers), fp32, int32
-        _HALF, _F32, _I32 = (torch.float16, torch.int16, torch.uint16), (torch.float32,), (torch.int32,)
-        _torch = torch
-    dev = t.get_device() if isinstance(t, _torch.Tensor) else -1
-    if dev < 0:
-        raise EEError(1, "%s: %s has to be a tensor on a CUDA device" % (what, name))
-    return dev
-
-
-_HALF = _F32 = _I32 = ()
-
-
-def _refuse(what: str, dev: int, name: str, t, kinds, shape, how: str):
-    is_t = isinstance(t, _torch.Tensor)
-    got = "%s %s, strides %s on %s" % (t.dtype, tuple(t.shape), t.stride(), t.device) if is_t else type(t).__name__
-    raise EEError(1, "%s: %s has to be a %s %s tensor of shape %s on cuda:%d, not %s"
-                  % (what, name, how, kinds[0], tuple(shape), dev, got))
-
-
-def _addr(what: str, dev: int, name: str, t, kinds, shape) -> int:
-    """t's address; refused (EE_ERR_INVALID_ARG, before any launch) unless t is a
-    contiguous tensor of that shape and type on device dev."""
-    if (not isinstance(t, _torch.Tensor) or t.get_device() != dev or t.dtype not in kinds or t.shape != shape
-            or not t.is_contiguous()):
-        _refuse(what, dev, name, t, kinds, shape, "contiguous")
-    return t.data_ptr()
-
-
-def _rows(what: str, dev: int, name: str, t, kinds, shape):
-    """(address, row stride) of fp16 rows that may lie apart, their values side by side."""
-    if not isinstance(t, _torch.Tensor) or t.get_device() != dev or t.dtype not in kinds or t.shape != shape:
-        _refuse(what, dev, name, t, kinds, shape, "row-wise contiguous")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1]
-    stride = t.stride(0) if shape[0] > 1 else shape[1]
-    if t.stride(1) != 1 or stride < shape[1]:
-        _refuse(what, dev, name, t, kinds, shape, "row-wise contiguous")
-    return t.data_ptr(), stride
-
-
-def _launch(what: str, dev: int, fn, *args):
-    """Calls fn on device dev and its current stream."""
-    if _torch._C._cuda_getDevice() != dev:
-        with _torch.cuda.device(dev):
-            return _launch(what, dev, fn, *args)
-    st = fn(*args, _torch._C._cuda_getCurrentRawStream(dev))
-    if st:
-        _raise(st, what)
+def _cache_ops():
+    """_binding.so: the checks of the cache operators' tensors and their calls (raises if
+    it has not been built; no fallback path)."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (the binding links to its libraries)
+        load_library()
+        try:
+            from . import _binding as native
+        except ImportError as e:
+            raise RuntimeError("_binding.so not built or not loadable: run `python -m "
+                               "early_exit_decoding_layer_gb300.build` (or __graft_entry__.build())") from e
+        _native = native
+    return _native
 
 
 def _on_stream(stream, fn, *args):
@@ -592,20 +553,8 @@ def prompt_attention(q, kcache, vcache, block_table, cu_q, ctx, n_heads, n_kv_he
     if stream is not None:
         return _on_stream(stream, prompt_attention, q, kcache, vcache, block_table, cu_q, ctx, n_heads, n_kv_heads, head_dim,
                           max_ctx, out, err)
-    what = "ee_op_prompt_attention"
-    dev = _device(what, "q", q)
-    T, S, nb, W = q.shape[0], ctx.shape[0], kcache.shape[0], block_table.shape[-1]
-    cache, width = (nb, n_kv_heads, 16, head_dim), n_heads * head_dim
-    qp, qs = _rows(what, dev, "q", q, _HALF, (T, width))
-    o = out if out is not None else _torch.empty((T, width), dtype=_torch.float16, device=q.device)
-    op, os_ = _rows(what, dev, "out", o, _HALF, (T, width))
-    lse = _torch.empty((n_heads, T), dtype=_torch.float32, device=q.device)
-    _launch(what, dev, load_library().ee_op_prompt_attention, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs,
-            _addr(what, dev, "kcache", kcache, _HALF, cache), _addr(what, dev, "vcache", vcache, _HALF, cache), nb,
-            _addr(what, dev, "block_table", block_table, _I32, (S, W)), W, _addr(what, dev, "cu_q", cu_q, _I32, (S + 1,)),
-            _addr(what, dev, "ctx", ctx, _I32, (S,)), op, os_, lse.data_ptr(),
-            0 if err is None else _addr(what, dev, "err", err, _I32, (1,)))
-    return o, lse
+    return _cache_ops().prompt_attention(q, kcache, vcache, block_table, cu_q, ctx, n_heads, n_kv_heads, head_dim, max_ctx,
+                                       out, err)
 
 
 def prompt_weights(q, kcache, block_table, cu_q, ctx, lse, weights, n_heads, n_kv_heads, head_dim, max_ctx,
@@ -616,17 +565,8 @@ def prompt_weights(q, kcache, block_table, cu_q, ctx, lse, weights, n_heads, n_k
     if stream is not None:
         return _on_stream(stream, prompt_weights, q, kcache, block_table, cu_q, ctx, lse, weights, n_heads, n_kv_heads, head_dim,
                           max_ctx, err)
-    what = "ee_op_prompt_weights"
-    dev = _device(what, "q", q)
-    T, S, nb, W = q.shape[0], ctx.shape[0], kcache.shape[0], block_table.shape[-1]
-    qp, qs = _rows(what, dev, "q", q, _HALF, (T, n_heads * head_dim))
-    _launch(what, dev, load_library().ee_op_prompt_weights, S, T, n_heads, n_kv_heads, head_dim, max_ctx, qp, qs,
-            _addr(what, dev, "kcache", kcache, _HALF, (nb, n_kv_heads, 16, head_dim)), nb,
-            _addr(what, dev, "block_table", block_table, _I32, (S, W)), W, _addr(what, dev, "cu_q", cu_q, _I32, (S + 1,)),
-            _addr(what, dev, "ctx", ctx, _I32, (S,)), _addr(what, dev, "lse", lse, _F32, (n_heads, T)),
-            _addr(what, dev, "weights", weights, _F32, (nb, n_kv_heads, 16)),
-            0 if err is None else _addr(what, dev, "err", err, _I32, (1,)))
-    return weights
+    return _cache_ops().prompt_weights(q, kcache, block_table, cu_q, ctx, lse, weights, n_heads, n_kv_heads, head_dim, max_ctx,
+                                     err)
 
 
 def attention_weights(q, kcache, vcache, block_table, pos, weights, n_heads, n_kv_heads, head_dim, max_ctx,
@@ -637,17 +577,8 @@ def attention_weights(q, kcache, vcache, block_table, pos, weights, n_heads, n_k
     if stream is not None:
         return _on_stream(stream, attention_weights, q, kcache, vcache, block_table, pos, weights, n_heads, n_kv_heads, head_dim,
                           max_ctx, out, err)
-    what = "ee_op_attention_weights"
-    dev = _device(what, "q", q)
-    B, nb, W = pos.shape[0], kcache.shape[0], block_table.shape[-1]
-    cache, rows = (nb, n_kv_heads, 16, head_dim), (B, n_heads * head_dim)
-    o = out if out is not None else _torch.empty(rows, dtype=_torch.float32, device=q.device)
-    _launch(what, dev, load_library().ee_op_attention_weights, B, n_heads, n_kv_heads, head_dim, max_ctx,
-            _addr(what, dev, "q", q, _F32, rows), _addr(what, dev, "kcache", kcache, _HALF, cache),
-            _addr(what, dev, "vcache", vcache, _HALF, cache), nb, _addr(what, dev, "block_table", block_table, _I32, (B, W)), W,
-            _addr(what, dev, "pos", pos, _I32, (B,)), _addr(what, dev, "out", o, _F32, rows),
-            _addr(what, dev, "weights", weights, _F32, cache[:3]), 0 if err is None else _addr(what, dev, "err", err, _I32, (1,)))
-    return o
+    return _cache_ops().attention_weights(q, kcache, vcache, block_table, pos, weights, n_heads, n_kv_heads, head_dim, max_ctx,
+                                        out, err)
 
 
 def evict(kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_table=None, err=None, stream=None):
@@ -657,23 +588,4 @@ def evict(kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_
     int32)."""
     if stream is not None:
         return _on_stream(stream, evict, kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_table, err)
-    what = "ee_op_evict"
-    dev = _device(what, "kcache", kcache)
-    if kcache.dim() != 4:
-        raise EEError(1, "%s: kcache has shape %s" % (what, tuple(kcache.shape)))
-    cache, B, W = kcache.shape, ctx.shape[0], block_table.shape[-1]
-    hkv, hd = cache[1], cache[3]
-    dp = ds = 0
-    if dst_table is not None:
-        ds = dst_table.shape[-1]
-        dp = _addr(what, dev, "dst_table", dst_table, _I32, (B, ds))
-    if not 1 <= keep <= max_ctx or (dst_table is not None and ds * 16 < keep):
-        raise EEError(1, "%s: keep has to be in [1, max_ctx] and to fit dst_table" % what)
-    kept = _torch.empty((B, hkv, keep), dtype=_torch.int32, device=kcache.device)
-    new = _torch.empty((B,), dtype=_torch.int32, device=kcache.device)
-    _launch(what, dev, load_library().ee_op_evict, B, hkv, hd, max_ctx, keep, recent,
-            _addr(what, dev, "kcache", kcache, _HALF, (cache[0], hkv, 16, hd)), _addr(what, dev, "vcache", vcache, _HALF, cache),
-            _addr(what, dev, "weights", weights, _F32, cache[:3]), cache[0],
-            _addr(what, dev, "block_table", block_table, _I32, (B, W)), W, dp, ds, _addr(what, dev, "ctx", ctx, _I32, (B,)),
-            new.data_ptr(), kept.data_ptr(), 0 if err is None else _addr(what, dev, "err", err, _I32, (1,)))
-    return kept, new
+    return _cache_ops().evict(kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_table, err)

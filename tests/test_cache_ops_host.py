@@ -94,6 +94,15 @@ def test_binding_refuses_host_tensors():
         assert e.value.status == 1
 
 
+def test_binding_refuses_what_is_no_tensor_or_integer():
+    torch = pytest.importorskip("torch")
+    q = torch.zeros(2, 256, dtype=torch.float16)
+    for call in (lambda: ee.prompt_attention([1.0], q, q, q, q, q, 4, 2, 64, 32), lambda: ee.evict(None, q, q, q, q, 1, 0, 32)):
+        with pytest.raises(ee.EEError) as e:
+            call()
+        assert e.value.status == 1
+
+
 def test_error_codes_match_header():
     import os
     import re

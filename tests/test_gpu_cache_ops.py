@@ -437,6 +437,10 @@ def test_refusals_on_device_tensors():
         with pytest.raises(ee.EEError) as e:
             ee.evict(d["k"], d["v"], w, d["table"], d["ctx"], **{"keep": 8, "recent": 2, "max_ctx": 20, **kw})
         assert e.value.status == 1, kw
+    for kw, error in ((dict(keep=1 << 40), ee.EEError), (dict(max_ctx=-(1 << 70)), ee.EEError), (dict(recent=2.5), TypeError),
+                      (dict(err=w), ee.EEError)):
+        with pytest.raises(error):
+            ee.evict(d["k"], d["v"], w, d["table"], d["ctx"], **{"keep": 8, "recent": 2, "max_ctx": 20, **kw})
     with pytest.raises(ee.EEError):
         ee.attention_weights(d["q"][:1], d["k"], d["v"], d["table"], d["ctx"], w, *c.shape)   # fp16 queries
     with pytest.raises(ee.EEError):
