@@ -76,11 +76,6 @@ EE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int 
       : "memory");
 }
 
-// The same box to L2 only.
-EE_DEV void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
-}
-
 // D[tmem] (+)= A * B, both operands in shared memory.
 EE_DEV void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
@@ -135,19 +130,6 @@ EE_DEV void tmem_ld16(uint32_t addr, uint32_t* v) {
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(addr));
 }
-// 64 columns of 16 lanes: v[4 k + 2 h + i] is column 8 k + 2 (lane % 4) + i of row
-// lane / 4 + 8 h.
-EE_DEV void tmem_ld_rows16(uint32_t addr, uint32_t* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-      "[%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(addr));
-}
 EE_DEV void tmem_st16(uint32_t addr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
@@ -162,15 +144,6 @@ template <int N>
 EE_DEV void tmem_pin(uint32_t* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
-}
-
-// mbar_wait_bounded with the wait itself out of line: where a thread's loop has to
-// stay in the instruction cache, only the first look is part of it.
-static __device__ __noinline__ bool bar_wait_slow(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code) {
-  return mbar_wait_bounded(bar, parity, err, code);
-}
-EE_DEV bool bar_wait(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code) {
-  return mbar_try_wait(bar, parity) || bar_wait_slow(bar, parity, err, code);
 }
 
 // mbar_wait_bounded by a whole warp with one answer for all its lanes, which stay

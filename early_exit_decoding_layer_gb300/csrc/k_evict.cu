@@ -14,7 +14,9 @@
 // warp on a counter (32 copies: clearing and adding them cost 2600 cycles a
 // pass, with 500 keys as with 16000).  Tokens above the resulting key stay, and of
 // those equal to it the first ones, so ties go to the lower index.  Warps own runs
-// of tokens and walk them twice in order, counting and then placing by ballots.
+// of tokens, of which lane i keeps the i-th 32 as a word of bits: slots come from
+// one scan over the words (with ballots and a running slot per 32 tokens, in
+// two walks, this took 10200 cycles of 35000 at 16384 tokens, now 4600).
 //
 // Moving: a kept token's slot is never above the token, so rows move in place in
 // ascending order: the cluster reads a chunk of rows into registers (K, V and
@@ -23,7 +25,8 @@
 //
 // Bound: kept rows read and written.  32 sequences of 256 to 2304 tokens cut to
 // 1024, 8 kv heads, hd 128: 48 us, 5.4 TB/s (0.80 of the measured copy rate); one of
-// 16384 cut to 4096: 25 us, of which the selection is 19; 513 to 256: 6.7 us.
+// 16384 cut to 4096: 22.8 us, of which the selection is 11 (20000 cycles, half of them
+// the histograms' shared-memory atomics); 513 to 256: 6.8 us.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -164,42 +167,50 @@ __global__ void __launch_bounds__(kThreads) k_evict(const EvictParams p) {
     // tokens.  Warp w owns tokens [t0, t1).
     const int each = (n + kThreads - 1) / kThreads * 32;
     const int t0 = min(n, warp * each), t1 = min(n, t0 + each);
-    auto look = [&](int t, bool* eq) {
-      const bool cand = t < m && need > 0;
-      const uint32_t k = cand ? keys[t] & mask : 0u;
-      *eq = cand && k == prefix;
-      return (t >= m && t < t1) || (cand && t < t1 && k > prefix);
-    };
-    int equal = 0, more = 0;
-#pragma unroll 4
-    for (int t = t0 + lane; t < t1 + lane; t += 32) {
-      bool eq;
-      more += look(t, &eq);
-      equal += eq && t < t1;
+    static_assert(kCacheMaxCtx <= 32 * kThreads, "a warp's run is 32 words of 32 tokens");
+    unsigned more = 0, equal = 0;  // of lane i: word i of the run, a bit per token
+#pragma unroll 8
+    for (int i = 0; i < each / 32; ++i) {
+      const uint32_t k = keys[t0 + i * 32 + lane] & mask;  // past the run: other words of shared memory, whose bits go below
+      const unsigned a = __ballot_sync(0xffffffffu, k > prefix), e = __ballot_sync(0xffffffffu, k == prefix);
+      if (lane == i) {
+        more = a;
+        equal = e;
+      }
     }
-    more = __reduce_add_sync(0xffffffffu, (unsigned)more);
-    equal = __reduce_add_sync(0xffffffffu, (unsigned)equal);
-    if (lane == 0) {
-      sums[0][warp] = more;
-      sums[1][warp] = equal;
+    const int word0 = t0 + lane * 32;
+    auto before = [&](int t) { return t <= word0 ? 0u : t >= word0 + 32 ? ~0u : (1u << (t - word0)) - 1u; };
+    const unsigned cand = need > 0 ? before(min(m, t1)) : 0u;
+    equal &= cand;
+    more = (more & cand) | (before(t1) & ~before(m));
+    int slot = __popc(more), seen = __popc(equal);  // up to and with the word
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, slot, o), y = __shfl_up_sync(0xffffffffu, seen, o);
+      if (lane >= o) {
+        slot += x;
+        seen += y;
+      }
+    }
+    if (lane == 31) {
+      sums[0][warp] = slot;
+      sums[1][warp] = seen;
     }
     __syncthreads();
-    int slot = 0, seen = 0;  // kept tokens and equal keys before
     for (int w = 0; w < warp; ++w) {
       slot += sums[0][w];
       seen += sums[1][w];
     }
+    slot -= __popc(more);  // before the word
+    seen -= __popc(equal);
     slot += min(seen, rest);
+    for (int over = __popc(equal) - max(0, rest - seen); over > 0; --over) equal &= ~(0x80000000u >> __clz(equal));
+    const unsigned stay = more | equal;
 #pragma unroll 4
-    for (int t = t0 + lane; t < t1 + lane; t += 32) {
-      bool eq;
-      const bool above = look(t, &eq);
-      const unsigned below = (1u << lane) - 1u, e = __ballot_sync(0xffffffffu, eq && t < t1);
-      const bool stay = above || (eq && t < t1 && seen + __popc(e & below) < rest);
-      const unsigned k = __ballot_sync(0xffffffffu, stay);
-      if (stay) kept[slot + __popc(k & below)] = (uint16_t)t;
-      slot += __popc(k);
-      seen += __popc(e);
+    for (int i = 0; i < each / 32; ++i) {
+      const unsigned word = __shfl_sync(0xffffffffu, stay, i);
+      const int at = __shfl_sync(0xffffffffu, slot, i) + __popc(word & ((1u << lane) - 1u));
+      if (word >> lane & 1) kept[at] = (uint16_t)(t0 + i * 32 + lane);
     }
   }
   __syncthreads();
@@ -257,8 +268,8 @@ cudaError_t launch_t(const EvictParams& p, cudaStream_t st) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // Two CTAs per SM, as long as each has a chunk of rows to move.  16384 to 4096 with 8
-  // kv heads of 128: 81 us with one CTA per head, 35 with 4, 27 with 8, 25 with 12,
-  // 30 with 16 (too large for some GPCs); 32 sequences of up to 2304 to 1024:
+  // kv heads of 128: 78 us with one CTA per head, 33 with 4, 25 with 8, 23 with 12,
+  // and more with 16, too large for some GPCs; 32 sequences of up to 2304 to 1024:
   // 50 us with one, 48 with two, 50 with four.
   const int units = p.batch * p.c.n_kv_heads, chunk = kThreads * kPieces / (HD / 8);
   const int C = std::max(1, std::min({kMaxCluster, (2 * sms + units - 1) / units, (p.keep + chunk - 1) / chunk}));

@@ -5,7 +5,7 @@
 // The keys are the MMA's rows: S = K_tile Q^T gives every thread of a softmax
 // warpgroup one key and, along its registers, 128 query rows, so the sum over
 // the rows stays in the thread: no shuffles, and no second pass over anything.
-// A CTA owns 256 keys of one kv head, two M = 128 tiles that stay in shared memory
+// A CTA owns up to 256 keys of one kv head, two M = 128 tiles that stay in shared memory
 // (one read of the queries serves both: with one tile their way from L2 was the
 // limit); tiles of 128 query rows (128 / G positions x G heads) stream through
 // a ring by TMA from the first row that sees a key:
@@ -33,7 +33,7 @@ namespace cg = cooperative_groups;
 namespace ee {
 namespace {
 
-constexpr int kKeys = 256;     // per CTA: two MMA tiles of 128
+constexpr int kTiles = 2;      // key tiles of 128 per CTA at most
 constexpr int kCols = 128;     // query rows per tile
 constexpr int kGroups = 4;     // softmax warpgroups, each with an S buffer of 128 tensor-memory columns
 constexpr int kThreads = kGroups * 128 + 96;  // and TMA and two MMA warps
@@ -63,7 +63,7 @@ struct Shared {
 
 template <int HD, int G, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_prompt_weights(const PromptParams p, const __grid_constant__ Maps maps, const Exponent ex) {
+    k_prompt_weights(const PromptParams p, const __grid_constant__ Maps maps, const Exponent ex, const int key_tiles) {
   using S = Shape<HD>;
   constexpr int kPos = kCols / G;  // positions per query tile
   extern __shared__ uint8_t smem_raw[];
@@ -75,12 +75,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // first keys first: most rows see them
   const int unit = blockIdx.x / nsplit;
   const int g = unit % p.c.n_kv_heads, s = unit / p.c.n_kv_heads % p.n_seqs;
-  const int key0 = unit / p.c.n_kv_heads / p.n_seqs * kKeys;
+  const int key0 = unit / p.c.n_kv_heads / p.n_seqs * 128 * key_tiles;
   const PromptSeq sq = prompt_seq(p, s);
   const int off = sq.ctx - sq.n;
   const int first = max(0, key0 - off);  // first row that sees a key of the tile
   if (key0 >= sq.ctx || first >= sq.n) return;  // the whole cluster
-  const int nh = key0 + 128 < sq.ctx ? 2 : 1;  // key tiles
+  const int nh = key_tiles == 2 && key0 + 128 < sq.ctx ? 2 : 1;  // key tiles
   const int all = (sq.n - first + kPos - 1) / kPos;
   const int nq = (all - split + nsplit - 1) / nsplit;  // this CTA's: tiles split, split + nsplit, ...
   auto tile_row = [&](int j) { return first + (split + j * nsplit) * kPos; };
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t k_s = smem_addr(tiles), q_s = k_s + 2 * S::kTile;
 
   if (warp == kTma) {
-    const int here = min(kKeys / 16, ((sq.ctx + 15) >> 4) - key0 / 16);  // blocks of the keys
+    const int here = min(nh * 8, ((sq.ctx + 15) >> 4) - key0 / 16);  // blocks of the keys
     const int b16 = lane & 15, half = lane >> 4;
     if (nq > 0) {
       int id = b16 < here ? p.c.table[(int64_t)s * p.c.table_stride + key0 / 16 + b16] : 0;
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_free(tmem, kBuf * kCols);
   }
   if (SPLIT) cg::this_cluster().sync();
-  if (split == 0 && tid < kKeys && key0 + tid < sq.ctx) {
+  if (split == 0 && tid < nh * 128 && key0 + tid < sq.ctx) {
     const int h = tid >> 7, r = tid & 127;
     float w = sh.sum[h][r] + sh.sum[2 + h][r];
     if (SPLIT)
@@ -273,7 +273,14 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   if (!encode_tensor_map(&maps.q, false, 3, p.q, qd, qs, qb) || !encode_tensor_map(&maps.k, false, 2, p.c.k, cd, cs, cb))
     return cudaErrorInvalidValue;
   const Exponent ex = make_exponent(HD);
-  const int64_t units = (int64_t)((p.c.max_ctx + kKeys - 1) / kKeys) * p.n_seqs * p.c.n_kv_heads;
+  // Two key tiles per CTA, or one as long as there is an SM for each; clusters where
+  // SMs are left.  512 tokens of 32/8 heads, hd 64: 7.8 us with one tile, 9.4 with
+  // two; 8 sequences of 4096 with 64/8 heads, hd 128: 1154 with one, 914 with two.
+  auto units_of = [&](int tiles) {
+    return (int64_t)((p.c.max_ctx + 128 * tiles - 1) / (128 * tiles)) * p.n_seqs * p.c.n_kv_heads;
+  };
+  const int key_tiles = units_of(1) <= sms ? 1 : kTiles;
+  const int64_t units = units_of(key_tiles);
   int split = 1;
   while (split < kMaxCluster && units * split * 2 <= sms) split *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -281,7 +288,7 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
-  if (split == 1) return cudaLaunchKernelEx(&cfg, k_prompt_weights<HD, G, false>, p, maps, ex);
+  if (split == 1) return cudaLaunchKernelEx(&cfg, k_prompt_weights<HD, G, false>, p, maps, ex, key_tiles);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = split;
@@ -289,7 +296,7 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_prompt_weights<HD, G, true>, p, maps, ex);
+  return cudaLaunchKernelEx(&cfg, k_prompt_weights<HD, G, true>, p, maps, ex, key_tiles);
 }
 
 }  // namespace
