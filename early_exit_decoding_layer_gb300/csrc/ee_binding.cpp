@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <sstream>
 #include <string>
@@ -262,8 +263,8 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
       D = size(dst, 1, 2, "dst_table");
       dp = address(dst, "dst_table", dev, kI32, {B, D});
     }
-    if (keep < 1 || keep > max_ctx || (a[8] != Py_None && D * 16 < keep))
-      throw Refused{"keep has to be in [1, max_ctx] and to fit dst_table"};
+    if (keep < 1 || keep > 16384 || (a[8] != Py_None && D * 16 < std::min(keep, max_ctx)))
+      throw Refused{"keep has to be in [1, 16384] and to fit dst_table"};
     int32_t* ep = error_word(a[9], dev);
     const at::Tensor kept = empty({B, hkv, keep}, c10::ScalarType::Int, dev), len = empty({B}, c10::ScalarType::Int, dev);
     const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);

@@ -143,8 +143,8 @@ ee_status ee_op_evict(int32_t B, int32_t n_kv_heads, int32_t head_dim, int32_t m
   if (!aligned(vcache, 16) || !aligned(weights, 16) || !aligned(ctx, 4) || !aligned(new_ctx, 4) || new_ctx == ctx ||
       (kept && !aligned(kept, 4)))
     return EE_ERR_INVALID_ARG;
-  if (keep < 1 || keep > max_ctx || recent < 0 || recent > keep) return EE_ERR_INVALID_ARG;
-  if (dst_table && (!aligned(dst_table, 4) || dst_stride < 1 || (int64_t)dst_stride * EE_KV_BLOCK < keep))
+  if (keep < 1 || keep > kCacheMaxCtx || recent < 0 || recent > keep) return EE_ERR_INVALID_ARG;
+  if (dst_table && (!aligned(dst_table, 4) || dst_stride < 1 || (int64_t)dst_stride * EE_KV_BLOCK < std::min(keep, max_ctx)))
     return EE_ERR_INVALID_ARG;
   p.batch = B;
   p.keep = keep;

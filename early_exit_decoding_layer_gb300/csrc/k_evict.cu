@@ -272,11 +272,12 @@ cudaError_t launch_t(const EvictParams& p, cudaStream_t st) {
   // and more with 16, too large for some GPCs; 32 sequences of up to 2304 to 1024:
   // 50 us with one, 48 with two, 50 with four.
   const int units = p.batch * p.c.n_kv_heads, chunk = kThreads * kPieces / (HD / 8);
-  const int C = std::max(1, std::min({kMaxCluster, (2 * sms + units - 1) / units, (p.keep + chunk - 1) / chunk}));
+  const int keep = std::min(p.keep, p.c.max_ctx);
+  const int C = std::max(1, std::min({kMaxCluster, (2 * sms + units - 1) / units, (keep + chunk - 1) / chunk}));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = layout(p.c.max_ctx, min(p.keep, p.c.max_ctx)).bytes;
+  cfg.dynamicSmemBytes = layout(p.c.max_ctx, keep).bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

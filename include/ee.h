@@ -499,11 +499,11 @@ ee_status ee_op_attention_weights(int32_t B, int32_t n_heads, int32_t n_kv_heads
  * new_ctx[s] = keep.  Where ctx[s] <= keep all are kept and new_ctx[s] = ctx[s].
  * kept [B, Hkv, keep] (or NULL) gets the kept tokens' former indices, ascending,
  * then -1.  Slots behind the kept ones are left as they are, and the caller
- * may give away the blocks from ceil(new_ctx / 16) on.  1 <= keep <= max_ctx,
- * 0 <= recent <= keep.
- *   dst_table [B, dst_stride] with 16 * dst_stride >= keep: blocks that no row of
- *   block_table names and that occur once in dst_table; NULL moves in
- *   place (into block_table's own blocks, which then occur once).
+ * may give away the blocks from ceil(new_ctx / 16) on.  1 <= keep <= 16384
+ * (above max_ctx nothing is cut), 0 <= recent <= keep.
+ *   dst_table [B, dst_stride] with 16 * dst_stride >= min(keep, max_ctx): blocks
+ *   that no row of block_table names and that occur once in dst_table; NULL
+ *   moves in place (into block_table's own blocks, which then occur once).
  *   new_ctx must not be ctx. */
 ee_status ee_op_evict(int32_t B, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx, int32_t keep,
                       int32_t recent, uint16_t *kcache, uint16_t *vcache, float *weights, int32_t n_blocks,

@@ -68,7 +68,7 @@ def test_attention_weights_refuses(lib, kw):
     assert attention_weights(lib, **kw) == 1
 
 
-@pytest.mark.parametrize("kw", CACHE + [dict(B=0), dict(B=65), dict(keep=0), dict(keep=65), dict(recent=-1), dict(recent=9),
+@pytest.mark.parametrize("kw", CACHE + [dict(B=0), dict(B=65), dict(keep=0), dict(keep=16385), dict(recent=-1), dict(recent=9),
                                         dict(weights=None), dict(weights=24), dict(ctx=None), dict(new_ctx=None), dict(new_ctx=16), dict(kept=2),
                                         dict(dst=16, dst_stride=0), dict(dst=16, dst_stride=1, keep=17), dict(dst=2)], ids=str)
 def test_evict_refuses(lib, kw):

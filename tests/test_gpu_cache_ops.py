@@ -211,14 +211,14 @@ def test_attention_weights_agrees_with_attention():
 EVICT = [
     (1, 64, [1], 1, 0), (2, 64, [40], 24, 5), (2, 128, [17, 16, 300, 0], 16, 16), (3, 64, [100, 65], 64, 0),
     (8, 128, [513, 90], 100, 7), (1, 128, [2000], 1999, 3), (2, 64, [1500, 700], 1, 1), (2, 64, [129], 128, 1),
-    (1, 64, [5000], 2500, 100),
+    (1, 64, [5000], 2500, 100), (2, 64, [40, 7], 100, 50), (1, 128, [1], 16384, 16384),
 ]
 
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("hkv,hd,ctxs,keep,recent", EVICT)
 def test_evict(hkv, hd, ctxs, keep, recent, in_place):
-    nd = (keep + 15) // 16
+    nd = (min(keep, max(ctxs) + 3) + 15) // 16
     h = History(hd + keep + sum(ctxs), ctxs, hkv, hd, spare=3 + len(ctxs) * nd)
     free = np.setdiff1d(np.arange(h.n_blocks), h.table)
     dst = h.table if in_place else h.rng.permutation(free)[: len(ctxs) * nd].astype(np.int32).reshape(len(ctxs), nd)
@@ -433,7 +433,7 @@ def test_refusals_on_device_tensors():
         with pytest.raises(ee.EEError) as e:
             attn(**kw)
         assert e.value.status == 1, kw
-    for kw in (dict(keep=0), dict(recent=-1), dict(recent=9), dict(keep=21), dict(dst_table=d["table"][:, :0])):
+    for kw in (dict(keep=0), dict(recent=-1), dict(recent=9), dict(keep=16385), dict(dst_table=d["table"][:, :0])):
         with pytest.raises(ee.EEError) as e:
             ee.evict(d["k"], d["v"], w, d["table"], d["ctx"], **{"keep": 8, "recent": 2, "max_ctx": 20, **kw})
         assert e.value.status == 1, kw
