@@ -16,24 +16,24 @@ bool encode_tensor_map(CUtensorMap* map, bool bf16, int rank, const void* base, 
                        const uint64_t* strides, const uint32_t* box);
 
 // Shared memory descriptor of a K-major tile with 128-byte rows and the
-// 128-byte swizzle: start address, stride between 8-row groups (1024 B),
+// 128-byte swizzle: start address, stride between 8-row groups (`group` bytes),
 // descriptor version 1, swizzle mode 2 (leading offset unused: 1).
-EE_DEV uint64_t smem_desc_sw128(uint32_t saddr) {
+EE_DEV uint64_t smem_desc_sw128(uint32_t saddr, uint32_t group = 1024) {
   uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
   d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)(group >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
 }
 
 // The same tile read with its rows along K (MN-major: a row's 64 elements lie
-// along M or N): the stride along K between groups of 8 rows is 1024 B, `half`
+// along M or N): `group` is the stride along K between groups of 8 rows, `half`
 // the bytes between one 64-element column group and the next.
-EE_DEV uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t half) {
+EE_DEV uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t half, uint32_t group = 1024) {
   uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
   d |= (uint64_t)(half >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)(group >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
@@ -73,6 +73,14 @@ EE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int 
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+EE_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
 }
 

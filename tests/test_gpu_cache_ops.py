@@ -163,15 +163,12 @@ DECODE = [
 ]
 
 
-@pytest.mark.parametrize("hq,hkv,hd,ctxs", DECODE)
-def test_attention_weights(hq, hkv, hd, ctxs):
-    h = History(hq + hd + sum(ctxs), ctxs, hkv, hd)
-    B = len(ctxs)
-    q = h.rng.standard_normal((B, hq, hd)).astype(np.float32)
+def check_attention_weights(h, q, ctxs, hkv, table, max_ctx):
+    """One call on history h against the formulas in 64 bits."""
+    B, hq, hd = q.shape
     pos = dev(np.array(ctxs, dtype=np.int32) - 1)
     w, err = dev(h.w), torch.zeros(1, dtype=torch.int32, device="cuda")
-    o = ee.attention_weights(dev(q.reshape(B, -1)), dev(h.k), dev(h.v), dev(h.table), pos, w, hq, hkv, hd, max(ctxs) + 9,
-                             err=err)
+    o = ee.attention_weights(dev(q.reshape(B, -1)), dev(h.k), dev(h.v), dev(table), pos, w, hq, hkv, hd, max_ctx, err=err)
     o, w = o.cpu().numpy().reshape(B, hq, hd), w.cpu().numpy()
     assert err.item() == 0
     g = np.arange(hq) * hkv // hq
@@ -195,6 +192,28 @@ def test_attention_weights(hq, hkv, hd, ctxs):
         assert np.all(np.abs(got - h.W[s] - rw) <= bw + 8 * U32 * (h.W[s] + rw)), s
     unowned = ~np.broadcast_to(h.owned()[:, None], w.shape)
     assert np.all(np.isnan(w[unowned]))
+
+
+@pytest.mark.parametrize("hq,hkv,hd,ctxs", DECODE)
+def test_attention_weights(hq, hkv, hd, ctxs):
+    h = History(hq + hd + sum(ctxs), ctxs, hkv, hd)
+    q = h.rng.standard_normal((len(ctxs), hq, hd)).astype(np.float32)
+    check_attention_weights(h, q, ctxs, hkv, h.table, max(ctxs) + 9)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("hq,hkv,hd,seqs", [(32, 8, 128, 40), (64, 8, 128, 20), (16, 16, 64, 33), (8, 4, 64, 64)])
+def test_attention_weights_many_units(hq, hkv, hd, seqs, wide):
+    """More (sequence, kv head) pairs than the GPU has SMs, so that every cluster has several
+    one after another.  wide: room for 16384 tokens, of which few exist, so that clusters
+    are large and some of their CTAs have nothing to do."""
+    r = np.random.default_rng(seqs + hd)
+    ctxs = [0, 1, 700] + [int(x) for x in np.exp(r.uniform(0, np.log(500), seqs - 3))]
+    h = History(hq + seqs, ctxs, hkv, hd)
+    q = h.rng.standard_normal((seqs, hq, hd)).astype(np.float32)
+    table = np.full((seqs, 1024), 0x7FFFFFF0, dtype=np.int32)
+    table[:, : h.table.shape[1]] = h.table
+    check_attention_weights(h, q, ctxs, hkv, table, 16384 if wide else max(ctxs))
 
 
 def test_attention_weights_agrees_with_attention():
