@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.p_ready[i], 128);
     mbar_init(&sh.o_full[i], 1);
     mbar_init(&sh.q_ready[i], 128);
-    mbar_init(&sh.part_full[i], 128);
+    mbar_init(&sh.part_full[i], 129);  // the softmax warps, and the MMA thread past q_ready
     mbar_init(&sh.part_free[i], 128);
     fence_mbar_init();
   } else if (tid >= 64 && tid < 67) {
@@ -286,6 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; w.s >= 0 && ok; w = work(++r)) {
         const uint64_t qd = smem_desc_sw128(smem_addr(qs) + (r & 1) * Lay::kQ);
         if (!(ok = mbar_wait_bounded(&sh.q_ready[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT))) break;
+        // Where this CTA has no tile nobody waits for this thread's products: without this
+        // arrival Q of unit r + 2 could be placed before it has seen that of unit r.
+        mbar_arrive(&sh.part_full[r & 1]);
         Slot vs[2];  // V of tile t, by t & 1
         auto issue_scores = [&](int t) {
           if (!landed(slot)) return false;
