@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 1; x < 8; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
       const float a = l == 0.0f ? 0.0f : m == M ? 1.0f : ex2((m - M) * c);  // 0: saw nothing
-      float sum = a == 0.0f ? 0.0f : a * l;
+      float sum = a * l;  // a may have gone to 0: a NaN stays
 #pragma unroll
       for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
       if (has) {
@@ -614,8 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               cl.map_shared_rank(reinterpret_cast<float*>(tiles), k0 + k < nsplit ? k0 + k : split) + (size_t)r * S::kPad + col);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float a = k0 + k < nsplit ? sh.fac[k0 + k][i] : 0.0f;
-          if (a != 0.0f) {  // (NaN is not 0)
+          if (k0 + k < nsplit) {
+            // a rank that saw nothing has O = 0; one that counts 0 for its small scores may
+            // have an infinity or NaN, which stays
+            const float a = sh.fac[k0 + k][i];
             o.x = fmaf(a, x[k].x, o.x);
             o.y = fmaf(a, x[k].y, o.y);
             o.z = fmaf(a, x[k].z, o.z);

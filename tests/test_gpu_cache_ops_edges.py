@@ -43,3 +43,70 @@ def test_attention_weights_ranks_without_tiles(hq, hkv, hd):
         first = (o, w) if first is None else first
         assert torch.equal(o, first[0]) and torch.equal(w, first[1])
     assert err.item() == 0
+
+
+# ------------------------------------------------ values that are not finite
+
+def sharpen(h, s, q, t0):
+    """Scores of sequence s's tokens from t0 on about 256 above those before, whatever the
+    row: exp of the difference is 0 in fp32."""
+    q[..., 0] = 16.0
+    step = np.float16(16.0 * math.sqrt(h.hd))
+    for t in range(h.ctxs[s]):
+        h.K[s][t, :, 0] = step if t >= t0 else 0
+        h.k[h.table[s, t // 16], :, t % 16, 0] = h.K[s][t, :, 0]
+
+
+def bits(x):
+    return torch.nan_to_num(x.float(), nan=777.0, posinf=888.0, neginf=999.0)
+
+
+# keys of every unit split over six CTAs; over two; not split
+SPLITS = [(8, 2, 64, [70], [2100]), (4, 1, 128, [9, 30], [640, 40]), (8, 8, 128, [300, 3] * 10, [300, 290] * 10)]
+
+
+@pytest.mark.parametrize("sharp", [False, True])
+@pytest.mark.parametrize("hq,hkv,hd,rows,ctxs", SPLITS)
+def test_prompt_attention_nonfinite_visible_values(hq, hkv, hd, rows, ctxs, sharp):
+    """A value that is not finite reaches every row that sees its token, in its own component
+    alone, however small the token's probability and whichever CTA has it."""
+    c = Prompt(hq + hd + sum(rows), hq, hkv, hd, rows, ctxs)
+    n, ctx, G = rows[0], ctxs[0], hq // hkv
+    if sharp:
+        sharpen(c.h, 0, c.q[:n], ctx - n - 40 if ctx > n + 40 else ctx // 2)
+    d = c.args()
+    clean, lse = ee.prompt_attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+    # of an early tile, of the last tile before the rows' own, of a tile that some rows see in part
+    cells = {(3, 0, 5): np.inf, (7, hkv - 1, 6): np.nan, (130, 0, 9): -np.inf, (ctx - n // 2, hkv - 1, 11): np.inf,
+             (ctx - n, 0, 40): np.nan, (ctx - 1, 0, hd - 1): -np.inf}
+    v = c.h.v.copy()
+    hit = torch.zeros(c.T, hq, hd, dtype=torch.bool, device="cuda")
+    for (t, g, i), x in cells.items():
+        v[c.h.table[0, t // 16], g, t % 16, i] = x
+        hit[max(0, t - (ctx - n)):n, g * G:(g + 1) * G, i] = True
+    o, lse2 = ee.prompt_attention(d["q"], d["k"], dev(v), d["table"], d["cu"], d["ctx"], *c.shape)
+    o, clean = o.view(c.T, hq, hd), clean.view(c.T, hq, hd)
+    assert torch.isfinite(clean).all() and torch.equal(lse, lse2)
+    assert not torch.isfinite(o[hit]).any()
+    assert torch.equal(o[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("sharp", [False, True])
+@pytest.mark.parametrize("hq,hkv,hd,rows,ctxs", SPLITS)
+def test_prompt_attention_nan_key(hq, hkv, hd, rows, ctxs, sharp):
+    """A NaN key makes the rows that see it NaN, their log-sum-exp too, and no others."""
+    c = Prompt(hq + hd + sum(rows), hq, hkv, hd, rows, ctxs)
+    n, ctx, G = rows[0], ctxs[0], hq // hkv
+    if sharp:
+        sharpen(c.h, 0, c.q[:n], ctx - n - 40 if ctx > n + 40 else ctx // 2)
+    d = c.args()
+    clean, lse = ee.prompt_attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+    for t in (3, ctx - n // 2):
+        k = c.h.k.copy()
+        k[c.h.table[0, t // 16], hkv - 1, t % 16, 8] = np.nan
+        hit = torch.zeros(c.T, hq, dtype=torch.bool, device="cuda")
+        hit[max(0, t - (ctx - n)):n, (hkv - 1) * G:] = True
+        o, lse2 = ee.prompt_attention(d["q"], dev(k), d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+        o = o.view(c.T, hq, hd)
+        assert torch.isnan(o[hit]).all() and torch.isnan(lse2.t()[hit]).all(), t
+        assert torch.equal(o[~hit], clean.view(c.T, hq, hd)[~hit]) and torch.equal(lse2.t()[~hit], lse.t()[~hit]), t
