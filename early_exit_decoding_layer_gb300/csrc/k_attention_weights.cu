@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k < C) {
             const float lk = sh.sum[k][jt], f = lk == 0.0f ? 0.0f : mk[k] == mm ? 1.0f : ex2(mk[k] - mm);
             sh.f[k][jt] = f;
-            if (f != 0.0f) ll = fmaf(f, lk, ll);
+            ll = fmaf(f, lk, ll);  // f may have gone to 0: a NaN stays
           }
         sh.M[jt] = mm;
         sh.inv[jt] = ll == 0.0f ? 0.0f : 1.0f / ll;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float a = 0.0f;
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k)
-          if (k < C && sh.f[k][h] != 0.0f) a = fmaf(sh.f[k][h], parts_of[k * share + i - first], a);
+          if (k < C) a = fmaf(sh.f[k][h], parts_of[k * share + i - first], a);
         p.o[((size_t)s * p.n_heads + g * G) * HD + i] = a * sh.inv[h];
       }
       // the weights of this CTA's tokens; inv has the probabilities' 2^kLift

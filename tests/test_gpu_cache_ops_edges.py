@@ -110,3 +110,45 @@ def test_prompt_attention_nan_key(hq, hkv, hd, rows, ctxs, sharp):
         o = o.view(c.T, hq, hd)
         assert torch.isnan(o[hit]).all() and torch.isnan(lse2.t()[hit]).all(), t
         assert torch.equal(o[~hit], clean.view(c.T, hq, hd)[~hit]) and torch.equal(lse2.t()[~hit], lse.t()[~hit]), t
+
+
+# sequences on clusters, and more of them than SMs
+DECODE = [(8, 2, 64, [2100]), (32, 8, 128, [2304, 700]), (4, 4, 128, [290, 600, 33] * 21)]
+
+
+@pytest.mark.parametrize("sharp", [False, True])
+@pytest.mark.parametrize("hq,hkv,hd,ctxs", DECODE)
+def test_attention_weights_nonfinite(hq, hkv, hd, ctxs, sharp):
+    """The same of decode steps: a value reaches its component of the group's heads, a NaN key
+    all their outputs and the weight of every token of its kv head."""
+    h = History(hq + hd + sum(ctxs), ctxs, hkv, hd)
+    B, G, c = len(ctxs), hq // hkv, ctxs[0]
+    q = h.rng.standard_normal((B, hq, hd)).astype(np.float32)
+    if sharp:
+        sharpen(h, 0, q[0], c - 20)
+    pos, table = dev(np.array(ctxs, dtype=np.int32) - 1), dev(h.table)
+
+    def call(k, v):
+        w = dev(h.w)
+        o = ee.attention_weights(dev(q.reshape(B, -1)), dev(k), dev(v), table, pos, w, hq, hkv, hd, max(ctxs))
+        return o.view(B, hq, hd), w
+
+    clean, w0 = call(h.k, h.v)
+    assert torch.isfinite(clean).all()
+    v, hit = h.v.copy(), torch.zeros(B, hq, hd, dtype=torch.bool, device="cuda")
+    for (t, g, i), x in {(3, 0, 5): np.inf, (140, hkv - 1, 6): np.nan, (c - 1, 0, hd - 1): -np.inf, (c - 150, 0, 9): -np.inf}.items():
+        v[h.table[0, t // 16], g, t % 16, i] = x
+        hit[0, g * G:(g + 1) * G, i] = True
+    o, w = call(h.k, v)
+    assert not torch.isfinite(o[hit]).any()
+    assert torch.equal(o[~hit], clean[~hit]) and torch.equal(bits(w), bits(w0))
+    for t in (3, c - 150, c - 1):
+        k, hit = h.k.copy(), torch.zeros(B, hq, dtype=torch.bool, device="cuda")
+        k[h.table[0, t // 16], hkv - 1, t % 16, 8] = np.nan
+        hit[0, (hkv - 1) * G:] = True
+        o, w = call(k, h.v)
+        assert torch.isnan(o[hit]).all() and torch.equal(o[~hit], clean[~hit]), t
+        own = np.zeros(h.w.shape, dtype=bool)
+        own[h.table[0, np.arange(c) // 16], hkv - 1, np.arange(c) % 16] = True
+        own = dev(own)
+        assert torch.isnan(w[own]).all() and torch.equal(bits(w[~own]), bits(w0[~own])), t
