@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.f[k][jt] = f;
             ll = fmaf(f, lk, ll);  // f may have gone to 0: a NaN stays
           }
-        sh.M[jt] = mm;
+        sh.M[jt] = mm == -INFINITY ? 0.0f : mm;  // scores of -inf alone: no weight, not NaN
         sh.inv[jt] = ll == 0.0f ? 0.0f : 1.0f / ll;
       }
       meet();

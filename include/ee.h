@@ -490,7 +490,8 @@ ee_status ee_op_prompt_weights(int32_t n_seqs, int32_t total_q, int32_t n_heads,
  * rounding) that also adds what each token weighs:
  *   weights[block(t), g, t % 16] += sum over the query heads of kv head g of
  *   softmax_t(q_h . k_t / sqrt(hd)),  t <= pos[s].
- * pos[s] = -1 is an empty sequence: o = 0, no weight is added. */
+ * pos[s] = -1 is an empty sequence: o = 0, no weight is added.  Nor is any by a
+ * head whose scores are all -INF. */
 ee_status ee_op_attention_weights(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                   int32_t max_ctx, const float *q, const uint16_t *kcache,
                                   const uint16_t *vcache, int32_t n_blocks, const int32_t *block_table,

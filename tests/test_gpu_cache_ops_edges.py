@@ -152,3 +152,28 @@ def test_attention_weights_nonfinite(hq, hkv, hd, ctxs, sharp):
         own[h.table[0, np.arange(c) // 16], hkv - 1, np.arange(c) % 16] = True
         own = dev(own)
         assert torch.isnan(w[own]).all() and torch.equal(bits(w[~own]), bits(w0[~own])), t
+
+
+def test_attention_weights_all_scores_minus_infinity():
+    """A head whose scores are all -infinity weighs nothing: o = 0, as prompt_attention has it,
+    and no weight is added; the other heads' are."""
+    hq, hkv, hd, c = 4, 2, 64, 300
+    h = History(17, [c, 40], hkv, hd)
+    q = h.rng.standard_normal((2, hq, hd)).astype(np.float32)
+    # sequence 0, kv head 0: keys of -infinity in dimension 0, the only one its two heads ask for
+    q[0, :2] = 0
+    q[0, :2, 0] = 1.0
+    t = np.arange(c)
+    k = h.k.copy()
+    k[h.table[0, t // 16], 0, t % 16, 0] = -np.inf
+    pos, table = dev(np.array([c - 1, 39], dtype=np.int32)), dev(h.table)
+    out = []
+    for kk in (h.k, k):
+        w = dev(h.w)
+        out.append((ee.attention_weights(dev(q.reshape(2, -1)), dev(kk), dev(h.v), table, pos, w, hq, hkv, hd, 320), w))
+    (o0, w0), (o, w) = out
+    o0, o = o0.view(2, hq, hd), o.view(2, hq, hd)
+    assert torch.all(o[0, :2] == 0) and torch.equal(o[0, 2:], o0[0, 2:]) and torch.equal(o[1], o0[1])
+    got, before = h.gather(w.cpu().numpy(), 0), h.W[0]
+    assert np.array_equal(got[:, 0], before[:, 0])
+    assert np.array_equal(got[:, 1], h.gather(w0.cpu().numpy(), 0)[:, 1])
