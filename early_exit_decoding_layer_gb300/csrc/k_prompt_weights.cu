@@ -58,6 +58,7 @@ struct Shared {
   uint64_t k_full, q_full[8], q_empty[8], s_full[kBuf], s_free[kBuf];
   uint32_t tmem;
   alignas(16) float lse[kGroups][2][kCols];  // by warpgroup, two tiles
+  uint2 odd[kGroups][kCols / 32];            // its columns of infinite (x) and NaN (y) lse, a bit each
   float sum[kGroups][128];
 };
 
@@ -165,8 +166,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warpgroup t: key tile t & 1, query tiles j = t / 2, t / 2 + 2, ..
     const int t = warp >> 2, r = tid & 127, keys = key0 + (t & 1) * 128, key = keys + r;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    // column r of a tile: its lse, -inf for a row of nobody.  What becomes of it waits
-    // until the next tile, when the load is over.
+    // Column r of a tile: its lse, -inf for a row of nobody.  What becomes of it waits
+    // until the next tile, when the load is over.  A column whose lse is infinite adds
+    // nothing, whatever its scores are, and one with a NaN lse is NaN only for the keys that
+    // it sees.  Neither comes out of c S - f lse, so a vote with the barrier that is there finds
+    // tiles with such a column, and their scores are set.
     auto load_lse = [&](int j) {
       const int row = j < nq ? tile_row(j) + r / G : sq.n;
       return row < sq.n ? p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row] : -INFINITY;
@@ -176,11 +180,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = t >> 1; j < ((t & 1) < nh ? nq : 0); j += 2) {
       float* ls = sh.lse[t][(j >> 1) & 1];
-      // in the exponent's unit; a row with an infinite lse adds nothing
-      ls[r] = isinf(next) ? -INFINITY : -fmaf(next, ex.f_hi, next * ex.f_lo);
+      const float now = next;
+      ls[r] = isinf(now) ? -INFINITY : -fmaf(now, ex.f_hi, now * ex.f_lo);  // in the exponent's unit
       next = load_lse(j + 2);
       // the other buffer was read two tiles ago, before the barrier of the last one
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+      int odd = !(fabsf(now) < INFINITY);
+      asm volatile(
+          "{ .reg .pred p, q; setp.ne.s32 p, %0, 0; barrier.cta.red.or.pred q, %1, 128, p; selp.s32 %0, 1, 0, q; }"
+          : "+r"(odd)
+          : "r"(1 + t)
+          : "memory");
+      if (odd) {
+        const unsigned none = __ballot_sync(0xffffffffu, isinf(now)), nan = __ballot_sync(0xffffffffu, isnan(now));
+        if (lane == 0) sh.odd[t][warp & 3] = make_uint2(none, nan);
+        if (!(fabsf(now) < INFINITY)) ls[r] = 0.0f;
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+      }
       const int row0 = tile_row(j);
       const uint32_t at = tmem + t * kCols + lane_base;
       // after a wait that gave up the loop goes on without waiting: every thread
@@ -205,6 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.s_free[t]);
         }
         uint32_t* x = v[k & 1];
+        if (odd) {
+          const uint2 m = sh.odd[t][k];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (m.x >> i & 1) x[i] = 0xff800000u;
+            if (m.y >> i & 1) x[i] = 0x7fffffffu;
+          }
+        }
         if (masked) {  // rows before the key, rows of no one: -inf
 #pragma unroll
           for (int i = 0; i < 32; ++i)

@@ -479,7 +479,8 @@ ee_status ee_op_prompt_attention(int32_t n_seqs, int32_t total_q, int32_t n_head
  *   weights[block(t), g, t % 16] += sum over rows with p >= t and over the query
  *   heads h of kv head g of exp(z_t - lse[h, row]).
  * Arguments as above; lse [Hq, total_q] as ee_op_prompt_attention wrote it (a
- * row whose lse is -INF adds nothing). */
+ * row whose lse is -INF adds nothing, whatever its queries; one whose lse is NaN
+ * makes the weights of the tokens that it sees NaN, and no others). */
 ee_status ee_op_prompt_weights(int32_t n_seqs, int32_t total_q, int32_t n_heads, int32_t n_kv_heads,
                                int32_t head_dim, int32_t max_ctx, const uint16_t *q, int64_t q_stride,
                                const uint16_t *kcache, int32_t n_blocks, const int32_t *block_table,

@@ -177,3 +177,36 @@ def test_attention_weights_all_scores_minus_infinity():
     got, before = h.gather(w.cpu().numpy(), 0), h.W[0]
     assert np.array_equal(got[:, 0], before[:, 0])
     assert np.array_equal(got[:, 1], h.gather(w0.cpu().numpy(), 0)[:, 1])
+
+
+@pytest.mark.parametrize("hq,hkv,hd,n,ctx", [(8, 2, 64, 200, 200), (8, 1, 128, 150, 420), (4, 4, 64, 700, 700), (16, 8, 64, 5, 90)])
+def test_prompt_weights_of_rows_that_do_not_count(hq, hkv, hd, n, ctx):
+    """A row's log-sum-exp of NaN reaches the tokens that the row sees and no others; a row
+    whose log-sum-exp is -infinity adds nothing, whatever its queries are."""
+    c = Prompt(hq + n, hq, hkv, hd, [n, 30], [ctx, 50])
+    d, G, off = c.args(), hq // hkv, ctx - n
+    _, lse = ee.prompt_attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+
+    def weights(q, lse):
+        w = torch.zeros(c.h.n_blocks, hkv, 16, device="cuda")
+        ee.prompt_weights(q, d["k"], d["table"], d["cu"], d["ctx"], lse, w, *c.shape)
+        w = w.cpu().numpy()
+        return c.h.gather(w, 0), c.h.gather(w, 1)
+
+    clean, other = weights(d["q"], lse)
+    q = d["q"].clone().view(c.T, hq, hd)
+    for r in (n // 2, n - 1, 0):
+        bad = lse.clone()
+        bad[G - 1, r] = math.nan
+        got, o = weights(d["q"], bad)
+        assert np.isnan(got[: off + r + 1, 0]).all(), r
+        assert np.array_equal(got[off + r + 1:, 0], clean[off + r + 1:, 0]), r
+        assert np.array_equal(got[:, 1:], clean[:, 1:]) and np.array_equal(o, other), r
+        off_row = lse.clone()
+        off_row[:, r] = -math.inf
+        want, _ = weights(d["q"], off_row)
+        for x in (math.nan, math.inf, -math.inf):
+            q2 = q.clone()
+            q2[r, :, 3] = x
+            got, o = weights(q2.view(c.T, -1), off_row)
+            assert np.array_equal(got, want) and np.array_equal(o, other), (r, x)
