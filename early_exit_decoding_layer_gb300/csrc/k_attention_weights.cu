@@ -483,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < HD / 32; ++e) big = fmaxf(big, fabsf(x[i][e]));
           big = warp_max(big);
-          // 2^k with 2^9 <= big 2^k < 2^10, k within +-60
-          int k = 136 - (int)(__float_as_uint(big) >> 23);
-          k = max(-60, min(60, k));
+          // 2^k with 2^9 <= big 2^k < 2^10; k is -119 or more, and at most 60: what is smaller
+          // scores less than 2^-28 with any keys
+          const int k = min(60, 136 - (int)(__float_as_uint(big) >> 23));
           const float up = __uint_as_float((uint32_t)(127 + k) << 23);
           if (lane == 0) sh.unscale[buf][h] = __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll

@@ -210,3 +210,33 @@ def test_prompt_weights_of_rows_that_do_not_count(hq, hkv, hd, n, ctx):
             q2[r, :, 3] = x
             got, o = weights(q2.view(c.T, -1), off_row)
             assert np.array_equal(got, want) and np.array_equal(o, other), (r, x)
+
+
+@pytest.mark.parametrize("power", [-100, -70, 58, 70, 80, 110])
+@pytest.mark.parametrize("hq,hkv,hd", [(8, 2, 64), (8, 8, 128)])
+def test_attention_weights_queries_of_any_size(hq, hkv, hd, power):
+    """Queries of 2^power: far down every token weighs the same, far up one has all the
+    weight.  Scores are within fp32 in all of them."""
+    ctxs = [300, 45]
+    h = History(power + 200 + hd, ctxs, hkv, hd)
+    q = (h.rng.standard_normal((2, hq, hd)) * 2.0 ** power).astype(np.float32)
+    pos, w = dev(np.array(ctxs, dtype=np.int32) - 1), dev(h.w)
+    o = ee.attention_weights(dev(q.reshape(2, -1)), dev(h.k), dev(h.v), dev(h.table), pos, w, hq, hkv, hd, 300)
+    o, w, g = o.cpu().numpy().reshape(2, hq, hd), w.cpu().numpy(), np.arange(hq) * hkv // hq
+    for s, c in enumerate(ctxs):
+        K, V, q64 = h.K[s].astype(np.float64), h.V[s].astype(np.float64), q[s].astype(np.float64)
+        z = np.einsum("hd,thd->ht", q64, K[:, g]) / math.sqrt(hd)
+        if power > 0:   # the largest score is ahead of the next by more than any error of theirs
+            order = np.sort(z, 1)
+            assert np.all(order[:, -1] - order[:, -2] > 200 + 2 * score_error(q64, K))
+        p = np.exp(z - z.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        # as in check_attention_weights; a one-hot row has no error but its division's
+        rel = 0.0 if power > 0 else 2 * score_error(q64, K).max() + 4 * U32 * np.abs(z).max()
+        rel += (c + 32) * U32
+        ref, mag = np.einsum("ht,thd->hd", p, V[:, g]), np.einsum("ht,thd->hd", p, np.abs(V[:, g]))
+        assert np.all(np.abs(o[s] - ref) <= rel * mag + 1e-30), s
+        add = np.zeros_like(h.W[s], dtype=np.float64)
+        for a in range(hq):
+            add[:, g[a]] += p[a]
+        assert np.all(np.abs(h.gather(w, s) - h.W[s] - add) <= rel * add + 8 * U32 * (h.W[s] + add)), s
