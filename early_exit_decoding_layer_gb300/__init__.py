@@ -3,7 +3,7 @@
 Argument marshalling only: every step of the decode path runs in the CUDA
 kernels behind the C ABI of ``include/ee.h``.  PyTorch provides device
 memory (the arena and op buffers) and streams.  The operators on the paged cache
-(prompt_attention and the functions behind it) go through _binding.so, which
+(prompt_attention and the functions behind it) go through _binding, which
 looks their tensors over in C++.  There is no CPU fallback:
 importing works without a GPU, but every call needs the built library and
 a CUDA device and raises otherwise.
@@ -521,17 +521,20 @@ _native = None
 
 
 def _cache_ops():
-    """_binding.so: the checks of the cache operators' tensors and their calls (raises if
-    it has not been built; no fallback path)."""
+    """_binding: the checks of the cache operators' tensors and their calls (raises if it
+    has not been built, or for another PyTorch; no fallback path)."""
     global _native
     if _native is None:
-        import torch  # noqa: F401  (the binding links to its libraries)
+        import torch  # the binding links to its libraries
         load_library()
         try:
             from . import _binding as native
         except ImportError as e:
-            raise RuntimeError("_binding.so not built or not loadable: run `python -m "
+            raise RuntimeError("_binding not built or not loadable: run `python -m "
                                "early_exit_decoding_layer_gb300.build` (or __graft_entry__.build())") from e
+        if native.torch_version != torch.__version__:
+            raise RuntimeError("_binding was built for PyTorch %s, not %s: run `python -m early_exit_decoding_layer_gb300.build`"
+                               % (native.torch_version, torch.__version__))
         _native = native
     return _native
 

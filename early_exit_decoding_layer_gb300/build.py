@@ -1,8 +1,10 @@
-"""Builds libee.so (the CUDA kernels, runtime and C ABI) in-tree for sm_103a, and
-_binding.so (the paged-cache operators' binding to PyTorch, with g++).
+"""Builds libee.so (the CUDA kernels, runtime and C ABI) in-tree for sm_103a, and the
+_binding extension module (the paged-cache operators' binding to PyTorch, with g++).
 
 Each source is compiled in parallel, then linked into a shared library next to
-this file.  Usage: ``python -m early_exit_decoding_layer_gb300.build``.
+this file.  libee.so needs nvcc alone.  The binding is left out where there is no
+PyTorch, and an error in it is printed and stops nothing else: the operators' Python
+functions raise where it is missing.  Usage: ``python -m early_exit_decoding_layer_gb300.build``.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -19,7 +22,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libee.so")
-BINDING = os.path.join(HERE, "_binding.so")
+# named for this Python, so that another one does not load it
+BINDING = os.path.join(HERE, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 BINDING_SRC = os.path.join(CSRC, "ee_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -34,24 +38,76 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: set NVCC or put CUDA's bin directory on PATH")
 
 
-def torch_dir() -> str:
+def torch_dir():
+    """The directory of PyTorch, None where there is none (it is not imported)."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.origin:
-        raise RuntimeError("PyTorch not found: the binding is built against its headers")
-    return os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
-def _binding_commands(cc: str, obj: str, out: str):
-    """(compile, link) of _binding.so."""
-    t, cuda = torch_dir(), os.path.dirname(os.path.dirname(os.path.realpath(cc)))
+def _torch_version(t: str) -> str:
+    """The text of PyTorch's version file."""
+    with open(os.path.join(t, "version.py")) as f:
+        return f.read()
+
+
+def _binding_commands(cc: str, t: str, obj: str, out: str):
+    """(compile, link) of the binding."""
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(cc)))
     cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    compile_ = [cxx, "-O2", "-fPIC", "-std=c++17", "-fvisibility=hidden", *["-I" + i for i in inc], "-c", BINDING_SRC, "-o", obj]
+    version = re.search(r"^__version__ = '([^']*)'", _torch_version(t), re.M).group(1)
+    compile_ = [cxx, "-O2", "-fPIC", "-std=c++17", "-fvisibility=hidden", '-DEE_TORCH_VERSION="%s"' % version,
+                *["-I" + i for i in inc], "-c", BINDING_SRC, "-o", obj]
     lib = os.path.join(t, "lib")
-    link = [cxx, "-shared", "-o", out, obj, "-L" + HERE, "-l:libee.so", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib,
-            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    link = [cxx, "-shared", "-o", out, obj, "-L" + os.path.dirname(LIB), "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+            "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     return compile_, link
+
+
+class _Binding:
+    """The binding's part of a build.  `stamp` says what the binding on disk was built with:
+    the commands and PyTorch's version file, in which neither source nor header shows."""
+
+    def __init__(self, cc: str, hdrs, force: bool):
+        self.dir = torch_dir()
+        self.compile = None
+        if self.dir is None:
+            return
+        obj, self.stamp = os.path.join(BUILD, "ee_binding.o"), os.path.join(BUILD, "ee_binding.stamp")
+        compile_, self.link = _binding_commands(cc, self.dir, obj, BINDING)
+        self.want = "\n".join([" ".join(compile_), " ".join(self.link), sys.version, _torch_version(self.dir)])
+        have = ""
+        if os.path.exists(self.stamp):
+            with open(self.stamp) as f:
+                have = f.read()
+        if force or have != self.want or _stale(obj, [BINDING_SRC] + hdrs) or _stale(BINDING, [obj]):
+            self.compile = compile_
+
+    def finish(self, compiled):
+        """Links what `compiled` (the finished compile process) made; True if the binding is there."""
+        if os.path.exists(self.stamp):
+            os.remove(self.stamp)
+        tmp = BINDING + ".%d.tmp" % os.getpid()
+        r = compiled
+        if r.returncode == 0:
+            r = _run([tmp if x == BINDING else x for x in self.link])[1]
+        if r.returncode != 0:
+            sys.stderr.write("the binding to PyTorch was not built (libee.so is not affected):\n" + r.stdout + r.stderr)
+            if os.path.exists(BINDING):
+                os.remove(BINDING)  # it is not of these sources
+            return False
+        os.replace(tmp, BINDING)
+        with open(self.stamp, "w") as f:
+            f.write(self.want)
+        return True
+
+
+def _run(cmd):
+    try:
+        return cmd, subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return cmd, subprocess.CompletedProcess(cmd, 1, "", "%s: %s\n" % (cmd[0], e))
 
 
 def _sources():
@@ -86,23 +142,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
-    bobj = os.path.join(BUILD, "ee_binding.o")
-    bcompile, _ = _binding_commands(cc, bobj, BINDING)
-    bnew = force or _stale(bobj, [BINDING_SRC] + hdrs)
-    if bnew:
-        jobs.append(bcompile)
-
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return cmd, r
-
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        for cmd, r in ex.map(run, jobs):
+    binding = _Binding(cc, hdrs, force)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        bound = ex.submit(_run, binding.compile) if binding.compile else None
+        for cmd, r in ex.map(_run, jobs):
             if verbose or ptxas_info or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
                 raise RuntimeError("compilation of %s failed" % cmd[-3])
-    if force or len(jobs) > bnew or _stale(LIB, objs):
+    if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".%d.tmp" % os.getpid()
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -110,14 +158,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link of libee.so failed")
         os.replace(tmp, LIB)
-    if bnew or _stale(BINDING, [bobj]):
-        tmp = BINDING + ".%d.tmp" % os.getpid()
-        cmd = _binding_commands(cc, bobj, tmp)[1]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            raise RuntimeError("link of _binding.so failed")
-        os.replace(tmp, BINDING)
+    if bound:
+        binding.finish(bound.result()[1])
     return LIB
 
 

@@ -1,4 +1,4 @@
-// Python binding of the paged-cache operators (_binding.so): the checks of their
+// Python binding of the paged-cache operators (the _binding module): the checks of their
 // tensors, the results' allocation and the call of libee.so.
 //
 // A decode step calls these once per layer.  Through ctypes a call cost 8 to 16 us of
@@ -286,4 +286,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  // inlined accessors of tensors fit the PyTorch that they were compiled against alone
+  if (m && PyModule_AddStringConstant(m, "torch_version", EE_TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
