@@ -1,5 +1,7 @@
 // Host side of the tiled TMA loads: the driver's tensor-map encoder, looked up
-// once.
+// until it is found.
+#include <atomic>
+
 #include "ee_tcgen05.cuh"
 
 namespace ee {
@@ -22,8 +24,15 @@ EncodeTiledFn lookup() {
 
 bool encode_tensor_map(CUtensorMap* map, bool bf16, int rank, const void* base, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box) {
-  static const EncodeTiledFn fn = lookup();
-  if (!fn || rank < 1 || rank > 5) return false;
+  static std::atomic<EncodeTiledFn> found{nullptr};
+  EncodeTiledFn fn = found.load(std::memory_order_acquire);
+  if (!fn) {
+    // a failure is of this call: the next one asks again
+    fn = lookup();
+    if (!fn) return false;
+    found.store(fn, std::memory_order_release);
+  }
+  if (rank < 1 || rank > 5) return false;
   cuuint64_t d[5], st[5];
   cuuint32_t b[5], es[5];
   for (int i = 0; i < rank; ++i) {
