@@ -87,6 +87,7 @@ template <int HD, int G>
 struct Shared {
   uint64_t full[Layout<HD>::kMost], empty[Layout<HD>::kMost], s_full[2], p_ready[2], o_full[2];
   uint64_t q_ready[2], part_full[2], part_free[2];  // by unit & 1
+  uint64_t drained;                                 // every MMA issued is over
   uint64_t joined[3];                               // every rank's part of a unit is there; by unit % 3
   uint32_t tmem;
   int order[EE_MAX_BATCH], tokens[EE_MAX_BATCH];  // sequences by falling length
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   } else if (tid >= 64 && tid < 67) {
     mbar_init(&sh.joined[tid - 64], 1);
+    if (tid == 64) mbar_init(&sh.drained, 1);
     fence_mbar_init();
   }
   if (warp == 9) tmem_alloc(&sh.tmem, 64);
@@ -266,9 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       w = then;
       now = first;
     }
-    if (!ok)  // copies land before the CTA ends
-      for (int i = max(0, issued - ns); i < issued; ++i)
-        mbar_wait_bounded(&sh.full[i % ns], (uint32_t)(i / ns) & 1, p.c.err, DERR_DRAIN_WAIT);
+    // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
+    for (int i = max(0, issued - ns); i < issued; ++i)
+      mbar_wait_bounded(&sh.full[i % ns], (uint32_t)(i / ns) & 1, p.c.err, DERR_DRAIN_WAIT);
     __syncwarp();
     cluster_ready();
     cluster_done();
@@ -320,6 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&sh.o_full[t & 1]);
         }
       }
+      // and so are the products, before tensor memory is given back
+      mma_commit(&sh.drained);
+      mbar_wait_bounded(&sh.drained, 0, p.c.err, DERR_DRAIN_WAIT);
     }
     __syncwarp();
     cluster_ready();

@@ -105,6 +105,7 @@ struct Shared : Join<SPLIT> {
   static constexpr int NST = Shape<HD, SPLIT>::NST;
   uint64_t q_full, q_free, kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
   uint64_t unit_full[kUnits], unit_free[kUnits];
+  uint64_t drained;  // every MMA issued is over
   Unit unit[kUnits];
   uint32_t tmem;
   int bad_v[8];  // [unit & 7]: the last unit in which a non-finite V value was replaced
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_free, 1);
+    mbar_init(&sh.drained, 1);
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 1);
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one before have read theirs
       if (u.kb > u.ka) {
         if (loads > 0) ok = warp_wait(&sh.q_free, (loads - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
-        ++loads;
+        loads += ok;
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&sh.q_full, (u.n[0] > 0 ? S::kTile : 0) + (u.n[1] > 0 ? S::kTile : 0));
 #pragma unroll
@@ -263,9 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         id = next;
       }
     }
-    if (!ok)  // copies land before the CTA ends
-      for (int i = max(0, issued - S::NST); i < issued; ++i)
-        mbar_wait_bounded(&sh.kv_full[stage(i)], phase(i), p.c.err, DERR_DRAIN_WAIT);
+    // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
+    for (int i = max(0, issued - S::NST); i < issued; ++i)
+      mbar_wait_bounded(&sh.kv_full[stage(i)], phase(i), p.c.err, DERR_DRAIN_WAIT);
+    if (loads > 0) mbar_wait_bounded(&sh.q_full, (loads - 1) & 1, p.c.err, DERR_DRAIN_WAIT);
   } else if (warp == 9) {
     // One thread issues every MMA.  The tensor core takes an MMA from it when it
     // starts on it, so what the thread does between two products costs the
@@ -317,6 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       base += 2 * nk;
       loads += nk > 0;
     }
+    if (lane == 0) {  // and so are the products, before tensor memory is given back
+      mma_commit(&sh.drained);
+      mbar_wait_bounded(&sh.drained, 0, p.c.err, DERR_DRAIN_WAIT);
+    }
+    __syncwarp();
   } else if (warp == 10) {
     // Waits for V_j and K_{j + 1} on behalf of the MMA thread: P_t(j)'s barriers
     // count this warp's arrival too.  In tiles that are masked for some row, V

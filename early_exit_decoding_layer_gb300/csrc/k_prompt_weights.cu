@@ -56,6 +56,7 @@ struct Maps {
 
 struct Shared {
   uint64_t k_full, q_full[8], q_empty[8], s_full[kBuf], s_free[kBuf];
+  uint64_t drained[2];  // every MMA of an issuing thread is over
   uint32_t tmem;
   alignas(16) float lse[kGroups][2][kCols];  // by warpgroup, two tiles
   uint2 odd[kGroups][kCols / 32];            // its columns of infinite (x) and NaN (y) lse, a bit each
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&sh.k_full, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.drained[i], 1);
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], nh);  // a warpgroup per key tile
@@ -129,9 +131,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < S::H; ++h)
           tma_load_3d(q_s + st * S::kTile + h * S::kHalf, &maps.q, h * 64, g * G, sq.first + tile_row(j), &sh.q_full[st]);
       }
-      if (issued < nq)  // copies land before the CTA ends
-        for (int i = max(0, issued - S::NST); i < issued; ++i)
-          mbar_wait_bounded(&sh.q_full[i % S::NST], (i / S::NST) & 1, p.c.err, DERR_DRAIN_WAIT);
+      // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
+      if (nq > 0) mbar_wait_bounded(&sh.k_full, 0, p.c.err, DERR_DRAIN_WAIT);
+      for (int i = max(0, issued - S::NST); i < issued; ++i)
+        mbar_wait_bounded(&sh.q_full[i % S::NST], (i / S::NST) & 1, p.c.err, DERR_DRAIN_WAIT);
     }
     __syncwarp();
   } else if (warp > kTma) {
@@ -160,6 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&sh.s_full[b]);
         }
       }
+      // and so are the products, before tensor memory is given back
+      mma_commit(&sh.drained[t]);
+      mbar_wait_bounded(&sh.drained[t], 0, p.c.err, DERR_DRAIN_WAIT);
     }
     __syncwarp();
   } else {
