@@ -240,3 +240,60 @@ def test_attention_weights_queries_of_any_size(hq, hkv, hd, power):
         for a in range(hq):
             add[:, g[a]] += p[a]
         assert np.all(np.abs(h.gather(w, s) - h.W[s] - add) <= rel * add + 8 * U32 * (h.W[s] + add)), s
+
+
+# ------------------------------------------------ faulty lengths and block ids
+
+@pytest.mark.parametrize("bad", [0, 1])
+@pytest.mark.parametrize("what", ["block", "negative block", "long", "negative"])
+def test_faults_of_one_sequence_leave_the_other_alone(what, bad):
+    """With a fault in one sequence every operator reports it, and the other sequence's
+    results, its rows and the blocks of no sequence are those of a call without it.  Block
+    ids out of range are read as block 0, which here is the good sequence's."""
+    hq, hkv, hd = 4, 2, 64
+    c = Prompt(51, hq, hkv, hd, [20, 30], [20, 30])
+    h, good = c.h, 1 - bad
+    # block 0 is the good sequence's first
+    at = h.table[good, 0]
+    for x in (h.k, h.v, h.w):
+        x[[0, at]] = x[[at, 0]]
+    h.table[:] = np.where(h.table == 0, -1, np.where(h.table == at, 0, h.table))
+    h.table[h.table == -1] = at
+    d = c.args()
+    own = np.zeros((2, h.n_blocks), dtype=bool)
+    for s, n in enumerate(h.ctxs):
+        own[s, h.table[s, : (n + 15) // 16]] = True
+    rest = dev(~own[bad])   # the good sequence's blocks and those of none
+    table, ctx = d["table"].clone(), d["ctx"].clone()
+    if "block" in what:
+        table[bad, 1] = -3 if "negative" in what else h.n_blocks
+    else:
+        # whatever is read lies in the cache, and whatever is written in the bad sequence's blocks
+        table[bad] = int(h.table[bad, 0])
+        ctx[bad] = -5 if what == "negative" else 1 << 30
+    decode_q = dev(h.rng.standard_normal((2, hq * hd)).astype(np.float32))
+    _, lse = ee.prompt_attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+
+    def calls(table, ctx):
+        err = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(4)]
+        res = []
+        o, l = ee.prompt_attention(d["q"], d["k"], d["v"], table, d["cu"], ctx, *c.shape, err=err[0])
+        rows = c.seq_rows(good)
+        res += [o[rows], l[:, rows]]
+        w = dev(h.w)
+        ee.prompt_weights(d["q"], d["k"], table, d["cu"], ctx, lse, w, *c.shape, err=err[1])
+        res.append(w[rest])
+        w = dev(h.w)
+        x = ee.attention_weights(decode_q, d["k"], d["v"], table, ctx - 1, w, *c.shape, err=err[2])
+        res += [x[good], w[rest]]
+        k, v, w = d["k"].clone(), d["v"].clone(), dev(h.w)
+        kept, new = ee.evict(k, v, w, table, ctx, 7, 2, c.max_ctx, err=err[3])
+        res += [kept[good], new[good], k[rest], v[rest], w[rest]]
+        return [e.item() for e in err], res
+
+    no_err, want = calls(d["table"], d["ctx"])
+    assert no_err == [0] * 4
+    errs, got = calls(table, ctx)
+    assert errs == [EE_DERR_BLOCK if "block" in what else EE_DERR_LENGTH] * 4
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(bits(a), bits(b)), i
