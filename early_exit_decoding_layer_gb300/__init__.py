@@ -540,8 +540,12 @@ def _cache_ops():
 
 
 def _on_stream(stream, fn, *args):
-    """fn(*args) with `stream` current, so that what it allocates belongs to it."""
+    """fn(*args) with `stream` current, so that what it allocates belongs to it.  The work
+    goes to the current stream of the tensors' device, so the stream has to be of that one."""
     import torch
+    dev = getattr(args[0], "device", None)
+    if isinstance(dev, torch.device) and dev.type == "cuda" and dev != stream.device:
+        raise EEError(1, "%s: the stream is of %s, the tensors are on %s" % (fn.__name__, stream.device, dev))
     with torch.cuda.stream(stream):
         return fn(*args)
 

@@ -297,3 +297,27 @@ def test_faults_of_one_sequence_leave_the_other_alone(what, bad):
     assert errs == [EE_DERR_BLOCK if "block" in what else EE_DERR_LENGTH] * 4
     for i, (a, b) in enumerate(zip(got, want)):
         assert torch.equal(bits(a), bits(b)), i
+
+
+def test_stream_argument():
+    """Each operator on a stream that is given: the results of the current one, on that stream."""
+    c = Prompt(101, 8, 2, 64, [70, 33], [70, 90])
+    d = c.args()
+    qd = dev(c.h.rng.standard_normal((2, 512)).astype(np.float32))
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (None, side):
+        k, v, w = d["k"].clone(), d["v"].clone(), torch.zeros(c.h.n_blocks, 2, 16, device="cuda")
+        torch.cuda.synchronize()
+        o, lse = ee.prompt_attention(d["q"], k, v, d["table"], d["cu"], d["ctx"], *c.shape, stream=stream)
+        ee.prompt_weights(d["q"], k, d["table"], d["cu"], d["ctx"], lse, w, *c.shape, stream=stream)
+        # behind the others on the same stream
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            pos = d["ctx"] - 1
+        x = ee.attention_weights(qd, k, v, d["table"], pos, w, *c.shape, stream=stream)
+        kept, new = ee.evict(k, v, w, d["table"], d["ctx"], 33, 5, c.max_ctx, stream=stream)
+        (stream or torch.cuda.current_stream()).synchronize()
+        got.append([o, lse, x, kept, new, k, v, w])
+    for a, b in zip(*got):
+        assert torch.equal(bits(a), bits(b))
+    assert torch.cuda.current_stream() != side
