@@ -38,7 +38,7 @@
 //
 // Bound: bytes.  32 sequences of 8192 tokens, 32/8 heads, hd 128: 5.5 TB/s (0.82 of
 // the measured copy rate); 257 to 2176 tokens: 4.5 TB/s, where 152 SMs share 256 units
-// unevenly and 5.5 us of launch, first loads and last join show; one of 2113: 8.5 us.
+// unevenly and 5.5 us of launch, first loads and last join show; one of 2113: 8.3 us.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>

@@ -16,6 +16,10 @@
 // Each tile's 128 terms are summed in four chains, and the tiles' sums with
 // compensation, so that the error does not grow with the prompt's length.
 //
+// Bound: 8 sequences of 4096 tokens, 64/8 heads, hd 128: 938 us, 1170 TFLOP/s.  Nothing
+// is full (tensor pipe 53%, exponentials and issue slots about the same): with one S
+// buffer each, a warpgroup's exponentials and its next product take turns.
+//
 // Few keys: the query tiles are dealt to the CTAs of a cluster, whose
 // sums are joined through distributed shared memory in rank order.  A token's
 // weight is added once per sequence and call (red.add: a block that several
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // until the next tile, when the load is over.  A column whose lse is infinite adds
     // nothing, whatever its scores are, and one with a NaN lse is NaN only for the keys that
     // it sees.  Neither comes out of c S - f lse, so a vote with the barrier that is there finds
-    // tiles with such a column, and their scores are set.
+    // tiles with such a column, and their scores are set (918 -> 938 us for 8 x 4096).
     auto load_lse = [&](int j) {
       const int row = j < nq ? tile_row(j) + r / G : sq.n;
       return row < sq.n ? p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row] : -INFINITY;
@@ -303,8 +307,8 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const Exponent ex = make_exponent(HD);
   // Two key tiles per CTA, or one as long as there is an SM for each; clusters where
-  // SMs are left.  512 tokens of 32/8 heads, hd 64: 7.8 us with one tile, 9.4 with
-  // two; 8 sequences of 4096 with 64/8 heads, hd 128: 1154 with one, 914 with two.
+  // SMs are left.  512 tokens of 32/8 heads, hd 64: 8.0 us with one tile, 9.5 with
+  // two; 8 sequences of 4096 with 64/8 heads, hd 128: 1268 with one, 938 with two.
   auto units_of = [&](int tiles) {
     return (int64_t)((p.c.max_ctx + 128 * tiles - 1) / (128 * tiles)) * p.n_seqs * p.c.n_kv_heads;
   };

@@ -432,6 +432,8 @@ ee_status ee_op_attention_noalloc(int32_t B, int32_t n_heads, int32_t n_kv_heads
  *    tokens that exist are read.  head_dim 64 or 128, Hq / Hkv in {1, 2, 4, 8},
  *    at most EE_MAX_BATCH sequences, max_ctx <= 16384.  q, o, the caches and
  *    the weights are 16-byte aligned, the other arrays by their element's size.
+ *  - max_ctx bounds every length, and the launch is laid out for it: a bound near
+ *    the lengths is faster than the capacity.
  *  - They need no scratch, allocate nothing and keep nothing between calls: calls
  *    on different streams, and captured ones, share no memory but the
  *    caller's.
@@ -492,7 +494,9 @@ ee_status ee_op_prompt_weights(int32_t n_seqs, int32_t total_q, int32_t n_heads,
  *   weights[block(t), g, t % 16] += sum over the query heads of kv head g of
  *   softmax_t(q_h . k_t / sqrt(hd)),  t <= pos[s].
  * pos[s] = -1 is an empty sequence: o = 0, no weight is added.  Nor is any by a
- * head whose scores are all -INF. */
+ * head whose scores are all -INF.  Products, sums and statistics are fp32;
+ * queries and probabilities have 22 bits, down to 2^-34 of a head's largest
+ * query and 2^-32 of its largest probability. */
 ee_status ee_op_attention_weights(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                   int32_t max_ctx, const float *q, const uint16_t *kcache,
                                   const uint16_t *vcache, int32_t n_blocks, const int32_t *block_table,
