@@ -443,11 +443,12 @@ ee_status ee_op_attention_noalloc(int32_t B, int32_t n_heads, int32_t n_kv_heads
  *    [0, min(max_ctx, 16 * bt_stride)], a block id outside [0, n_blocks) is read
  *    as some block and not written -- but the results of that sequence mean
  *    nothing.  *err_flag is never cleared.
- *  - An infinity or NaN in q or K goes into the scores of its rows or token and on
- *    from there as the formulas have it.  One in V makes its own component of every
- *    row that sees the token infinite or NaN, however small the probability; a
- *    row that does not see it is not touched, and slots behind a sequence's last
- *    token may hold anything.
+ *  - A token whose score in a row is -INF weighs nothing there.  A score of +INF or
+ *    NaN makes the row's o and lse, and the weights of the tokens that it sees, NaN.
+ *    An infinity or NaN in V makes its own component of every row that sees the
+ *    token infinite or NaN, however small the probability.  A row that does not see
+ *    a token is what it is without it, to rounding, and slots behind a sequence's
+ *    last token may hold anything.
  *  - A block may stand in the tables of several sequences (a shared prefix) where
  *    a call only reads it.  Weights of a shared block get every sequence's part;
  *    the order of these additions, and with it the last bit, is not

@@ -321,3 +321,58 @@ def test_stream_argument():
     for a, b in zip(*got):
         assert torch.equal(bits(a), bits(b))
     assert torch.cuda.current_stream() != side
+
+
+@pytest.mark.parametrize("hq,hkv,hd,ctx", [(8, 2, 64, 200), (8, 8, 128, 1500)])
+def test_infinite_scores(hq, hkv, hd, ctx):
+    """A score of -infinity weighs nothing, in prompts and decode steps alike; one of +infinity
+    makes the rows that see it NaN, with the weights of all tokens that they see."""
+    n, G, t = 60, hq // hkv, ctx - 30
+    c = Prompt(hq + ctx, hq, hkv, hd, [n], [ctx])
+    c.q[:, :, 3] = np.abs(c.q[:, :, 3]) + 0.5
+    qd = c.q[-1:].astype(np.float32)
+    d, h, off = c.args(), c.h, ctx - n
+    at = h.table[0, t // 16], hkv - 1, t % 16, 3
+
+    def call(x):
+        k = h.k.copy()
+        k[at] = x
+        k = dev(k)
+        w, wd = (torch.zeros(h.n_blocks, hkv, 16, device="cuda") for _ in range(2))
+        o, lse = ee.prompt_attention(d["q"], k, d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+        ee.prompt_weights(d["q"], k, d["table"], d["cu"], d["ctx"], lse, w, *c.shape)
+        od = ee.attention_weights(dev(qd.reshape(1, -1)), k, d["v"], d["table"], d["ctx"] - 1, wd, *c.shape)
+        w, wd = (h.gather(y.cpu().numpy(), 0).astype(np.float64) for y in (w, wd))
+        return o.cpu().numpy().astype(np.float64).reshape(n, hq, hd), lse.cpu().numpy(), w, od.cpu().numpy().reshape(hq, hd), wd
+
+    o, lse, w, od, wd = call(-np.inf)
+    K, V = h.K[0].astype(np.float64), h.V[0].astype(np.float64)
+    # a score's error twice, the exponential's argument, sums of ctx and n G terms, the division:
+    # as in prompt_reference, with the token's key finite
+    q64 = c.q.astype(np.float64)
+    z = max(np.abs(np.einsum("nhd,thd->nht", q64, K[:, np.arange(hq) // G])).max() / math.sqrt(hd), 1.0)
+    rel = 2 * max(score_error(q, K).max() for q in q64) + (ctx + n * G + 40) * U32 + 8 * U32 * z
+    K[t, hkv - 1, 3] = -np.inf
+    ro, rl, rw = oracle.prompt_attention(q64, K, V)
+    # probabilities and result in fp16: half a step each of at most the largest value
+    big = np.abs(V).max()
+    bo = (2 * 2.0 ** -11 + rel) * big + 2.0 ** -24 * ctx
+    assert np.all(np.abs(o - ro) <= bo)
+    assert np.all(np.abs(lse - rl) <= rel)
+    assert np.all(np.abs(w - rw) <= rel * rw) and np.all(w[t, hkv - 1] == 0)
+    rod, _, rw = oracle.prompt_attention(qd.astype(np.float64), K, V)
+    assert np.all(np.abs(od - rod[0]) <= rel * big) and np.all(np.abs(wd - rw) <= rel * rw) and wd[t, hkv - 1] == 0
+
+    _, _, w0, od0, wd0 = call(h.k[at])
+    o, lse, w, od, wd = call(np.inf)
+    g = slice((hkv - 1) * G, hq)   # the heads of the token's kv head
+    assert np.isnan(o[t - off:, g]).all() and np.isnan(lse[g, t - off:]).all() and np.isnan(od[g]).all()
+    assert np.isnan(w[:, hkv - 1]).all() and np.isnan(wd[:, hkv - 1]).all()   # the last row sees them all
+    # Rows before the token do not see it and are what they were, to rounding: a warp goes over
+    # to its rows' new maxima for all of them when one's has grown, and an infinite one has.  A
+    # probability is off by half a step of fp16 at most whichever maximum it is relative to, so
+    # the bounds are the same.
+    assert np.all(np.abs(o[: t - off] - ro[: t - off]) <= bo) and np.all(np.abs(lse[:, : t - off] - rl[:, : t - off]) <= rel)
+    assert np.array_equal(od[: g.start], od0[: g.start])
+    for got, before in ((w, w0), (wd, wd0)):
+        assert np.array_equal(got[:, : hkv - 1], before[:, : hkv - 1])
