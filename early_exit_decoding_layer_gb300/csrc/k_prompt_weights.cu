@@ -16,7 +16,7 @@
 // Each tile's 128 terms are summed in four chains, and the tiles' sums with
 // compensation, so that the error does not grow with the prompt's length.
 //
-// Bound: 8 sequences of 4096 tokens, 64/8 heads, hd 128: 938 us, 1170 TFLOP/s.  Nothing
+// Bound: 8 sequences of 4096 tokens, 64/8 heads, hd 128: 908 us, 1210 TFLOP/s.  Nothing
 // is full (tensor pipe 53%, exponentials and issue slots about the same): with one S
 // buffer each, a warpgroup's exponentials and its next product take turns.
 //
@@ -176,14 +176,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warpgroup t: key tile t & 1, query tiles j = t / 2, t / 2 + 2, ..
     const int t = warp >> 2, r = tid & 127, keys = key0 + (t & 1) * 128, key = keys + r;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    // Column r of a tile: its lse, -inf for a row of nobody.  What becomes of it waits
+    // Column r of a tile: its lse (a row of nobody is masked).  What becomes of it waits
     // until the next tile, when the load is over.  A column whose lse is infinite adds
     // nothing, whatever its scores are, and one with a NaN lse is NaN only for the keys that
     // it sees.  Neither comes out of c S - f lse, so a vote with the barrier that is there finds
-    // tiles with such a column, and their scores are set (918 -> 938 us for 8 x 4096).
+    // tiles with such a column, which go their own way (with its conditions in the other
+    // tiles' loop 8 x 4096 tokens took 938 us instead of 908).
     auto load_lse = [&](int j) {
       const int row = j < nq ? tile_row(j) + r / G : sq.n;
-      return row < sq.n ? p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row] : -INFINITY;
+      return row < sq.n ? p.lse_in[(size_t)(g * G + r % G) * p.total_q + sq.first + row] : 0.0f;
     };
     float sum = 0.0f, comp = 0.0f, next = load_lse(t >> 1);
     const uint64_t c2 = pack2(ex.c, ex.c);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = t >> 1; j < ((t & 1) < nh ? nq : 0); j += 2) {
       float* ls = sh.lse[t][(j >> 1) & 1];
       const float now = next;
-      ls[r] = isinf(now) ? -INFINITY : -fmaf(now, ex.f_hi, now * ex.f_lo);  // in the exponent's unit
+      ls[r] = -fmaf(now, ex.f_hi, now * ex.f_lo);  // in the exponent's unit
       next = load_lse(j + 2);
       // the other buffer was read two tiles ago, before the barrier of the last one
       int odd = !(fabsf(now) < INFINITY);
@@ -215,41 +216,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (r == 0) mbar_arrive(&sh.q_empty[j % S::NST]);  // the product has read its queries
       const bool masked = off + row0 < keys + 127 || row0 + kPos > sq.n;
       const int lo = (key - off - row0) * G, hi = (sq.n - row0) * G;
-      // 32 columns at a time, the next ones on their way
       uint32_t v[2][32];
       uint64_t acc[2] = {0, 0};
-      tmem_ld32(at, v[0]);
-#pragma unroll
-      for (int k = 0; k < kCols / 32; ++k) {
-        tmem_wait_ld();
-        tmem_pin<32>(v[k & 1]);
-        if (k < kCols / 32 - 1) {
-          tmem_ld32(at + 32 * (k + 1), v[(k + 1) & 1]);
-        } else {
-          tc_fence_before();
-          mbar_arrive(&sh.s_free[t]);
-        }
-        uint32_t* x = v[k & 1];
-        if (odd) {
+      if (odd) {
+        // as below, one piece after another, with the scores of the odd columns set
+#pragma unroll 1
+        for (int k = 0; k < kCols / 32; ++k) {
+          tmem_ld32(at + 32 * k, v[0]);
+          tmem_wait_ld();
+          tmem_pin<32>(v[0]);
           const uint2 m = sh.odd[t][k];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (m.x >> i & 1) x[i] = 0xff800000u;
-            if (m.y >> i & 1) x[i] = 0x7fffffffu;
+          for (int i = 0; i < 32; i += 4) {
+            float e[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int n = 32 * k + i + w;
+              float x = __uint_as_float(v[0][i + w]);
+              if (m.y >> (i + w) & 1) x = NAN;
+              if (n < lo || n >= hi || (m.x >> (i + w) & 1)) x = -INFINITY;
+              e[w] = ex2(fmaf(x, ex.c, ls[n]));
+            }
+            acc[0] = add2(acc[0], pack2(e[0], e[1]));
+            acc[1] = add2(acc[1], pack2(e[2], e[3]));
           }
         }
-        if (masked) {  // rows before the key, rows of no one: -inf
+        tc_fence_before();
+        mbar_arrive(&sh.s_free[t]);
+      } else {
+        // 32 columns at a time, the next ones on their way
+        tmem_ld32(at, v[0]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * k + i < lo || 32 * k + i >= hi) x[i] = 0xff800000u;
-        }
+        for (int k = 0; k < kCols / 32; ++k) {
+          tmem_wait_ld();
+          tmem_pin<32>(v[k & 1]);
+          if (k < kCols / 32 - 1) {
+            tmem_ld32(at + 32 * (k + 1), v[(k + 1) & 1]);
+          } else {
+            tc_fence_before();
+            mbar_arrive(&sh.s_free[t]);
+          }
+          uint32_t* x = v[k & 1];
+          if (masked) {  // rows before the key, rows of no one: -inf
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * k + i);
-          const float2 y = unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, pack2(l4.x, l4.y)));
-          const float2 z = unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), c2, pack2(l4.z, l4.w)));
-          acc[0] = add2(acc[0], pack2(ex2(y.x), ex2(y.y)));
-          acc[1] = add2(acc[1], pack2(ex2(z.x), ex2(z.y)));
+            for (int i = 0; i < 32; ++i)
+              if (32 * k + i < lo || 32 * k + i >= hi) x[i] = 0xff800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * k + i);
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, pack2(l4.x, l4.y)));
+            const float2 z = unpack2(fma2(pack2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), c2, pack2(l4.z, l4.w)));
+            acc[0] = add2(acc[0], pack2(ex2(y.x), ex2(y.y)));
+            acc[1] = add2(acc[1], pack2(ex2(z.x), ex2(z.y)));
+          }
         }
       }
       const float2 a = unpack2(add2(acc[0], acc[1]));
@@ -307,8 +327,8 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const Exponent ex = make_exponent(HD);
   // Two key tiles per CTA, or one as long as there is an SM for each; clusters where
-  // SMs are left.  512 tokens of 32/8 heads, hd 64: 8.0 us with one tile, 9.5 with
-  // two; 8 sequences of 4096 with 64/8 heads, hd 128: 1268 with one, 938 with two.
+  // SMs are left.  512 tokens of 32/8 heads, hd 64: 7.8 us with one tile, 9.3 with
+  // two; 8 sequences of 4096 with 64/8 heads, hd 128: 1135 with one, 908 with two.
   auto units_of = [&](int tiles) {
     return (int64_t)((p.c.max_ctx + 128 * tiles - 1) / (128 * tiles)) * p.n_seqs * p.c.n_kv_heads;
   };
