@@ -17,7 +17,7 @@
 // compensation, so that the error does not grow with the prompt's length.
 //
 // Bound: 8 sequences of 4096 tokens, 64/8 heads, hd 128: 908 us, 1210 TFLOP/s.  Nothing
-// is full (tensor pipe 53%, exponentials and issue slots about the same): with one S
+// is full (tensor pipe 55%, exponentials 56%, issue slots 53%): with one S
 // buffer each, a warpgroup's exponentials and its next product take turns.
 //
 // Few keys: the query tiles are dealt to the CTAs of a cluster, whose
