@@ -85,6 +85,13 @@ EE_DEV float log_sum(float m, float l, const Exponent& ex) {
   return l == 0.0f ? -INFINITY : fmaf(m, ex.unit_hi, fmaf(m, ex.unit_lo, logf(l)));
 }
 
+// o is a mean of fp16 values and no larger than they are.  P's rounding may take it past the
+// largest one by up to 2^-11 of it, which would be infinite in fp16.
+constexpr float kMostHalf = 65504.0f;
+EE_DEV float within_half(float y) {
+  return fabsf(y) > kMostHalf && fabsf(y) < INFINITY ? copysignf(kMostHalf, y) : y;
+}
+
 // The work of one CTA on one (tile of rows, kv head): key tiles [ka, kb) of 128,
 // of which row tile t takes the first n[t]; those from jm[t] on are not seen whole by
 // every row of it.
@@ -515,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint16_t* row_b = (odd ? orow : other) + (odd ? 16 : 0);
         const bool a_valid = odd ? other_valid : valid, b_valid = odd ? valid : other_valid;
         const uint64_t il2 = pack2(il, il);
+        float most = 0.0f;
 #pragma unroll 1
         for (int i = 0; i < HD; i += 32) {
           uint32_t o[32], h[16], x[8];
@@ -524,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float2 y = unpack2(mul2(pack2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), il2));
+            most = max3(most, fabsf(y.x), fabsf(y.y));
             const __half2 z = __floats2half2_rn(y.x, y.y);
             h[k] = n > 0 ? *reinterpret_cast<const uint32_t*>(&z) : 0;
           }
@@ -547,6 +556,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        if (__any_sync(0xffffffffu, n > 0 && most > kMostHalf)) {  // rare, as below
+#pragma unroll 1
+          for (int i = 0; i < HD; i += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_at + i, o);
+            tmem_wait_ld();
+            tmem_pin<16>(o);
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+              const float y = __uint_as_float(o[w]) * il, z = within_half(y);
+              if (valid && z != y) orow[i + w] = float_to_half_bits(z);  // (a NaN differs too, and stays)
+            }
+          }
+        }
       }
       if (bad && ok && valid) {
         // the values taken out of V, for the rows that see them (rare: kept out of the
@@ -638,7 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int row = u.tl.i0 + r / G, head = u.g * G + r % G;
-      const __half2 h0 = __floats2half2_rn(o.x, o.y), h1 = __floats2half2_rn(o.z, o.w);
+      const __half2 h0 = __floats2half2_rn(within_half(o.x), within_half(o.y)),
+                    h1 = __floats2half2_rn(within_half(o.z), within_half(o.w));
       *reinterpret_cast<uint2*>(p.o + (int64_t)(u.tl.sq.first + row) * p.o_stride + head * HD + col) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
     }

@@ -376,3 +376,36 @@ def test_infinite_scores(hq, hkv, hd, ctx):
     assert np.array_equal(od[: g.start], od0[: g.start])
     for got, before in ((w, w0), (wd, wd0)):
         assert np.array_equal(got[:, : hkv - 1], before[:, : hkv - 1])
+
+
+@pytest.mark.parametrize("past", [0, 1800])
+@pytest.mark.parametrize("hq,hkv,hd", [(4, 2, 64), (8, 1, 128)])
+def test_prompt_attention_values_at_the_end_of_fp16(hq, hkv, hd, past):
+    """o is a mean of values, so it is no larger than the largest of them, 65504; where it is
+    rounded up on the way it does not become infinite.  Token 0 is ahead of all others so far
+    that their exponentials are 0.5 + 0.53 * 2^-11, which fp16 rounds up by 0.47 * 2^-11."""
+    n = 99
+    c = Prompt(7, hq, hkv, hd, [n], [n + past])
+    x = 0.5 + 0.53 * 2.0 ** -11
+    ahead = -math.log(x) * math.sqrt(hd)
+    c.q[:] = 0
+    c.q[..., :2] = 1
+    first = np.float16(ahead)
+    h = c.h
+    for t in range(n + past):
+        h.K[0][t] = 0
+        h.V[0][t] = 65504
+        h.V[0][t, :, 1] = -65504
+    h.K[0][0, :, 0], h.K[0][0, :, 1] = first, np.float16(ahead - float(first))
+    for t in range(n + past):
+        h.k[h.table[0, t // 16], :, t % 16], h.v[h.table[0, t // 16], :, t % 16] = h.K[0][t], h.V[0][t]
+    # the score's error, 2^-22 of it and of the residual's rounding, leaves the rounding as it is
+    z = (float(first) + float(np.float16(ahead - float(first)))) / math.sqrt(hd)
+    assert np.float16(math.exp(-z * (1 + 2.0 ** -20))) == np.float16(math.exp(-z * (1 - 2.0 ** -20))) == np.float16(0.5 + 2.0 ** -11)
+    d = c.args()
+    o, _ = ee.prompt_attention(d["q"], d["k"], d["v"], d["table"], d["cu"], d["ctx"], *c.shape)
+    o = o.cpu().numpy().astype(np.float64).reshape(n, hq, hd)
+    want = np.full(hd, 65504.0)
+    want[1] = -65504.0
+    # half a step of fp16 for the probabilities, half a step for o; no value beyond the largest
+    assert np.all(np.abs(o) <= 65504) and np.all(np.abs(o - want) <= 2 * 2.0 ** -11 * 65504)
