@@ -38,7 +38,9 @@ EXPORTS = (
     "ee_op_vocab_head", "ee_step_io", "ee_set_profile", "ee_profile_read", "ee_last_step_ms",
     "ee_op_attention_noalloc", "ee_set_exit_criterion", "ee_set_token_source",
     "ee_set_prefill_exit", "ee_prefill_exit_layers", "ee_op_prompt_attention", "ee_op_prompt_weights",
-    "ee_op_attention_weights", "ee_op_evict",
+    "ee_op_attention_weights", "ee_op_evict", "ee_op_quantize_cache", "ee_op_dequantize_cache",
+    "ee_quantized_attention_scratch_bytes", "ee_op_quantized_attention", "ee_shared_attention_scratch_bytes",
+    "ee_op_shared_attention",
 )
 
 LISTS = ("both", "full")  # EE_LISTS_*
@@ -142,6 +144,16 @@ def load_library(path: str = LIB_PATH):
                                           c_vp, c_vp, c_vp]),
         "ee_op_evict": (i32, [i32, i32, i32, i32, i32, i32, c_vp, c_vp, c_vp, i32, c_vp, i32, c_vp, i32, c_vp,
                               c_vp, c_vp, c_vp, c_vp]),
+        "ee_op_quantize_cache": (i32, [i32, i32, i32, i32, i32, i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, i32, c_vp,
+                                       i32, c_vp, c_vp, c_vp, c_vp]),
+        "ee_op_dequantize_cache": (i32, [i32, i32, i32, i32, c_vp, c_vp, i32, c_vp, i32, c_vp, c_vp, c_vp, i32, c_vp,
+                                         i32, c_vp, c_vp]),
+        "ee_quantized_attention_scratch_bytes": (c_sz, [i32, i32, i32, i32, i32]),
+        "ee_op_quantized_attention": (i32, [i32, i32, i32, i32, i32, c_vp, c_i64, c_vp, c_vp, i32, c_vp, i32, c_vp,
+                                            c_vp, c_i64, c_vp, c_vp, c_vp]),
+        "ee_shared_attention_scratch_bytes": (c_sz, [i32, i32, i32, i32, i32, i32]),
+        "ee_op_shared_attention": (i32, [i32, i32, i32, i32, i32, i32, c_vp, c_i64, c_vp, c_vp, i32, c_vp, i32, c_vp,
+                                         c_vp, c_i64, c_vp, c_vp, c_vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -596,3 +608,49 @@ def evict(kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_
     if stream is not None:
         return _on_stream(stream, evict, kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_table, err)
     return _cache_ops().evict(kcache, vcache, weights, block_table, ctx, keep, recent, max_ctx, dst_table, err)
+
+
+# ------------------------------------------------- caches in eight bits, shared prefixes
+
+def quantize_cache(k, v, codes, exponents, block_table, cu, ctx, max_ctx, err=None, stream=None):
+    """Writes packed K and V rows of new tokens into the eight-bit cache
+    (ee_op_quantize_cache).  k, v [T, Hkv*hd] fp16 or fp32 (rows may lie apart by whole
+    16 bytes); codes [blocks, Hkv, 2, 16, hd] uint8 or float8_e4m3fn, exponents
+    [blocks, Hkv, 2, 16] int8; block_table [S, W], cu [S+1], ctx [S] int32.  Returns
+    (codes, exponents)."""
+    if stream is not None:
+        return _on_stream(stream, quantize_cache, k, v, codes, exponents, block_table, cu, ctx, max_ctx, err)
+    return _cache_ops().quantize_cache(k, v, codes, exponents, block_table, cu, ctx, max_ctx, err)
+
+
+def dequantize_cache(codes, exponents, block_table, ctx, kcache, vcache, max_ctx, dst_table=None, err=None, stream=None):
+    """Reads every sequence's tokens back into the fp16 cache [blocks, Hkv, 16, hd], at
+    dst_table's blocks or block_table's own (ee_op_dequantize_cache).  Returns (kcache, vcache)."""
+    if stream is not None:
+        return _on_stream(stream, dequantize_cache, codes, exponents, block_table, ctx, kcache, vcache, max_ctx, dst_table, err)
+    return _cache_ops().dequantize_cache(codes, exponents, block_table, ctx, kcache, vcache, max_ctx, dst_table, err)
+
+
+def quantized_attention(q, codes, exponents, block_table, pos, n_heads, n_kv_heads, head_dim, max_ctx, out=None, err=None,
+                        stream=None):
+    """Decode attention over the eight-bit cache (ee_op_quantized_attention).  q [B, Hq*hd]
+    fp16 (rows may lie apart by a multiple of 8 values), pos [B] int32 (-1: an empty
+    sequence).  Returns o [B, Hq*hd] fp16.  Its scratch is allocated per call, on the call's stream."""
+    if stream is not None:
+        return _on_stream(stream, quantized_attention, q, codes, exponents, block_table, pos, n_heads, n_kv_heads, head_dim,
+                          max_ctx, out, err)
+    return _cache_ops().quantized_attention(q, codes, exponents, block_table, pos, n_heads, n_kv_heads, head_dim, max_ctx, out,
+                                            err)
+
+
+def shared_attention(q, kcache, vcache, block_table, pos, prefix, n_heads, n_kv_heads, head_dim, max_ctx, out=None, err=None,
+                     stream=None):
+    """Decode attention of a batch whose first `prefix` tokens are the same: their
+    blocks, which block_table's first row names, are read once (ee_op_shared_attention).
+    q [B, Hq*hd] fp16 (rows may lie apart by a multiple of 8 values), caches [blocks, Hkv,
+    16, hd] fp16, pos [B] int32 (-1: an empty sequence).  Returns o [B, Hq*hd] fp16."""
+    if stream is not None:
+        return _on_stream(stream, shared_attention, q, kcache, vcache, block_table, pos, prefix, n_heads, n_kv_heads, head_dim,
+                          max_ctx, out, err)
+    return _cache_ops().shared_attention(q, kcache, vcache, block_table, pos, prefix, n_heads, n_kv_heads, head_dim, max_ctx,
+                                         out, err)

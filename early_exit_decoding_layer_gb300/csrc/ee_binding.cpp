@@ -29,18 +29,21 @@ struct Refused {
 };
 struct PythonError {};  // a Python error is set
 
-// Element types by kind: fp16 (or its bits in 16-bit integers), fp32, int32.
-enum Kind { kHalf, kF32, kI32 };
+// Element types by kind: fp16 (or its bits in 16-bit integers), fp32, int32, e4m3 (or its
+// bits), int8.
+enum Kind { kHalf, kF32, kI32, kCode, kI8 };
 
 bool is_kind(const at::Tensor& t, Kind k) {
   const auto s = t.scalar_type();
   if (k == kF32) return s == c10::ScalarType::Float;
   if (k == kI32) return s == c10::ScalarType::Int;
+  if (k == kCode) return s == c10::ScalarType::Byte || s == c10::ScalarType::Float8_e4m3fn;
+  if (k == kI8) return s == c10::ScalarType::Char;
   return s == c10::ScalarType::Half || s == c10::ScalarType::Short || s == c10::ScalarType::UInt16;
 }
 
 [[noreturn]] void refuse(const char* name, const at::Tensor& t, Kind k, c10::IntArrayRef shape, int dev, const char* how) {
-  static const char* const kinds[] = {"fp16", "fp32", "int32"};
+  static const char* const kinds[] = {"fp16", "fp32", "int32", "e4m3 or uint8", "int8"};
   std::ostringstream s;
   s << name << " has to be a " << how << " " << kinds[k] << " tensor of shape " << shape << " on cuda:" << dev << ", not "
     << t.scalar_type() << " " << t.sizes() << ", strides " << t.strides() << " on " << t.device();
@@ -69,11 +72,11 @@ void* address(const at::Tensor& t, const char* name, int dev, Kind k, c10::IntAr
 }
 
 // Rows that may lie apart, their values side by side.
-void* rows(const at::Tensor& t, const char* name, int dev, int64_t n, int64_t width, int64_t* stride) {
+void* rows(const at::Tensor& t, const char* name, int dev, int64_t n, int64_t width, int64_t* stride, Kind k = kHalf) {
   *stride = width;
-  const bool same = t.is_cuda() && t.get_device() == dev && is_kind(t, kHalf) && t.sizes() == c10::IntArrayRef({n, width});
+  const bool same = t.is_cuda() && t.get_device() == dev && is_kind(t, k) && t.sizes() == c10::IntArrayRef({n, width});
   if (same && !t.is_contiguous()) *stride = n > 1 ? t.stride(0) : width;
-  if (!same || (width > 1 && t.stride(1) != 1) || *stride < width) refuse(name, t, kHalf, {n, width}, dev, "row-wise contiguous");
+  if (!same || (width > 1 && t.stride(1) != 1) || *stride < width) refuse(name, t, k, {n, width}, dev, "row-wise contiguous");
   return t.data_ptr();
 }
 
@@ -276,11 +279,144 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (k, v, codes, exponents, block_table, cu, ctx, max_ctx, err)
+PyObject* quantize_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  static const char* const what = "ee_op_quantize_cache";
+  return guarded(what, [&]() -> PyObject* {
+    count(n, 9);
+    const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &codes = tensor(a[2], "codes"),
+                     &exps = tensor(a[3], "exponents"), &table = tensor(a[4], "block_table"), &cu = tensor(a[5], "cu"),
+                     &ctx = tensor(a[6], "ctx");
+    const int dev = device_of(codes, "codes");
+    const int32_t max_ctx = integer(a[7], "max_ctx");
+    const int64_t nb = size(codes, 0, 5, "codes"), hkv = codes.size(1), hd = codes.size(4), T = size(k, 0, 2, "k"),
+                  S = size(ctx, 0, 1, "ctx"), W = size(table, 1, 2, "block_table");
+    const Kind kind = is_kind(k, kF32) ? kF32 : kHalf;
+    int64_t ks, vs;
+    const void* kp = rows(k, "k", dev, T, hkv * hd, &ks, kind);
+    const void* vp = rows(v, "v", dev, T, hkv * hd, &vs, kind);
+    void* cp = address(codes, "codes", dev, kCode, {nb, hkv, 2, 16, hd});
+    void* xp = address(exps, "exponents", dev, kI8, {nb, hkv, 2, 16});
+    const void* tp = address(table, "block_table", dev, kI32, {S, W});
+    const void* up = address(cu, "cu", dev, kI32, {S + 1});
+    const void* lp = address(ctx, "ctx", dev, kI32, {S});
+    int32_t* ep = error_word(a[8], dev);
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    check(what, ee_op_quantize_cache(size32(S, "ctx"), size32(T, "k"), size32(hkv, "codes"), size32(hd, "codes"), max_ctx,
+                                     kind == kF32 ? EE_ROWS_F32 : EE_ROWS_F16, kp, ks, vp, vs, (uint8_t*)cp, (int8_t*)xp,
+                                     size32(nb, "codes"), (const int32_t*)tp, size32(W, "block_table"), (const int32_t*)up,
+                                     (const int32_t*)lp, ep, stream_of(dev)));
+    return PyTuple_Pack(2, a[2], a[3]);
+  });
+}
+
+// (codes, exponents, block_table, ctx, kcache, vcache, max_ctx, dst_table, err)
+PyObject* dequantize_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  static const char* const what = "ee_op_dequantize_cache";
+  return guarded(what, [&]() -> PyObject* {
+    count(n, 9);
+    const at::Tensor &codes = tensor(a[0], "codes"), &exps = tensor(a[1], "exponents"), &table = tensor(a[2], "block_table"),
+                     &ctx = tensor(a[3], "ctx"), &k = tensor(a[4], "kcache"), &v = tensor(a[5], "vcache");
+    const int dev = device_of(codes, "codes");
+    const int32_t max_ctx = integer(a[6], "max_ctx");
+    const int64_t nb = size(codes, 0, 5, "codes"), hkv = codes.size(1), hd = codes.size(4), B = size(ctx, 0, 1, "ctx"),
+                  W = size(table, 1, 2, "block_table"), nd = size(k, 0, 4, "kcache");
+    const void* cp = address(codes, "codes", dev, kCode, {nb, hkv, 2, 16, hd});
+    const void* xp = address(exps, "exponents", dev, kI8, {nb, hkv, 2, 16});
+    const void* tp = address(table, "block_table", dev, kI32, {B, W});
+    const void* lp = address(ctx, "ctx", dev, kI32, {B});
+    void* kp = address(k, "kcache", dev, kHalf, {nd, hkv, 16, hd});
+    void* vp = address(v, "vcache", dev, kHalf, {nd, hkv, 16, hd});
+    const void* dp = nullptr;
+    int64_t D = 0;
+    if (a[7] != Py_None) {
+      const at::Tensor& dst = tensor(a[7], "dst_table");
+      D = size(dst, 1, 2, "dst_table");
+      dp = address(dst, "dst_table", dev, kI32, {B, D});
+    }
+    int32_t* ep = error_word(a[8], dev);
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    check(what, ee_op_dequantize_cache(size32(B, "ctx"), size32(hkv, "codes"), size32(hd, "codes"), max_ctx,
+                                       (const uint8_t*)cp, (const int8_t*)xp, size32(nb, "codes"), (const int32_t*)tp,
+                                       size32(W, "block_table"), (const int32_t*)lp, (uint16_t*)kp, (uint16_t*)vp,
+                                       size32(nd, "kcache"), (const int32_t*)dp, size32(D, "dst_table"), ep, stream_of(dev)));
+    return PyTuple_Pack(2, a[4], a[5]);
+  });
+}
+
+// (q, codes, exponents, block_table, pos, n_heads, n_kv_heads, head_dim, max_ctx, out, err)
+PyObject* quantized_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  static const char* const what = "ee_op_quantized_attention";
+  return guarded(what, [&]() -> PyObject* {
+    count(n, 11);
+    const at::Tensor &q = tensor(a[0], "q"), &codes = tensor(a[1], "codes"), &exps = tensor(a[2], "exponents"),
+                     &table = tensor(a[3], "block_table"), &pos = tensor(a[4], "pos");
+    const int dev = device_of(q, "q");
+    const int32_t hq = integer(a[5], "n_heads"), hkv = integer(a[6], "n_kv_heads"), hd = integer(a[7], "head_dim"),
+                  max_ctx = integer(a[8], "max_ctx");
+    const int64_t B = size(pos, 0, 1, "pos"), W = size(table, 1, 2, "block_table"), nb = size(codes, 0, 5, "codes"),
+                  width = (int64_t)hq * hd;
+    int64_t qs, os;
+    const void* qp = rows(q, "q", dev, B, width, &qs);
+    const void* cp = address(codes, "codes", dev, kCode, {nb, hkv, 2, 16, hd});
+    const void* xp = address(exps, "exponents", dev, kI8, {nb, hkv, 2, 16});
+    const void* tp = address(table, "block_table", dev, kI32, {B, W});
+    const void* pp = address(pos, "pos", dev, kI32, {B});
+    int32_t* ep = error_word(a[10], dev);
+    const at::Tensor o = a[9] == Py_None ? empty({B, width}, c10::ScalarType::Half, dev) : tensor(a[9], "out");
+    void* op = rows(o, "out", dev, B, width, &os);
+    const size_t bytes = ee_quantized_attention_scratch_bytes(size32(B, "pos"), hq, hkv, hd, max_ctx);
+    const at::Tensor scratch = empty({(int64_t)bytes}, c10::ScalarType::Byte, dev);
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    check(what, ee_op_quantized_attention((int32_t)B, hq, hkv, hd, max_ctx, (const uint16_t*)qp, qs, (const uint8_t*)cp,
+                                          (const int8_t*)xp, size32(nb, "codes"), (const int32_t*)tp,
+                                          size32(W, "block_table"), (const int32_t*)pp, (uint16_t*)op, os, scratch.data_ptr(),
+                                          ep, stream_of(dev)));
+    return THPVariable_Wrap(o);
+  });
+}
+
+// (q, kcache, vcache, block_table, pos, prefix, n_heads, n_kv_heads, head_dim, max_ctx, out, err)
+PyObject* shared_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  static const char* const what = "ee_op_shared_attention";
+  return guarded(what, [&]() -> PyObject* {
+    count(n, 12);
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "kcache"), &v = tensor(a[2], "vcache"),
+                     &table = tensor(a[3], "block_table"), &pos = tensor(a[4], "pos");
+    const int dev = device_of(q, "q");
+    const int32_t prefix = integer(a[5], "prefix"), hq = integer(a[6], "n_heads"), hkv = integer(a[7], "n_kv_heads"),
+                  hd = integer(a[8], "head_dim"), max_ctx = integer(a[9], "max_ctx");
+    const int64_t B = size(pos, 0, 1, "pos"), W = size(table, 1, 2, "block_table"), nb = size(k, 0, 4, "kcache"),
+                  width = (int64_t)hq * hd;
+    int64_t qs, os;
+    const void* qp = rows(q, "q", dev, B, width, &qs);
+    const void* kp = address(k, "kcache", dev, kHalf, {nb, hkv, 16, hd});
+    const void* vp = address(v, "vcache", dev, kHalf, {nb, hkv, 16, hd});
+    const void* tp = address(table, "block_table", dev, kI32, {B, W});
+    const void* pp = address(pos, "pos", dev, kI32, {B});
+    int32_t* ep = error_word(a[11], dev);
+    const at::Tensor o = a[10] == Py_None ? empty({B, width}, c10::ScalarType::Half, dev) : tensor(a[10], "out");
+    void* op = rows(o, "out", dev, B, width, &os);
+    const size_t bytes = ee_shared_attention_scratch_bytes(size32(B, "pos"), hq, hkv, hd, max_ctx, prefix);
+    const at::Tensor scratch = empty({(int64_t)bytes}, c10::ScalarType::Byte, dev);
+    const c10::cuda::CUDAGuard on((c10::DeviceIndex)dev);
+    check(what, ee_op_shared_attention((int32_t)B, hq, hkv, hd, max_ctx, prefix, (const uint16_t*)qp, qs,
+                                       (const uint16_t*)kp, (const uint16_t*)vp, size32(nb, "kcache"), (const int32_t*)tp,
+                                       size32(W, "block_table"), (const int32_t*)pp, (uint16_t*)op, os, scratch.data_ptr(),
+                                       ep, stream_of(dev)));
+    return THPVariable_Wrap(o);
+  });
+}
+
 PyMethodDef methods[] = {
     {"prompt_attention", (PyCFunction)(void (*)(void))prompt_attention, METH_FASTCALL, nullptr},
     {"prompt_weights", (PyCFunction)(void (*)(void))prompt_weights, METH_FASTCALL, nullptr},
     {"attention_weights", (PyCFunction)(void (*)(void))attention_weights, METH_FASTCALL, nullptr},
     {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, nullptr},
+    {"quantize_cache", (PyCFunction)(void (*)(void))quantize_cache, METH_FASTCALL, nullptr},
+    {"dequantize_cache", (PyCFunction)(void (*)(void))dequantize_cache, METH_FASTCALL, nullptr},
+    {"quantized_attention", (PyCFunction)(void (*)(void))quantized_attention, METH_FASTCALL, nullptr},
+    {"shared_attention", (PyCFunction)(void (*)(void))shared_attention, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

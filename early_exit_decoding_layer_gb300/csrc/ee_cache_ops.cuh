@@ -1,6 +1,7 @@
 // Parameters and launchers of the operators on the paged cache: attention of
 // packed prompt rows, the weights of its tokens, decode attention that adds
-// weights, eviction.  Lengths and block ids come from device memory and are
+// weights, eviction; the eight-bit cache's writing, reading back and decode
+// attention; decode attention behind a shared prefix.  Lengths and block ids come from device memory and are
 // checked here, in the kernels: what is out of range is cut to the range and
 // reported in the error word.
 #pragma once
@@ -63,6 +64,46 @@ struct EvictParams {
   int32_t* kept = nullptr;
 };
 
+// The eight-bit cache: codes [n_blocks, Hkv, 2, 16, hd], exponents [n_blocks, Hkv, 2, 16].
+struct QuantizeParams {
+  PagedCache c;  // k, v, weights unused
+  uint8_t* codes = nullptr;
+  int8_t* exponents = nullptr;
+  int32_t n_seqs = 0, total = 0, rows_type = 0;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  int64_t k_stride = 0, v_stride = 0;  // in elements
+  const int32_t* cu = nullptr;
+  const int32_t* ctx = nullptr;
+};
+
+struct DequantizeParams {
+  PagedCache c;  // k, v, weights unused
+  const uint8_t* codes = nullptr;
+  const int8_t* exponents = nullptr;
+  int32_t batch = 0;
+  const int32_t* ctx = nullptr;
+  uint16_t* k = nullptr;
+  uint16_t* v = nullptr;
+  int32_t n_dst = 0;
+  const int32_t* dst_table = nullptr;
+  int32_t dst_stride = 0;
+};
+
+// One query row per sequence, fp16 in and out.
+struct DecodeParams {
+  PagedCache c;
+  const uint8_t* codes = nullptr;  // of the eight-bit cache; else c.k and c.v
+  const int8_t* exponents = nullptr;
+  int32_t batch = 0, n_heads = 0, prefix = 0;  // prefix in whole blocks' tokens, at most c.max_ctx of them
+  const uint16_t* q = nullptr;
+  int64_t q_stride = 0;
+  const int32_t* pos = nullptr;
+  uint16_t* o = nullptr;
+  int64_t o_stride = 0;
+  void* scratch = nullptr;
+};
+
 // exp(z - x) of a score z = q . k / sqrt(hd), from the tensor core's sum s, as
 // 2^(c s - f x): c is log2(e) / sqrt(hd) rounded to fp32 and f c's counterpart in two
 // terms, so that c's rounding multiplies z - x and not z and x each (1e-6 at a
@@ -92,6 +133,13 @@ cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t st);
 cudaError_t launch_prompt_weights(const PromptParams& p, cudaStream_t st);
 cudaError_t launch_attention_weights(const DecodeWeightsParams& p, cudaStream_t st);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
+cudaError_t launch_quantize_cache(const QuantizeParams& p, cudaStream_t st);
+cudaError_t launch_dequantize_cache(const DequantizeParams& p, cudaStream_t st);
+cudaError_t launch_quantized_attention(const DecodeParams& p, cudaStream_t st);
+cudaError_t launch_shared_attention(const DecodeParams& p, cudaStream_t st);
+size_t quantized_attention_scratch(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx);
+size_t shared_attention_scratch(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx,
+                                int32_t prefix);
 
 #ifdef __CUDACC__
 EE_DEV void report(int32_t* err, int32_t code) {

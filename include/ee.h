@@ -523,6 +523,94 @@ ee_status ee_op_evict(int32_t B, int32_t n_kv_heads, int32_t head_dim, int32_t m
                       int32_t dst_stride, const int32_t *ctx, int32_t *new_ctx, int32_t *kept,
                       int32_t *err_flag, void *stream);
 
+/* ---- caches held in eight bits ------------------------------------------------
+ * Not part of the early-exit method: the pages have no counterpart.  Three
+ * operators on a paged cache of half the bytes: rows written into it, sequences
+ * read back into the fp16 cache (for ee_op_prompt_attention and the others above),
+ * and the decode attention that reads it as it is.
+ *
+ * The cache:  codes [n_blocks, Hkv, 2, 16, hd] in e4m3 (four bits of exponent, three
+ * of fraction; K then V) and exponents [n_blocks, Hkv, 2, 16] int8.  A value is
+ *   code * 2^exponent  of its (block, head, K or V, slot).
+ * Exponents are in [-15, 8]: a code has four significant bits whatever the scale, so that
+ * powers of two lose nothing against finer scales, products with them are exact,
+ * and every value with code and exponent is an fp16 value (the largest one, 65536,
+ * reads as 65504).  codes and exponents are 16-byte aligned.
+ * What the operators above have in common holds for these too: head_dim, heads,
+ * sequences and max_ctx, lengths and block ids on the device with EE_DERR_LENGTH and
+ * EE_DERR_BLOCK, blocks that several sequences only read, asynchronous calls that keep
+ * nothing between them. */
+enum { EE_ROWS_F16 = 0, EE_ROWS_F32 = 1 };
+
+/* Writes packed rows of new tokens: sequence s has the rows cu[s] .. cu[s+1]-1 (n of them;
+ * device, [n_seqs + 1], ascending, within [0, total]) and ctx[s] tokens with them; row
+ * i goes to position ctx[s] - n + i (one before position 0 goes nowhere).  For each row,
+ * kv head, K and V:
+ *   exponent = the least e >= -15 with max |x| <= 448 * 2^e over the finite x,
+ *   code     = x * 2^-e rounded to e4m3 (nearest, ties to even).
+ * An x that fp16 does not hold (infinite, NaN, |x| >= 65520) becomes NaN.
+ *   k, v [total, stride] of rows_type, head g at column g * hd, 16-byte aligned, strides
+ *   of whole 16 bytes and at least Hkv * hd.  total may be 0.  A block that is
+ *   written occurs in one sequence's table. */
+ee_status ee_op_quantize_cache(int32_t n_seqs, int32_t total, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx,
+                               int32_t rows_type, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                               uint8_t *codes, int8_t *exponents, int32_t n_blocks, const int32_t *block_table,
+                               int32_t bt_stride, const int32_t *cu, const int32_t *ctx, int32_t *err_flag,
+                               void *stream);
+
+/* Reads tokens 0 .. ctx[s]-1 of every sequence back into an fp16 cache of n_dst blocks,
+ * kcache/vcache [n_dst, Hkv, 16, hd], at the same places of dst_table's blocks
+ * ([B, dst_stride], 16 * dst_stride >= min(max_ctx, 16 * bt_stride)), or of block_table's own where
+ * dst_table is NULL.  Slots behind the last token are left as they are.  Where
+ * two sequences share a block, they may share its destination too; other
+ * destinations occur once. */
+ee_status ee_op_dequantize_cache(int32_t B, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx,
+                                 const uint8_t *codes, const int8_t *exponents, int32_t n_blocks,
+                                 const int32_t *block_table, int32_t bt_stride, const int32_t *ctx, uint16_t *kcache,
+                                 uint16_t *vcache, int32_t n_dst, const int32_t *dst_table, int32_t dst_stride,
+                                 int32_t *err_flag, void *stream);
+
+/* Decode attention over the eight-bit cache, one new token per sequence at position
+ * pos[s] (-1: an empty sequence, o = 0):
+ *   o[s, h] = sum_{t <= pos[s]} softmax_t(q_h . k_t / sqrt(hd)) v_t,  k and v as held.
+ *   q [B, q_stride] fp16 in natural order, head h at column h * hd; o [B, o_stride] fp16
+ *   likewise, not overlapping q; strides multiples of 8, at least Hq * hd.
+ * Products are exact in fp32 accumulators, statistics and sums fp32; probabilities have 12
+ * bits.  A NaN in a key, or a value of q that is not finite, makes the rows
+ * that see it NaN, a NaN in a value its own component of them.
+ * scratch: device buffer of ee_quantized_attention_scratch_bytes(...) bytes, 16-byte
+ * aligned.  It needs no contents and keeps none; calls that may overlap in time
+ * (streams, captured graphs) need one each. */
+size_t ee_quantized_attention_scratch_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                            int32_t max_ctx);
+ee_status ee_op_quantized_attention(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx,
+                                    const uint16_t *q, int64_t q_stride, const uint8_t *codes,
+                                    const int8_t *exponents, int32_t n_blocks, const int32_t *block_table,
+                                    int32_t bt_stride, const int32_t *pos, uint16_t *o, int64_t o_stride,
+                                    void *scratch, int32_t *err_flag, void *stream);
+
+/* ---- a batch that shares a prefix -------------------------------------------------
+ * Decode attention over the fp16 cache of sequences whose first `prefix` tokens are the
+ * same and sit in the same blocks: these are read once for the whole batch.  The
+ * results are those of one query position per sequence as in ee_op_attention,
+ *   o[s, h] = sum_{t <= pos[s]} softmax_t(q_h . k_t / sqrt(hd)) v_t,
+ * with the first prefix / 16 blocks (whole blocks; 0 <= prefix <= 16384, and 0 shares
+ * nothing) taken from block_table's first row for every sequence, whatever
+ * pos[0] is, and all others from the sequence's own row.  A sequence that ends within
+ * the prefix sees its own tokens only; pos[s] = -1 is an empty one, o = 0.
+ *   q, o, scratch as for ee_op_quantized_attention, with
+ *   ee_shared_attention_scratch_bytes(...) bytes; the caches and the rules of values that are
+ *   not finite as for ee_op_prompt_attention.
+ * Products are exact in fp32 accumulators and statistics fp32; the probabilities are rounded
+ * to fp16 for the product with V. */
+size_t ee_shared_attention_scratch_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                         int32_t max_ctx, int32_t prefix);
+ee_status ee_op_shared_attention(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx,
+                                 int32_t prefix, const uint16_t *q, int64_t q_stride, const uint16_t *kcache,
+                                 const uint16_t *vcache, int32_t n_blocks, const int32_t *block_table,
+                                 int32_t bt_stride, const int32_t *pos, uint16_t *o, int64_t o_stride,
+                                 void *scratch, int32_t *err_flag, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,3 +45,37 @@ def evict_indices(w, keep, recent):
         order = sorted(range(n - recent), key=lambda t: (bool(np.isnan(w[t, g])), 0.0 if np.isnan(w[t, g]) else -w[t, g], t))
         out.append(sorted(order[: keep - recent]) + list(range(n - recent, n)))
     return np.array(out)
+
+
+# ---- the eight-bit cache: e4m3 codes times a power of two per row
+
+def e4m3_values():
+    """The 256 codes' values: sign, four bits of exponent (bias 7), three of fraction; exponent
+    0 is subnormal, and all ones (127, 255) is NaN -- there are no infinities."""
+    out = np.empty(256)
+    for c in range(256):
+        e, f = (c >> 3) & 15, c & 7
+        x = f * 2.0 ** -9 if e == 0 else (1 + f / 8) * 2.0 ** (e - 7)
+        out[c] = math.nan if c & 127 == 127 else -x if c & 128 else x
+    return out
+
+
+def quantize_row(x):
+    """One row: (codes uint8 [hd], exponent).  Values that fp16 does not hold become NaN (127)."""
+    x = np.asarray(x, dtype=np.float64)
+    finite = np.abs(x) < 65520   # false for NaN
+    big = np.abs(x[finite]).max(initial=0.0)
+    e = -15
+    while big > 448 * 2.0 ** e:
+        e += 1
+    grid = e4m3_values()[:127]   # ascending
+    codes = np.full(x.shape, 127, dtype=np.uint8)
+    for i in np.flatnonzero(finite):
+        y = abs(x[i]) * 2.0 ** -e
+        j = min(int(np.searchsorted(grid, y)), 126)
+        if j > 0:   # grid[j - 1] < y <= grid[j]: the nearer, of equally near ones the even code
+            lo, hi = y - grid[j - 1], grid[j] - y
+            if lo < hi or (lo == hi and j % 2 == 1):
+                j -= 1
+        codes[i] = j + (128 if math.copysign(1.0, x[i]) < 0 else 0)
+    return codes, e
