@@ -1,0 +1,84 @@
+// How the decode attentions with fp16 rows share their work: the blocks of all
+// (sequence, kv head) pairs in a row, cut into equal pieces, one for each CTA.
+//
+// Lengths are on the device, so every warp that needs the plan makes it (two lengths a lane
+// and a scan).  A piece may begin and end within a pair: what a CTA finds there is a
+// part, (O, m, l) in the scratch, and the join adds a pair's parts in the order of the
+// CTAs.  A CTA has at most two of them, of its first pair and of its last; pairs that lie
+// within a piece are finished where they are.
+#pragma once
+
+#include "ee_cache_ops.cuh"
+
+namespace ee {
+
+// A CTA's share of a pair: blocks first .. first + blocks - 1, `have` tokens in them.
+struct Share {
+  int s, g, first, blocks, have;
+  int slot;  // of its part in the scratch; -1: the whole pair
+};
+
+struct DecodePlan {
+  int tokens[2], base[2], blocks[2];  // of sequences lane and lane + 32; blocks before them
+  int hkv, total, each, begin, end;
+
+  // `least`: blocks of a piece at least.  whole: a CTA takes the pairs that begin in its
+  // piece.  The whole warp.
+  EE_DEV void init(const DecodeParams& p, int pieces, int least, bool whole, int me) {
+    static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
+    const int lane = threadIdx.x & 31;
+    hkv = p.c.n_kv_heads;
+    int sum[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int s = lane + 32 * u, at = s < p.batch ? p.pos[s] : -1;
+      tokens[u] = checked_length(at == INT32_MAX ? at : at + 1, p.c.max_ctx, p.c.err);
+      blocks[u] = (tokens[u] + 15) >> 4;
+      sum[u] = blocks[u];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum[u], o);
+        if (lane >= o) sum[u] += x;
+      }
+    }
+    const int half = __shfl_sync(0xffffffffu, sum[0], 31);
+    base[0] = sum[0] - blocks[0];
+    base[1] = half + sum[1] - blocks[1];
+    total = (half + __shfl_sync(0xffffffffu, sum[1], 31)) * hkv;
+    each = max(least, (total + pieces - 1) / pieces);
+    begin = min(total, me * each);
+    end = min(total, begin + each);
+    if (whole) {
+      begin = next_pair(begin);
+      end = next_pair(end);
+    }
+  }
+  // The lane's sequence u holds place c.
+  EE_DEV bool holds(int u, int c) const { return c >= base[u] * hkv && c < (base[u] + blocks[u]) * hkv; }
+  // Value a[u] of the sequence that holds place c < total.
+  EE_DEV int of(const int (&a)[2], unsigned lo, unsigned hi) const {
+    return lo ? __shfl_sync(0xffffffffu, a[0], __ffs(lo) - 1) : __shfl_sync(0xffffffffu, a[1], __ffs(hi) - 1);
+  }
+  EE_DEV int next_pair(int c) const {  // the first pair that begins at c or behind it
+    if (c >= total) return total;
+    const unsigned lo = __ballot_sync(0xffffffffu, holds(0, c)), hi = __ballot_sync(0xffffffffu, holds(1, c));
+    const int nb = of(blocks, lo, hi), b0 = of(base, lo, hi) * hkv;
+    return b0 + (c - b0 + nb - 1) / nb * nb;
+  }
+  // The share that begins at place c; s = -1: no more.
+  EE_DEV Share at(int c, int me) const {
+    Share r = {-1, 0, 0, 0, 0, -1};
+    if (c >= end) return r;
+    const unsigned lo = __ballot_sync(0xffffffffu, holds(0, c)), hi = __ballot_sync(0xffffffffu, holds(1, c));
+    const int nb = of(blocks, lo, hi), b0 = of(base, lo, hi) * hkv, n = of(tokens, lo, hi);
+    r.s = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+    r.g = (c - b0) / nb;
+    r.first = c - b0 - r.g * nb;
+    r.blocks = min(nb - r.first, end - c);
+    r.have = min(n - r.first * 16, r.blocks * 16);
+    if (r.blocks < nb) r.slot = 2 * me + (c > begin);
+    return r;
+  }
+};
+
+}  // namespace ee

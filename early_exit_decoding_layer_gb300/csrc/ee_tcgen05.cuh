@@ -15,6 +15,10 @@ namespace ee {
 bool encode_tensor_map(CUtensorMap* map, bool bf16, int rank, const void* base, const uint64_t* dims,
                        const uint64_t* strides, const uint32_t* box);
 
+// The same for bytes, rows of 128 or 64 of them (box[0]) with the swizzle of that width.
+bool encode_tensor_map_bytes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                             const uint32_t* box);
+
 // Shared memory descriptor of a K-major tile with 128-byte rows and the
 // 128-byte swizzle: start address, stride between 8-row groups (`group` bytes),
 // descriptor version 1, swizzle mode 2 (leading offset unused: 1).
@@ -37,6 +41,30 @@ EE_DEV uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t half, uint32_t group
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
+}
+
+// Tiles of bytes whose rows, 128, 64 or 32 bytes with the swizzle of that width, come in groups
+// of 8, `group` bytes from one to the next: K-major, or MN-major with one row's width along
+// M or N.
+template <int WIDTH>
+EE_DEV uint64_t smem_desc_rows(uint32_t saddr, uint32_t group) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(group >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(WIDTH == 128 ? 2 : WIDTH == 64 ? 4 : 6) << 61;
+  return d;
+}
+
+// Byte offset of 16-byte chunk j of row r (of groups that lie side by side) in such a tile.
+template <int WIDTH>
+EE_DEV uint32_t row_chunk(int r, int j) {
+  return (uint32_t)(r * WIDTH + ((j ^ (WIDTH == 128 ? r & 7 : WIDTH == 64 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4));
+}
+
+// Instruction descriptor, kind::f8f6f4: e4m3 by e4m3, fp32 accumulators.
+constexpr uint32_t instr_desc_e4m3(int n, int m, bool b_mn = false, bool a_mn = false) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Instruction descriptor, kind::f16: fp32 accumulators, A and B of type
@@ -84,6 +112,23 @@ EE_DEV void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int 
       : "memory");
 }
 
+EE_DEV void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, int v, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// 8 bytes to shared memory, counted by the next copies_arrive of this thread.
+EE_DEV void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on `bar` (which counts this arrival) when this thread's copies so far have landed.
+EE_DEV void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // D[tmem] (+)= A * B, both operands in shared memory.
 EE_DEV void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
@@ -91,7 +136,14 @@ EE_DEV void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc
                : "memory");
 }
 
-// The same with A in tensor memory (two 16-bit values of K per 32-bit column).
+// e4m3 operands, 32 of K.
+EE_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+               : "memory");
+}
+
+// mma_f16 with A in tensor memory (two 16-bit values of K per 32-bit column).
 EE_DEV void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
                "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)

@@ -20,10 +20,8 @@ EncodeTiledFn lookup() {
   return reinterpret_cast<EncodeTiledFn>(f);
 }
 
-}  // namespace
-
-bool encode_tensor_map(CUtensorMap* map, bool bf16, int rank, const void* base, const uint64_t* dims,
-                       const uint64_t* strides, const uint32_t* box) {
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int rank, const void* base,
+                const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
   static std::atomic<EncodeTiledFn> found{nullptr};
   EncodeTiledFn fn = found.load(std::memory_order_acquire);
   if (!fn) {
@@ -41,9 +39,22 @@ bool encode_tensor_map(CUtensorMap* map, bool bf16, int rank, const void* base, 
     es[i] = 1;
     if (i + 1 < rank) st[i] = strides[i];
   }
-  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-            const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, type, rank, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool encode_tensor_map(CUtensorMap* map, bool bf16, int rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box) {
+  return encode_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    CU_TENSOR_MAP_SWIZZLE_128B, rank, base, dims, strides, box);
+}
+
+bool encode_tensor_map_bytes(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                             const uint32_t* box) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    rank, base, dims, strides, box);
 }
 
 }  // namespace ee

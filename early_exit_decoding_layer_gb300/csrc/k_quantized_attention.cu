@@ -1,60 +1,557 @@
-// Decode attention over the eight-bit cache: a warp per sequence and query head walks
-// the tokens with a running maximum and sum, hd / 32 dims a lane.
+// Decode attention over the eight-bit cache, on the tensor cores.
+//
+// One new token per sequence: K and V are read once for the G query heads of a kv
+// head, so the bytes are the bound, and these are half of the fp16 cache's -- if the
+// arithmetic keeps out of the way.  Turning codes into fp16 first would cost
+// instructions for every byte; the MMAs take e4m3 as it is, with the cache as the big
+// operand:
+//   S = K_tile Q^T      128 tokens x N columns
+//   O^T += V_tile^T X   head dims x N columns, K = 128 tokens
+// Then Q and X have to be e4m3 too.  They go in as three parts of four bits,
+//   x = a + 2^-5 b + 2^-10 c,
+// each a column of its own (N = 3 G, to 16 or 32), so that fp16 queries are exact and
+// X has 12 bits; a part's remainder is at most 2^-4 of it, and times 2^5 the next part is
+// as large again, so that small values stay small relative to the largest and no part
+// falls below e4m3's range.  The columns that this adds are free: the tensor core is at
+// a few percent.
+//
+// The rows' scales are powers of two.  K's multiplies a score.  V's goes into the
+// probability: with w_t = log2(e) z_t + e_t the product takes X_t = 2^(w_t - M), M a
+// running maximum of w that may lag by 2^4, and the sum l adds X_t 2^-e_t, which is exact.
+//
+// A CTA has a piece of all blocks (ee_decode_plan.cuh), in tiles of eight blocks:
+//   warps 0-3  a thread per token: scores, maximum, X into shared memory; then a
+//              thread per head dim writes O, or a part of it to the scratch
+//   warp 4     codes by TMA, one box a block (K and V lie side by side), and exponents,
+//              into a ring
+//   warp 5     (one thread) the MMAs, S a tile ahead of O
+//   warps 6-7  the next pair's Q
+// A second kernel joins the parts of pairs that several CTAs had a share of.
+#include <limits.h>
 #include <math.h>
 
-#include "ee_cache_ops.cuh"
+#include <algorithm>
+#include <atomic>
+
+#include "ee_decode_plan.cuh"
 #include "ee_tcgen05.cuh"
 
 namespace ee {
 namespace {
 
-EE_DEV float from_e4m3(uint8_t c) {
+constexpr int kThreads = 256;
+constexpr int kTokens = 128;  // per tile, eight blocks
+constexpr int kMaxCtas = 3 * 160;
+constexpr float kLift = 4.0f, kLag = 4.0f;  // X is 2^kLift at the maximum, 2^(kLift + kLag) at most
+
+template <int HD, int G>
+struct Layout {
+  static constexpr int N = G == 8 ? 32 : 16;          // columns: part 0 of G heads, part 1, part 2
+  static constexpr int kCtas = G == 8 ? 2 : 3;        // per SM
+  static constexpr uint32_t kBlock = 32 * HD;         // K and V of a block: [2 groups][K, V][8][HD]
+  static constexpr uint32_t kGroup = 16 * HD;         // from 8 tokens to the next 8
+  static constexpr uint32_t kTile = 8 * kBlock;
+  static constexpr int NS = (HD == 64 ? 2 : 1) * (G == 8 ? 3 : 2);
+  static constexpr uint32_t kQ = N * HD;              // rows of HD bytes
+  static constexpr uint32_t kX = kTokens * 32;        // rows of 32 bytes, a token each
+  static constexpr uint32_t oQ = NS * kTile, oX = oQ + 2 * kQ, oE = oX + kX;
+  static constexpr size_t kSmem = 1024 + oE + NS * 256;
+};
+
+template <int HD, int G>
+struct Shared {
+  static constexpr int NS = Layout<HD, G>::NS;
+  uint64_t full[NS], empty[NS], s_full[2], x_ready, o_done;
+  uint64_t q_ready[2], q_free[2];  // by share & 1
+  uint64_t drained;                // every MMA issued is over
+  uint32_t tmem;
+  float unscale[2][G], red[4][G], sum[4][G];
+};
+
+// Two values as e4m3, the first in the low byte, and what they stand for.
+EE_DEV uint32_t to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+  return r;
+}
+EE_DEV float2 from_e4m3x2(uint32_t c) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-template <int HD>
-__global__ void k_quantized_attention(const DecodeParams p) {
-  constexpr int N = HD / 32;
-  const int lane = threadIdx.x & 31, at = blockIdx.x * 4 + (threadIdx.x >> 5), hkv = p.c.n_kv_heads;
-  if (at >= p.batch * p.n_heads) return;
-  const int s = at / p.n_heads, h = at % p.n_heads, g = h / (p.n_heads / hkv);
-  const int ctx = checked_length(p.pos[s] == INT32_MAX ? INT32_MAX : p.pos[s] + 1, p.c.max_ctx, p.c.err);
-  float q[N], o[N], m = -INFINITY, l = 0.0f;
-  for (int i = 0; i < N; ++i) {
-    q[i] = __half2float(__ushort_as_half(p.q[s * p.q_stride + h * HD + i * 32 + lane])) * (1.4426950408889634f / sqrtf((float)HD));
-    if (isinf(q[i])) q[i] = NAN;
-    o[i] = 0.0f;
+// The three parts of two values of at most 2^8.
+EE_DEV void parts3(float a, float b, uint32_t (&c)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    c[i] = to_e4m3x2(a, b);
+    if (i < 2) {
+      const float2 f = from_e4m3x2(c[i]);
+      a = (a - f.x) * 32.0f;
+      b = (b - f.y) * 32.0f;
+    }
   }
-  for (int t = 0; t < ctx; ++t) {
-    bool ok;
-    const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, s, t, p.c.err, &ok);
-    const int64_t k = ((int64_t)b * hkv + g) * 32 + (t & 15), v = k + 16;
-    float z = 0.0f;
-    for (int i = 0; i < N; ++i) z += q[i] * from_e4m3(p.codes[k * HD + i * 32 + lane]);
-    z = warp_sum(z) * exp2f((float)p.exponents[k]);
-    const float mn = fmaxf(m, z), a = ex2(m - mn), e = ex2(z - mn), w = e * exp2f((float)p.exponents[v]);
-    m = mn;
-    l = l * a + e;
-    for (int i = 0; i < N; ++i) o[i] = o[i] * a + w * from_e4m3(p.codes[v * HD + i * 32 + lane]);
+}
+
+// A value from the columns of its parts.
+EE_DEV float joined(uint32_t a, uint32_t b, uint32_t c) {
+  return fmaf(__uint_as_float(c), 0x1p-10f, fmaf(__uint_as_float(b), 0x1p-5f, __uint_as_float(a)));
+}
+
+EE_DEV float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// A part in the scratch: O of every head, then m and l.
+template <int HD, int G>
+EE_DEV float* part(const DecodeParams& p, int slot) {
+  return static_cast<float*>(p.scratch) + (size_t)slot * G * (HD + 2);
+}
+
+// o is a mean of held values; fp16 ends at 65504.
+EE_DEV float within_half(float y) {
+  return fabsf(y) > 65504.0f && fabsf(y) < INFINITY ? copysignf(65504.0f, y) : y;
+}
+
+template <int HD, int G>
+__global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
+    k_quantized_attention(const DecodeParams p, const __grid_constant__ CUtensorMap map, const float c, const int least,
+                          const bool whole) {
+  using Lay = Layout<HD, G>;
+  constexpr int N = Lay::N, NS = Lay::NS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared<HD, G> sh;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *qs = ring + Lay::oQ, *xs = ring + Lay::oX, *es = ring + Lay::oE;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = blockIdx.x;
+  grid_dep_launch();
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sh.full[i], 33);  // the copies' bytes; 32 lanes' exponents
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.q_ready[i], 64);
+      mbar_init(&sh.q_free[i], 5);  // the products with it, and four warps that have its scales
+    }
+    mbar_init(&sh.x_ready, 128);
+    mbar_init(&sh.o_done, 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init();
   }
-  for (int i = 0; i < N; ++i) {
-    const float x = ctx > 0 ? o[i] / l : 0.0f;
-    p.o[s * p.o_stride + h * HD + i * 32 + lane] =
-        float_to_half_bits(fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x);
+  if (warp == 5) tmem_alloc(&sh.tmem, 4 * N);
+  DecodePlan plan;
+  plan.init(p, gridDim.x, least, whole, me);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  auto s_col = [&](int t) { return tmem + (t & 1) * N; };
+  auto o_col = [&](int r) { return tmem + 2 * N + (r & 1) * N; };
+  // Tiles and shares count on; after a wait that gave up the loops go on without waiting:
+  // every thread still meets the barriers that count threads.
+  bool ok = true;
+
+  if (warp == 4) {
+    int t = 0;
+    for (int at = plan.begin; at < plan.end && ok;) {
+      const Share u = plan.at(at, me);
+      const int32_t* table = p.c.table + (int64_t)u.s * p.c.table_stride + u.first;
+      int ids = 0;
+      for (int j = 0; j < u.blocks && ok; j += 8, ++t) {
+        // block ids come 32 at a time
+        if ((j & 31) == 0) ids = j + lane < u.blocks ? table[j + lane] : 0;
+        const int here = min(8, u.blocks - j), st = t % NS;
+        int id = __shfl_sync(0xffffffffu, ids, (j & 31) + (lane & 7)), eid = __shfl_sync(0xffffffffu, ids, (j & 31) + (lane >> 2));
+        if (id < 0 || id >= p.c.n_blocks) {
+          if (lane < here) report(p.c.err, EE_DERR_BLOCK);
+          id = 0;
+        }
+        if (eid < 0 || eid >= p.c.n_blocks) eid = 0;
+        if (t >= NS) ok = warp_wait(&sh.empty[st], (t / NS - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], (uint32_t)here * Lay::kBlock);
+        __syncwarp();
+        if (lane < here)
+          tma_load_5d(smem_addr(ring + st * Lay::kTile + lane * Lay::kBlock), &map, 0, 0, 0, 0, id * p.c.n_kv_heads + u.g,
+                      &sh.full[st]);
+        if ((lane >> 2) < here)
+          copy8(smem_addr(es + st * 256 + lane * 8), p.exponents + ((int64_t)eid * p.c.n_kv_heads + u.g) * 32 + (lane & 3) * 8);
+        copies_arrive(&sh.full[st]);
+      }
+      at += u.blocks;
+    }
+    // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
+    for (int i = max(0, t - NS); i < t; ++i)
+      mbar_wait_bounded(&sh.full[i % NS], (uint32_t)(i / NS) & 1, p.c.err, DERR_DRAIN_WAIT);
+  } else if (warp == 5) {
+    constexpr uint32_t id_s = instr_desc_e4m3(N, kTokens), id_o = instr_desc_e4m3(N, HD, true, true);
+    int t = 0, r = 0;
+    bool first_scores = true;  // of a share are out already, or to be made
+    auto scores = [&](int t, int r, bool last) {  // of a tile of share r
+      if (!mbar_wait_bounded(&sh.full[t % NS], (t / NS) & 1, p.c.err, DERR_FULL_WAIT)) return false;
+      tc_fence_after();
+      const uint64_t k = smem_desc_rows<HD>(smem_addr(ring + t % NS * Lay::kTile), Lay::kGroup),
+                     q = smem_desc_rows<HD>(smem_addr(qs + (r & 1) * Lay::kQ), 8 * HD);
+#pragma unroll
+      for (int kk = 0; kk < HD / 32; ++kk) mma_f8(s_col(t), k + kk * 2, q + kk * 2, id_s, kk > 0);
+      mma_commit(&sh.s_full[t & 1]);
+      if (last) mma_commit(&sh.q_free[r & 1]);
+      return true;
+    };
+    auto q_there = [&](int r) { return mbar_wait_bounded(&sh.q_ready[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT); };
+    int at = plan.begin;
+    Share u = plan.at(at, me);
+    for (; u.s >= 0 && ok; ++r) {
+      at += u.blocks;
+      const Share then = plan.at(at, me);
+      const int tiles = (u.blocks + 7) >> 3;
+      if (lane == 0) {
+        if (first_scores) ok = q_there(r) && scores(t, r, tiles == 1);
+        for (int j = 0; j < tiles && ok; ++j, ++t) {
+          // the next tile's scores, of this share or of the next
+          if (j + 1 < tiles) ok = scores(t + 1, r, j + 2 == tiles);
+          else if (then.s >= 0) ok = q_there(r + 1) && scores(t + 1, r + 1, then.blocks <= 8);
+          if (!ok || !(ok = mbar_wait_bounded(&sh.x_ready, t & 1, p.c.err, DERR_FULL_WAIT))) break;
+          tc_fence_after();
+          const uint64_t v = smem_desc_rows<HD>(smem_addr(ring + t % NS * Lay::kTile) + 8 * HD, Lay::kGroup),
+                         x = smem_desc_rows<32>(smem_addr(xs), 256);
+#pragma unroll
+          for (int kk = 0; kk < kTokens / 32; ++kk)
+            mma_f8(o_col(r), v + kk * (4 * Lay::kGroup >> 4), x + kk * (1024 >> 4), id_o, j > 0 || kk > 0);
+          mma_commit(&sh.empty[t % NS]);
+          mma_commit(&sh.o_done);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      first_scores = false;
+      u = then;
+    }
+    if (lane == 0) {  // and so are the products, before tensor memory is given back
+      mma_commit(&sh.drained);
+      mbar_wait_bounded(&sh.drained, 0, p.c.err, DERR_DRAIN_WAIT);
+    }
+    __syncwarp();
+  } else if (warp >= 6) {
+    // empty sequences
+    for (int s = me; s < p.batch; s += gridDim.x) {
+      const int n = __shfl_sync(0xffffffffu, s < 32 ? plan.tokens[0] : plan.tokens[1], s & 31);
+      if (n == 0)
+        for (int i = (warp - 6) * 32 + lane; i < p.n_heads * HD; i += 64) p.o[s * p.o_stride + i] = 0;
+    }
+    constexpr int kHeads = (G + 1) / 2, kPer = HD / 32;
+    int r = 0;
+    for (int at = plan.begin; at < plan.end && ok; ++r) {
+      const Share u = plan.at(at, me);
+      at += u.blocks;
+      const uint16_t* q = p.q + u.s * p.q_stride + (int64_t)u.g * G * HD;
+      float x[kHeads][kPer];
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int h = 2 * i + warp - 6;
+        // neighbouring dims in a lane, whose codes are stored together
+        uint32_t w[kPer / 2] = {};
+        if (h < G) {
+          if constexpr (HD == 128) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(q + h * HD + lane * 4);
+          else w[0] = *reinterpret_cast<const uint32_t*>(q + h * HD + lane * 2);
+        }
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+          x[i][2 * e] = f.x;
+          x[i][2 * e + 1] = f.y;
+        }
+      }
+      if (r >= 2) ok = warp_wait(&sh.q_free[r & 1], (r / 2 - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int h = 2 * i + warp - 6;
+        float big = 0.0f;
+        bool fine = true;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          big = fmaxf(big, fabsf(x[i][e]));
+          fine = fine && fabsf(x[i][e]) < INFINITY;
+        }
+        big = warp_max(big);
+        fine = __all_sync(0xffffffffu, fine);
+        // 2^k with 2^7 <= big 2^k < 2^8; an fp16 value's exponent is -24 or more
+        const int k = fine ? min(31, 134 - (int)(__float_as_uint(big) >> 23)) : 0;
+        const float up = fine ? pow2(k) : __uint_as_float(0x7fffffffu);
+        if (h < G) {
+          if (lane == 0) sh.unscale[r & 1][h] = c * pow2(-k);
+#pragma unroll
+          for (int e = 0; e < kPer; e += 2) {
+            uint32_t a[3];
+            parts3(x[i][e] * up, x[i][e + 1] * up, a);
+            const int d = lane * kPer + e;
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              const int n = part * G + h;
+              *reinterpret_cast<uint16_t*>(qs + (r & 1) * Lay::kQ + (n >> 3) * 8 * HD + row_chunk<HD>(n & 7, d >> 4) + (d & 15)) =
+                  (uint16_t)a[part];
+            }
+          }
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(&sh.q_ready[r & 1]);
+    }
+  } else {
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    // M = 64: rows 16 w .. 16 w + 15 in the first lanes of warp w's part of tensor memory
+    const int dim = HD == 128 ? tid : warp * 16 + (lane & 15);
+    const bool has_dim = HD == 128 || lane < 16;
+    int t = 0, r = 0;
+    for (int at = plan.begin; at < plan.end; ++r) {
+      const Share u = plan.at(at, me);
+      at += u.blocks;
+      const int tiles = (u.blocks + 7) >> 3;
+      if (ok) ok = warp_wait(&sh.q_ready[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT);
+      float unscale[G], m[G], l[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        unscale[h] = sh.unscale[r & 1][h];
+        m[h] = -INFINITY;
+        l[h] = 0.0f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_free[r & 1]);
+#pragma unroll 1
+      for (int j = 0; j < tiles; ++j, ++t) {
+        if (ok) ok = warp_wait(&sh.s_full[t & 1], (t >> 1) & 1, p.c.err, DERR_FULL_WAIT);
+        // K's scores are made, so the tile has landed; a wait of its own orders its exponents
+        if (ok) ok = warp_wait(&sh.full[t % NS], (t / NS) & 1, p.c.err, DERR_FULL_WAIT);
+        tc_fence_after();
+        uint32_t v[N];
+        if constexpr (N == 32) tmem_ld32(s_col(t) + lane_base, v);
+        else tmem_ld16(s_col(t) + lane_base, v);
+        const int8_t* e8 = reinterpret_cast<const int8_t*>(es) + t % NS * 256 + (tid >> 4) * 32 + (tid & 15);
+        const int ek = e8[0], ev = e8[16];
+        tmem_wait_ld();
+        tmem_pin<N>(v);
+        const int left = u.have - j * kTokens;  // tokens from this tile on
+        const bool live = tid < left;
+        const float up = pow2(ek), evf = (float)ev, down = live ? pow2(-ev) : 0.0f;
+        float w[G], a[G];
+        int grow = 0;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          w[h] = live ? fmaf(joined(v[h], v[G + h], v[2 * G + h]) * unscale[h], up, evf) : -INFINITY;
+          grow |= w[h] - m[h] > kLag;
+          a[h] = 1.0f;
+        }
+        asm volatile(
+            "{ .reg .pred p, q; setp.ne.s32 p, %0, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.s32 %0, 1, 0, q; }"
+            : "+r"(grow)
+            :
+            : "memory");
+        if (grow) {  // the first tile, and rarely later
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float x = warp_max(w[h]);
+            if (lane == 0) sh.red[warp][h] = x;
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mn = fmaxf(fmaxf(fmaxf(sh.red[0][h], sh.red[1][h]), fmaxf(sh.red[2][h], sh.red[3][h])), m[h]);
+            a[h] = m[h] == mn ? 1.0f : ex2(m[h] - mn);
+            m[h] = mn;
+            l[h] *= a[h];
+          }
+        }
+        uint32_t x8[8] = {};  // the token's row of X: bytes part * G + h
+#pragma unroll
+        for (int h = 0; h < G; h += 2) {
+          float x[2] = {0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < (G == 1 ? 1 : 2); ++i) {
+            x[i] = ex2(w[h + i] - (m[h + i] == -INFINITY ? 0.0f : m[h + i]) + kLift);
+            l[h + i] = live ? fmaf(x[i], down, l[h + i]) : l[h + i];
+          }
+          uint32_t cs[3];
+          parts3(x[0], x[1], cs);
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const int n = part * G + h;
+            x8[n >> 2] |= (G == 1 ? cs[part] & 0xffu : cs[part]) << (8 * (n & 3));
+          }
+        }
+        // the product before has read X and is in O
+        if (t > 0 && ok) ok = warp_wait(&sh.o_done, (t - 1) & 1, p.c.err, DERR_FULL_WAIT);
+        *reinterpret_cast<uint4*>(xs + (tid >> 3) * 256 + row_chunk<32>(tid & 7, 0)) = make_uint4(x8[0], x8[1], x8[2], x8[3]);
+        if constexpr (N == 32)
+          *reinterpret_cast<uint4*>(xs + (tid >> 3) * 256 + row_chunk<32>(tid & 7, 1)) = make_uint4(x8[4], x8[5], x8[6], x8[7]);
+        if (left < kTokens) {
+          // slots behind the last token hold anything: their V becomes zero
+          uint8_t* tile = ring + t % NS * Lay::kTile + 8 * HD;
+          for (int i = left * (HD / 16) + tid; i < kTokens * (HD / 16); i += 128) {
+            const int row = i / (HD / 16);
+            *reinterpret_cast<uint4*>(tile + (row >> 3) * Lay::kGroup + (row & 7) * HD + (i % (HD / 16)) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        if (grow && j > 0) {
+          tc_fence_after();
+          uint32_t o[N];
+          if constexpr (N == 32) tmem_ld32(o_col(r) + lane_base, o);
+          else tmem_ld16(o_col(r) + lane_base, o);
+          tmem_wait_ld();
+          tmem_pin<N>(o);
+#pragma unroll
+          for (int i = 0; i < 3 * G; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a[i % G]);
+          tmem_st16(o_col(r) + lane_base, o);
+          if constexpr (N == 32) tmem_st16(o_col(r) + 16 + lane_base, o + 16);
+          tmem_wait_st();
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&sh.x_ready);
+      }
+      // the share's end: l of all warps, O of this thread's dim
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float x = warp_sum(l[h]);
+        if (lane == 0) sh.sum[warp][h] = x;
+      }
+      if (ok) ok = warp_wait(&sh.o_done, (t - 1) & 1, p.c.err, DERR_FULL_WAIT);
+      tc_fence_after();
+      uint32_t o[N];
+      if constexpr (N == 32) tmem_ld32(o_col(r) + lane_base, o);
+      else tmem_ld16(o_col(r) + lane_base, o);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      tmem_wait_ld();
+      tmem_pin<N>(o);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float sum = (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]);
+        const float y = joined(o[h], o[G + h], o[2 * G + h]);
+        if (u.slot < 0) {
+          if (has_dim && ok) p.o[u.s * p.o_stride + (u.g * G + h) * HD + dim] = float_to_half_bits(within_half(y / sum));
+        } else {
+          float* to = part<HD, G>(p, u.slot);
+          if (has_dim) to[h * HD + dim] = y;
+          if (tid == h) {
+            to[G * HD + h] = m[h];
+            to[G * HD + G + h] = sum;
+          }
+        }
+      }
+      // sum is read before the next share's is written: its first tile's barrier is between
+      tc_fence_before();
+    }
   }
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_free(tmem, 4 * N);
+  }
+  if (!ok) __nanosleep(1000000);  // what this CTA no longer waited for may be on its way
+}
+
+// The join: a CTA per sequence and query head adds the parts of its pair, where there are any.
+template <int HD, int G>
+__global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int pieces, const int least) {
+  __shared__ float red[4][2], outs[4][HD];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s = blockIdx.x / p.n_heads, head = blockIdx.x - s * p.n_heads, g = head / G, h = head % G;
+  DecodePlan plan;
+  plan.init(p, pieces, least, false, 0);
+  const int nb = __shfl_sync(0xffffffffu, s < 32 ? plan.blocks[0] : plan.blocks[1], s & 31);
+  const int from = __shfl_sync(0xffffffffu, s < 32 ? plan.base[0] : plan.base[1], s & 31) * plan.hkv + g * nb;
+  grid_dep_wait();
+  if (nb == 0) return;
+  const int w0 = from / plan.each, w1 = (from + nb - 1) / plan.each, n = w1 - w0 + 1;
+  if (n == 1) return;
+  // the first CTA has the pair as its last one, unless it begins with it
+  auto slot = [&](int k) { return 2 * (w0 + k) + (k == 0 && from > w0 * plan.each ? 1 : 0); };
+  float mm = -INFINITY;
+  for (int k = tid; k < n; k += 128) mm = fmaxf(mm, part<HD, G>(p, slot(k))[G * HD + h]);
+  mm = warp_max(mm);
+  if (lane == 0) red[warp][0] = mm;
+  __syncthreads();
+  mm = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+  constexpr int P = HD / 32;  // dims per lane
+  float o[P], l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) o[i] = 0.0f;
+#pragma unroll 4
+  for (int k = warp; k < n; k += 4) {
+    const float* x = part<HD, G>(p, slot(k));
+    const float f = ex2(x[G * HD + h] - mm);
+    l = fmaf(f, x[G * HD + G + h], l);
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] = fmaf(f, x[h * HD + i * 32 + lane], o[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) outs[warp][i * 32 + lane] = o[i];
+  if (lane == 0) red[warp][1] = l;
+  __syncthreads();
+  if (tid < HD) {
+    const float sum = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+    const float y = (outs[0][tid] + outs[1][tid]) + (outs[2][tid] + outs[3][tid]);
+    p.o[s * p.o_stride + head * HD + tid] = float_to_half_bits(within_half(y / sum));
+  }
+}
+
+template <int HD, int G>
+cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
+  using Lay = Layout<HD, G>;
+  static std::atomic<uint64_t> prepared{0};  // a bit per device
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(k_quantized_attention<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) prepared.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  CUtensorMap map;
+  // a block of a kv head, as groups of 8 tokens: [group][K, V][8][HD]
+  const uint64_t d[5] = {(uint64_t)HD, 8, 2, 2, (uint64_t)p.c.n_blocks * p.c.n_kv_heads},
+                 s[4] = {(uint64_t)HD, (uint64_t)HD * 16, (uint64_t)HD * 8, (uint64_t)HD * 32};
+  const uint32_t b[5] = {(uint32_t)HD, 8, 2, 2, 1};
+  if (!encode_tensor_map_bytes(&map, 5, p.codes, d, s, b)) return cudaErrorInvalidValue;
+  const int64_t most = (int64_t)p.batch * p.c.n_kv_heads * ((p.c.max_ctx + 15) / 16);
+  const int least = 8;
+  const bool whole = p.c.max_ctx <= kTokens;
+  const int pieces = (int)std::min<int64_t>(std::min(Lay::kCtas * sms, kMaxCtas), (most + least - 1) / least);
+  k_quantized_attention<HD, G><<<pieces, kThreads, Lay::kSmem, st>>>(p, map, 1.44269504f / sqrtf((float)HD), least, whole);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || whole) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(p.batch * p.n_heads));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join<HD, G>, p, pieces, least);
 }
 
 }  // namespace
 
 cudaError_t launch_quantized_attention(const DecodeParams& p, cudaStream_t st) {
-  const unsigned n = (unsigned)(p.batch * p.n_heads + 3) / 4;
-  if (p.c.head_dim == 64) k_quantized_attention<64><<<n, 128, 0, st>>>(p);
-  else k_quantized_attention<128><<<n, 128, 0, st>>>(p);
-  return cudaGetLastError();
+  const int G = p.n_heads / p.c.n_kv_heads, hd = p.c.head_dim;
+#define EE_DECODE_CASE(HD_, G_) \
+  if (hd == HD_ && G == G_) return launch_t<HD_, G_>(p, st);
+  EE_DECODE_CASE(64, 1)
+  EE_DECODE_CASE(64, 2)
+  EE_DECODE_CASE(64, 4)
+  EE_DECODE_CASE(64, 8)
+  EE_DECODE_CASE(128, 1)
+  EE_DECODE_CASE(128, 2)
+  EE_DECODE_CASE(128, 4)
+  EE_DECODE_CASE(128, 8)
+#undef EE_DECODE_CASE
+  return cudaErrorInvalidValue;
 }
 
-size_t quantized_attention_scratch(int32_t, int32_t, int32_t, int32_t, int32_t) { return 16; }
+size_t quantized_attention_scratch(int32_t, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t) {
+  return (size_t)2 * kMaxCtas * (n_heads / n_kv_heads) * (head_dim + 2) * 4;
+}
 
 }  // namespace ee

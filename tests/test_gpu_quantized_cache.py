@@ -401,7 +401,14 @@ def test_bad_lengths_and_blocks_are_reported():
             table[0, 19:] = 0
         o, err = calls(dev(table), dev(ctx), cu)
         assert err == [code] * 3, what
-        assert np.array_equal(o[1].cpu().numpy().reshape(4, 64).astype(np.float64), good[1]), what
+        got = o[1].cpu().numpy().reshape(4, 64).astype(np.float64)
+        if "block" in what:
+            assert np.array_equal(got, good[1]), what
+        else:
+            # another length moves the borders between the CTAs' shares, so that the same sums are
+            # taken in another order: within the bound that holds for every order
+            want, bound = attention_reference(q[1].astype(np.float64), *h.history(1))
+            assert np.all(np.abs(got - want) <= bound), what
     for bad in ((0, 2, 1 << 30), (-1, 2, 5), (0, 4, 2)):
         assert calls(dev(h.table), dev(np.array(h.ctxs, np.int32)), i32(*bad))[1] == [0, 0, EE_DERR_LENGTH], bad
 

@@ -233,7 +233,14 @@ def test_bad_lengths_and_blocks_are_reported():
         err = i32(0)
         o = h.call(q, 4, max_ctx=410, table=table, pos=dev(pos), err=err)
         assert err.item() == code, what
-        assert torch.equal(o[0], good[0]) and torch.equal(o[2], good[2]), what
+        for s in (0, 2):
+            if "block" in what:
+                assert torch.equal(o[s], good[s]), what
+            else:
+                # another length moves the borders between the CTAs' shares, so that the same sums
+                # are taken in another order: within the bound that holds for every order
+                want, _, _, bound, _, _ = prompt_reference(h, s, q[s][None])
+                assert np.all(np.abs(o[s].cpu().numpy().astype(np.float64).reshape(4, 64) - want[0]) <= bound[0]), what
     table = h.table.copy()
     table[0, 3] = h.n_blocks   # of the prefix
     err = i32(0)
