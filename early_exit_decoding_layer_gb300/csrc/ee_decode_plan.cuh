@@ -28,23 +28,28 @@ struct DecodePlan {
     static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
     const int lane = threadIdx.x & 31;
     hkv = p.c.n_kv_heads;
-    int sum[2];
+    int at[2];  // both loads before either is waited for
+#pragma unroll
+    for (int u = 0; u < 2; ++u) at[u] = lane + 32 * u < p.batch ? p.pos[lane + 32 * u] : -1;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int s = lane + 32 * u, at = s < p.batch ? p.pos[s] : -1;
-      tokens[u] = checked_length(at == INT32_MAX ? at : at + 1, p.c.max_ctx, p.c.err);
+      tokens[u] = checked_length(at[u] == INT32_MAX ? at[u] : at[u] + 1, p.c.max_ctx, p.c.err);
       blocks[u] = (tokens[u] + 15) >> 4;
-      sum[u] = blocks[u];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sum[u], o);
-        if (lane >= o) sum[u] += x;
-      }
     }
-    const int half = __shfl_sync(0xffffffffu, sum[0], 31);
-    base[0] = sum[0] - blocks[0];
-    base[1] = half + sum[1] - blocks[1];
-    total = (half + __shfl_sync(0xffffffffu, sum[1], 31)) * hkv;
+    // both scans at once: sums of 32 lengths are at most 2^15 blocks
+    static_assert(kCacheMaxCtx / 16 * 32 < 1 << 16, "two sums in a word");
+    const uint32_t mine = (uint32_t)blocks[0] | (uint32_t)blocks[1] << 16;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+    sum -= mine;
+    base[0] = (int)(sum & 0xffffu);
+    base[1] = (int)(all & 0xffffu) + (int)(sum >> 16);
+    total = ((int)(all & 0xffffu) + (int)(all >> 16)) * hkv;
     each = max(least, (total + pieces - 1) / pieces);
     begin = min(total, me * each);
     end = min(total, begin + each);

@@ -49,7 +49,7 @@ struct Layout {
   static constexpr int N = G == 8 ? 32 : 16;          // columns: part 0 of G heads, part 1, part 2
   static constexpr int kCtas = G == 8 ? 2 : 3;        // per SM
   static constexpr uint32_t kBlock = 32 * HD;         // K and V of a block: [2 groups][K, V][8][HD]
-  static constexpr uint32_t kGroup = 16 * HD;         // from 8 tokens to the next 8
+  static constexpr uint32_t kRows8 = 16 * HD;         // from 8 tokens to the next 8
   static constexpr uint32_t kTile = 8 * kBlock;
   static constexpr int NS = (HD == 64 ? 2 : 1) * (G == 8 ? 3 : 2);
   static constexpr uint32_t kQ = N * HD;              // rows of HD bytes
@@ -120,36 +120,47 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared<HD, G> sh;
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *qs = ring + Lay::oQ, *xs = ring + Lay::oX, *es = ring + Lay::oE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = blockIdx.x;
+  uint8_t *qs = ring + Lay::oQ, *xs = ring + Lay::oX, *es = ring + Lay::oE;
   grid_dep_launch();
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.full[i], 33);  // the copies' bytes; 32 lanes' exponents
-      mbar_init(&sh.empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.q_ready[i], 64);
-      mbar_init(&sh.q_free[i], 5);  // the products with it, and four warps that have its scales
-    }
-    mbar_init(&sh.x_ready, 128);
-    mbar_init(&sh.o_done, 1);
-    mbar_init(&sh.drained, 1);
-    fence_mbar_init();
-  }
-  if (warp == 5) tmem_alloc(&sh.tmem, 4 * N);
-  DecodePlan plan;
-  plan.init(p, gridDim.x, least, whole, me);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  auto s_col = [&](int t) { return tmem + (t & 1) * N; };
-  auto o_col = [&](int r) { return tmem + 2 * N + (r & 1) * N; };
   // Tiles and shares count on; after a wait that gave up the loops go on without waiting:
   // every thread still meets the barriers that count threads.
   bool ok = true;
+
+  // The loads begin before anything else is ready: their warp makes the barriers, and
+  // does not wait for the others.
+  if (warp == 4) {
+    if (lane == 0) {
+      for (int i = 0; i < NS; ++i) {
+        mbar_init(&sh.full[i], 33);  // the copies' bytes; 32 lanes' exponents
+        mbar_init(&sh.empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.s_full[i], 1);
+        mbar_init(&sh.q_ready[i], 64);
+        mbar_init(&sh.q_free[i], 5);  // the products with it, and four warps that have its scales
+      }
+      mbar_init(&sh.x_ready, 128);
+      mbar_init(&sh.o_done, 1);
+      mbar_init(&sh.drained, 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("bar.arrive 2, 256;" ::: "memory");
+  }
+  DecodePlan plan;
+  plan.init(p, gridDim.x, least, whole, me);
+  if (warp != 4) {
+    if (warp == 5) {
+      tmem_alloc(&sh.tmem, 4 * N);
+      tc_fence_before();
+    }
+    asm volatile("bar.sync 2, 256;" ::: "memory");
+    tc_fence_after();
+  }
+  const uint32_t tmem = warp == 4 ? 0 : sh.tmem;
+  auto s_col = [&](int t) { return tmem + (t & 1) * N; };
+  auto o_col = [&](int r) { return tmem + 2 * N + (r & 1) * N; };
 
   if (warp == 4) {
     int t = 0;
@@ -185,46 +196,66 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
       mbar_wait_bounded(&sh.full[i % NS], (uint32_t)(i / NS) & 1, p.c.err, DERR_DRAIN_WAIT);
   } else if (warp == 5) {
     constexpr uint32_t id_s = instr_desc_e4m3(N, kTokens), id_o = instr_desc_e4m3(N, HD, true, true);
-    int t = 0, r = 0;
-    bool first_scores = true;  // of a share are out already, or to be made
     auto scores = [&](int t, int r, bool last) {  // of a tile of share r
-      if (!mbar_wait_bounded(&sh.full[t % NS], (t / NS) & 1, p.c.err, DERR_FULL_WAIT)) return false;
       tc_fence_after();
-      const uint64_t k = smem_desc_rows<HD>(smem_addr(ring + t % NS * Lay::kTile), Lay::kGroup),
+      const uint64_t k = smem_desc_rows<HD>(smem_addr(ring + t % NS * Lay::kTile), Lay::kRows8),
                      q = smem_desc_rows<HD>(smem_addr(qs + (r & 1) * Lay::kQ), 8 * HD);
 #pragma unroll
       for (int kk = 0; kk < HD / 32; ++kk) mma_f8(s_col(t), k + kk * 2, q + kk * 2, id_s, kk > 0);
       mma_commit(&sh.s_full[t & 1]);
       if (last) mma_commit(&sh.q_free[r & 1]);
-      return true;
     };
-    auto q_there = [&](int r) { return mbar_wait_bounded(&sh.q_ready[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT); };
-    int at = plan.begin;
+    int t = 0, r = 0, at = plan.begin;
     Share u = plan.at(at, me);
+    bool out = false;  // tile t's scores
     for (; u.s >= 0 && ok; ++r) {
       at += u.blocks;
       const Share then = plan.at(at, me);
       const int tiles = (u.blocks + 7) >> 3;
       if (lane == 0) {
-        if (first_scores) ok = q_there(r) && scores(t, r, tiles == 1);
         for (int j = 0; j < tiles && ok; ++j, ++t) {
-          // the next tile's scores, of this share or of the next
-          if (j + 1 < tiles) ok = scores(t + 1, r, j + 2 == tiles);
-          else if (then.s >= 0) ok = q_there(r + 1) && scores(t + 1, r + 1, then.blocks <= 8);
-          if (!ok || !(ok = mbar_wait_bounded(&sh.x_ready, t & 1, p.c.err, DERR_FULL_WAIT))) break;
+          auto landed = [&](int t, int r) {
+            return mbar_wait_bounded(&sh.q_ready[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT) &&
+                   mbar_wait_bounded(&sh.full[t % NS], (t / NS) & 1, p.c.err, DERR_FULL_WAIT);
+          };
+          if (!out) {
+            if (!(ok = landed(t, r))) break;
+            scores(t, r, j + 1 == tiles);
+          }
+          // The next tile's scores as soon as it is there, of this share or of the next; but the
+          // product with X does not wait for them: a tile of the ring is free behind it.
+          const int rn = j + 1 < tiles ? r : r + 1;
+          const bool more = j + 1 < tiles || then.s >= 0, last = j + 1 < tiles ? j + 2 == tiles : then.blocks <= 8;
+          out = false;
+          uint64_t since = 0;
+          for (int i = 1; !mbar_test(&sh.x_ready, t & 1); ++i) {
+            if (more && !out && mbar_test(&sh.q_ready[rn & 1], (rn >> 1) & 1) && mbar_test(&sh.full[(t + 1) % NS], ((t + 1) / NS) & 1)) {
+              scores(t + 1, rn, last);
+              out = true;
+            }
+            if ((i & 255) == 0) {
+              const uint64_t now = globaltimer();
+              if (since == 0) since = now;
+              if (now - since > kWaitTimeoutNs) {
+                if (p.c.err) atomicCAS(p.c.err, 0, DERR_FULL_WAIT);
+                ok = false;
+                break;
+              }
+            }
+          }
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t v = smem_desc_rows<HD>(smem_addr(ring + t % NS * Lay::kTile) + 8 * HD, Lay::kGroup),
+          const uint64_t v = smem_desc_rows<HD>(smem_addr(ring + t % NS * Lay::kTile) + 8 * HD, Lay::kRows8),
                          x = smem_desc_rows<32>(smem_addr(xs), 256);
 #pragma unroll
           for (int kk = 0; kk < kTokens / 32; ++kk)
-            mma_f8(o_col(r), v + kk * (4 * Lay::kGroup >> 4), x + kk * (1024 >> 4), id_o, j > 0 || kk > 0);
+            mma_f8(o_col(r), v + kk * (4 * Lay::kRows8 >> 4), x + kk * (1024 >> 4), id_o, j > 0 || kk > 0);
           mma_commit(&sh.empty[t % NS]);
           mma_commit(&sh.o_done);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
       t = __shfl_sync(0xffffffffu, t, 0);
-      first_scores = false;
       u = then;
     }
     if (lane == 0) {  // and so are the products, before tensor memory is given back
@@ -388,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
           uint8_t* tile = ring + t % NS * Lay::kTile + 8 * HD;
           for (int i = left * (HD / 16) + tid; i < kTokens * (HD / 16); i += 128) {
             const int row = i / (HD / 16);
-            *reinterpret_cast<uint4*>(tile + (row >> 3) * Lay::kGroup + (row & 7) * HD + (i % (HD / 16)) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(tile + (row >> 3) * Lay::kRows8 + (row & 7) * HD + (i % (HD / 16)) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         if (grow && j > 0) {
@@ -427,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
         const float sum = (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]);
         const float y = joined(o[h], o[G + h], o[2 * G + h]);
         if (u.slot < 0) {
-          if (has_dim && ok) p.o[u.s * p.o_stride + (u.g * G + h) * HD + dim] = float_to_half_bits(within_half(y / sum));
+          if (has_dim && ok) p.o[u.s * p.o_stride + (u.g * G + h) * HD + dim] = float_to_half_bits(within_half(__fdividef(y, sum)));
         } else {
           float* to = part<HD, G>(p, u.slot);
           if (has_dim) to[h * HD + dim] = y;
@@ -449,48 +480,69 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
   if (!ok) __nanosleep(1000000);  // what this CTA no longer waited for may be on its way
 }
 
-// The join: a CTA per sequence and query head adds the parts of its pair, where there are any.
+// The join: a CTA per sequence and query head adds the parts of its pair, where there are
+// any: every fourth one a warp, eight of them in flight, then the four warps' sums.
 template <int HD, int G>
 __global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int pieces, const int least) {
-  __shared__ float red[4][2], outs[4][HD];
+  constexpr int P = HD / 32, U = 8;  // dims per lane; parts in flight
+  __shared__ float ms[4], ls[4], outs[4][HD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x / p.n_heads, head = blockIdx.x - s * p.n_heads, g = head / G, h = head % G;
   DecodePlan plan;
   plan.init(p, pieces, least, false, 0);
   const int nb = __shfl_sync(0xffffffffu, s < 32 ? plan.blocks[0] : plan.blocks[1], s & 31);
   const int from = __shfl_sync(0xffffffffu, s < 32 ? plan.base[0] : plan.base[1], s & 31) * plan.hkv + g * nb;
+  const int w0 = from / plan.each, n = nb == 0 ? 0 : (from + nb - 1) / plan.each - w0 + 1;
   grid_dep_wait();
-  if (nb == 0) return;
-  const int w0 = from / plan.each, w1 = (from + nb - 1) / plan.each, n = w1 - w0 + 1;
-  if (n == 1) return;
+  if (n < 2) return;
   // the first CTA has the pair as its last one, unless it begins with it
-  auto slot = [&](int k) { return 2 * (w0 + k) + (k == 0 && from > w0 * plan.each ? 1 : 0); };
-  float mm = -INFINITY;
-  for (int k = tid; k < n; k += 128) mm = fmaxf(mm, part<HD, G>(p, slot(k))[G * HD + h]);
-  mm = warp_max(mm);
-  if (lane == 0) red[warp][0] = mm;
-  __syncthreads();
-  mm = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-  constexpr int P = HD / 32;  // dims per lane
-  float o[P], l = 0.0f;
+  const int late = from > w0 * plan.each;
+  float m = -INFINITY, l = 0.0f, o[P] = {};
+  for (int k0 = warp; k0 < n; k0 += 4 * U) {
+    float mk[U], lk[U], ok[U][P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) o[i] = 0.0f;
-#pragma unroll 4
-  for (int k = warp; k < n; k += 4) {
-    const float* x = part<HD, G>(p, slot(k));
-    const float f = ex2(x[G * HD + h] - mm);
-    l = fmaf(f, x[G * HD + G + h], l);
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 4 * u;
+      const float* x = part<HD, G>(p, 2 * (w0 + k) + (k == 0 ? late : 0));
+      mk[u] = k < n ? x[G * HD + h] : -INFINITY;
+      lk[u] = k < n ? x[G * HD + G + h] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) o[i] = fmaf(f, x[h * HD + i * 32 + lane], o[i]);
+      for (int i = 0; i < P; ++i) ok[u][i] = k < n ? x[h * HD + i * 32 + lane] : 0.0f;
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, mk[u]);
+    const float a = m == mn ? 1.0f : ex2(m - mn);
+    m = mn;
+    l *= a;
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] *= a;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // a part of NaN alone has no maximum; its l and O are NaN, which stays
+      const float f = mk[u] == m ? 1.0f : ex2(mk[u] - m);
+      l = fmaf(f, lk[u], l);
+#pragma unroll
+      for (int i = 0; i < P; ++i) o[i] = fmaf(f, ok[u][i], o[i]);
+    }
+  }
+  if (lane == 0) {
+    ms[warp] = m;
+    ls[warp] = l;
   }
 #pragma unroll
   for (int i = 0; i < P; ++i) outs[warp][i * 32 + lane] = o[i];
-  if (lane == 0) red[warp][1] = l;
   __syncthreads();
   if (tid < HD) {
-    const float sum = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
-    const float y = (outs[0][tid] + outs[1][tid]) + (outs[2][tid] + outs[3][tid]);
-    p.o[s * p.o_stride + head * HD + tid] = float_to_half_bits(within_half(y / sum));
+    const float mm = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+    float sum = 0.0f, y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = ms[w] == mm ? 1.0f : ex2(ms[w] - mm);
+      sum = fmaf(f, ls[w], sum);
+      y = fmaf(f, outs[w][tid], y);
+    }
+    p.o[s * p.o_stride + head * HD + tid] = float_to_half_bits(within_half(__fdividef(y, sum)));
   }
 }
 
