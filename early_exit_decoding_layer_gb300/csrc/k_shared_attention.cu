@@ -1,6 +1,36 @@
-// Decode attention of a batch that shares a prefix: a warp per sequence and query head
-// walks the tokens with a running maximum and sum, hd / 32 dims a lane.
+// Decode attention of a batch whose sequences begin with the same blocks, on the tensor
+// cores (tcgen05.mma, fp32 accumulators in tensor memory).
+//
+// The shared blocks are read once for all rows: of a kv head there are B G of them
+// (every sequence's query heads), 128 to an M tile, and what a decode step is bound
+// by, bytes, becomes flops there.  Each sequence's own blocks behind the prefix have
+// G rows to read them, padded to 128: wasted products, but the tensor core has twice the
+// time that the bytes take.
+//
+// Work is cut into equal pieces, one for each CTA: first the prefix, unit by unit of
+// (row tile, kv head), then the sequences' own blocks, by (sequence, kv head), in
+// tiles of 128 keys.  A piece may begin and end within a unit, so a unit's result comes in
+// parts, (O, m, l) in fp32 in the scratch; a second kernel adds each row's parts in the
+// order of the pieces.
+//
+// A CTA has two streams of key tiles, each with a softmax warpgroup; while one is busy with
+// its probabilities the tensor core works for the other:
+//   wide (a unit of 129 to 256 rows)  each stream has 128 rows, both see every key tile
+//   narrow (all others)  both have the same rows, and every second key tile
+//   warps 4t .. 4t + 3   a thread per row: S_t to registers, running maximum and sum,
+//                        P_t = exp2(c S - c m) as fp16 over S_t's columns
+//   warp 9 (one thread)  the products, O_t += P_t V_j and S_t = Q K_j'^T; in narrow units
+//                        stream 0's
+//   warp 10              narrow: stream 1's products.  wide: waits for K and V tiles in warp
+//                        9's place, which has none of the tensor core's time to lose
+//   warp 8               Q, K and V by TMA, a box per 16-slot block, into a ring
+//   warp 11              finds the CTA's next units of work
+// The maximum may lag behind by up to 8 (in log2), so that O is rarely rescaled.
+#include <limits.h>
 #include <math.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "ee_cache_ops.cuh"
 #include "ee_tcgen05.cuh"
@@ -8,47 +38,720 @@
 namespace ee {
 namespace {
 
+constexpr int kKeys = 128;     // of a tile, eight blocks
+constexpr int kThreads = 384;  // two softmax warpgroups, TMA, two for MMA, units
+constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsSingle = 88;  // at launch, and after
+static_assert(256 * kRegsSoftmax + 128 * kRegsSingle <= kThreads * kRegs, "no more than the launch has");
+constexpr int kMaxPieces = 160;
+// What a tile costs, and a unit's first loads and its parts' way out, in 200 cycles.
+constexpr int kWideCost = 16, kNarrowCost = 9, kOwnCost = 10, kStartCost = 12;
+
 template <int HD>
-__global__ void k_shared_attention(const DecodeParams p) {
-  constexpr int N = HD / 32;
-  const int lane = threadIdx.x & 31, at = blockIdx.x * 4 + (threadIdx.x >> 5), hkv = p.c.n_kv_heads;
-  if (at >= p.batch * p.n_heads) return;
-  const int s = at / p.n_heads, h = at % p.n_heads, g = h / (p.n_heads / hkv);
-  const int ctx = checked_length(p.pos[s] == INT32_MAX ? INT32_MAX : p.pos[s] + 1, p.c.max_ctx, p.c.err);
-  float q[N], o[N], m = -INFINITY, l = 0.0f;
-  for (int i = 0; i < N; ++i) {
-    q[i] = __half2float(__ushort_as_half(p.q[s * p.q_stride + h * HD + i * 32 + lane])) * (1.4426950408889634f / sqrtf((float)HD));
-    o[i] = 0.0f;
+struct Shape {
+  static constexpr int H = HD / 64;                // 64-column halves
+  static constexpr uint32_t kTile = 128 * HD * 2;  // a Q, K or V tile
+  static constexpr uint32_t kHalf = 128 * 128;     // a 64-column half of Q's
+  static constexpr uint32_t kRows8 = H * 1024;     // 8 tokens of K or V: [half][8][64]
+  static constexpr int NST = HD == 128 ? 5 : 9;    // ring tiles: as many as fit
+  static constexpr size_t kSmem = 1024 + (2 + NST) * (size_t)kTile;
+};
+
+struct Maps {
+  CUtensorMap q, q1, k, v;  // q1: the rows of one sequence
+};
+
+// A unit's share of a CTA: `tiles` key tiles, `have` tokens in them, from block `first` of
+// table row `row` on.
+struct Work {
+  int kind;  // 0: no more, 1: narrow, 2: wide; 3: a sequence's own (narrow)
+  int s, g, row, first, tiles, have, rows;
+  int64_t slot;  // of its part's first row
+};
+
+// The parts in the scratch: rows of O and of (m, l), first the prefix's.
+struct Scratch {
+  float *o, *ml;
+};
+__host__ __device__ inline int prefix_rows(int batch, int G) { return batch * G > 128 ? 256 : 2 * batch * G; }
+__host__ __device__ inline int64_t prefix_slots(int batch, int G, int hkv, int prefix) {
+  return prefix > 0 ? (int64_t)(batch * G + 255) / 256 * hkv + kMaxPieces : 0;
+}
+__host__ __device__ inline int64_t scratch_rows(int batch, int G, int hkv, int prefix) {
+  return prefix_slots(batch, G, hkv, prefix) * prefix_rows(batch, G) + ((int64_t)batch * hkv + kMaxPieces) * 2 * G;
+}
+
+// Where the pieces' borders lie.  A unit of n tiles has the places [x, x + kStartCost + n
+// cost); its first tile stands at x, tile k at x + kStartCost + k cost.  Two sequences per
+// lane, the whole warp.
+template <int G>
+struct Plan {
+  int tokens[2], base[2], cost[2];  // of sequences lane and lane + 32: their own blocks' cost, and that before them
+  int hkv, batch, prefix, pre, pre_cost[2], pre_end, total, each;
+
+  EE_DEV static int unit_cost(int tiles, int c) { return tiles > 0 ? kStartCost + tiles * c : 0; }
+  EE_DEV int first_own(int n) const { return pre > 0 && n >= pre * 16 ? pre : 0; }  // block
+  EE_DEV int own_tiles(int n) const { return (((n + 15) >> 4) - first_own(n) + 7) >> 3; }
+  EE_DEV int rows_of(int rt) const { return min(256, batch * G - rt * 256); }
+
+  EE_DEV void init(const DecodeParams& p, int pieces) {
+    static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
+    static_assert((kStartCost + kCacheMaxCtx / kKeys * kOwnCost) * 32 < 1 << 16, "two sums in a word");
+    const int lane = threadIdx.x & 31;
+    hkv = p.c.n_kv_heads;
+    batch = p.batch;
+    prefix = p.prefix;
+    int at[2];  // both loads before either is waited for
+#pragma unroll
+    for (int u = 0; u < 2; ++u) at[u] = lane + 32 * u < p.batch ? p.pos[lane + 32 * u] : -1;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) tokens[u] = checked_length(at[u] == INT32_MAX ? at[u] : at[u] + 1, p.c.max_ctx, p.c.err);
+    // the prefix is read if a sequence sees it whole; who does not has all its blocks to itself
+    pre = __any_sync(0xffffffffu, max(tokens[0], tokens[1]) >= p.prefix) ? p.prefix >> 4 : 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) cost[u] = unit_cost(own_tiles(tokens[u]), kOwnCost);
+    const uint32_t mine = (uint32_t)cost[0] | (uint32_t)cost[1] << 16;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+    sum -= mine;
+    base[0] = (int)(sum & 0xffffu);
+    base[1] = (int)(all & 0xffffu) + (int)(sum >> 16);
+    const int tiles = (pre + 7) >> 3;
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) pre_cost[rt] = rows_of(rt) > 0 ? unit_cost(tiles, rows_of(rt) > 128 ? kWideCost : kNarrowCost) : 0;
+    pre_end = hkv * (pre_cost[0] + pre_cost[1]);
+    total = pre_end + hkv * ((int)(all & 0xffffu) + (int)(all >> 16));
+    each = max(kStartCost + kNarrowCost, (total + pieces - 1) / pieces);
   }
-  for (int t = 0; t < ctx; ++t) {
-    bool ok;
-    const int b = checked_block(p.c.table, p.c.table_stride, p.c.n_blocks, t < p.prefix ? 0 : s, t, p.c.err, &ok);
-    const int64_t k = ((int64_t)b * hkv + g) * 16 + (t & 15);
-    float z = 0.0f;
-    for (int i = 0; i < N; ++i) z += q[i] * __half2float(__ushort_as_half(p.c.k[k * HD + i * 32 + lane]));
-    z = warp_sum(z);
-    if (z == INFINITY) z = NAN;
-    const float mn = fmaxf(m, z), mm = mn == -INFINITY ? 0.0f : mn, a = ex2(m - mm), e = ex2(z - mm);
+  // The first tile of a unit at x that stands at place c or behind it.
+  EE_DEV static int tile_at(int c, int x, int tiles, int cost) {
+    return c <= x ? 0 : min(tiles, max(1, (c - x - kStartCost + cost - 1) / cost));
+  }
+  EE_DEV int of(const int (&a)[2], int s) const { return s < 32 ? __shfl_sync(0xffffffffu, a[0], s) : __shfl_sync(0xffffffffu, a[1], s - 32); }
+
+  // The unit that holds place c < total, as far as it lies in piece `me`; *end: its end.
+  EE_DEV Work at(int c, int me, int* end) const {
+    Work w;
+    const int begin = me * each, stop = min(total, begin + each);
+    int x, tiles, cst;
+    if (c < pre_end) {
+      const int rt = c < hkv * pre_cost[0] ? 0 : 1, c0 = rt * hkv * pre_cost[0];
+      w.g = (c - c0) / pre_cost[rt];
+      x = c0 + w.g * pre_cost[rt];
+      *end = x + pre_cost[rt];
+      w.rows = rows_of(rt);
+      w.kind = w.rows > 128 ? 2 : 1;
+      w.s = rt * 256 / G;
+      w.row = 0;
+      tiles = (pre + 7) >> 3;
+      cst = w.kind == 2 ? kWideCost : kNarrowCost;
+      w.slot = (int64_t)(rt * hkv + w.g + me) * prefix_rows(batch, G);
+      w.first = 0;
+      w.have = pre * 16;
+    } else {
+      const unsigned lo = __ballot_sync(0xffffffffu, c >= pre_end + base[0] * hkv && c < pre_end + (base[0] + cost[0]) * hkv);
+      const unsigned hi = __ballot_sync(0xffffffffu, c >= pre_end + base[1] * hkv && c < pre_end + (base[1] + cost[1]) * hkv);
+      w.s = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+      const int b0 = pre_end + of(base, w.s) * hkv, cs = of(cost, w.s), n = of(tokens, w.s);
+      w.g = (c - b0) / cs;
+      x = b0 + w.g * cs;
+      *end = x + cs;
+      w.kind = 3;
+      w.rows = G;
+      w.first = first_own(n);
+      w.row = prefix > 0 && w.first == 0 ? 0 : w.s;  // who ends within the prefix has its blocks
+      tiles = own_tiles(n);
+      cst = kOwnCost;
+      w.slot = ((int64_t)w.s * hkv + w.g + me) * 2 * G;
+      w.have = n - w.first * 16;
+    }
+    const int k0 = tile_at(begin, x, tiles, cst), k1 = tile_at(stop, x, tiles, cst);
+    w.first += k0 * 8;
+    w.have = min(w.have, k1 * kKeys) - k0 * kKeys;
+    w.tiles = k1 - k0;
+    return w;
+  }
+};
+
+template <int G>
+EE_DEV Scratch scratch_of(const DecodeParams& p, bool own) {
+  const int64_t rows = scratch_rows(p.batch, G, p.c.n_kv_heads, p.prefix);
+  const int64_t before = own ? prefix_slots(p.batch, G, p.c.n_kv_heads, p.prefix) * prefix_rows(p.batch, G) : 0;
+  Scratch r;
+  r.o = reinterpret_cast<float*>(((uintptr_t)p.scratch + 31) & ~(uintptr_t)31);
+  r.ml = r.o + rows * p.c.head_dim + before * 2;
+  r.o += before * p.c.head_dim;
+  return r;
+}
+
+constexpr int kUnits = 4;  // units known ahead
+
+template <int HD>
+struct Shared {
+  static constexpr int NST = Shape<HD>::NST;
+  uint64_t q_full, q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
+  uint64_t unit_full[kUnits], unit_free[kUnits];
+  uint64_t drained[2];  // every MMA issued is over
+  Work unit[kUnits];
+  uint32_t tmem;
+};
+
+template <int HD, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_shared_attention(const DecodeParams p, const __grid_constant__ Maps maps, const float c) {
+  using S = Shape<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared<HD> sh;
+  uint8_t* tiles = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dep_launch();
+  if (tid == 0) {
+    mbar_init(&sh.q_full, 1);
+    for (int i = 0; i < S::NST; ++i) {
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_ready[t], 129);  // its warpgroup, and the tiles that the products need
+      mbar_init(&sh.q_free[t], 1);   // the stream's last product with it
+      mbar_init(&sh.o_done[t], 1);
+      mbar_init(&sh.drained[t], 1);
+    }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&sh.unit_full[i], 1);
+      mbar_init(&sh.unit_free[i], 11);  // every warp but the one that finds them
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t q_s = smem_addr(tiles), kv_s = q_s + 2 * S::kTile;
+  // tensor memory: S_t (128 columns, P_t over its first 64), then O_t
+  auto s_col = [&](int t) { return tmem + t * 128; };
+  auto o_col = [&](int t) { return tmem + 256 + t * HD; };
+  // Ring items count on over the units: item base + 2 j is K of the unit's key tile j, item
+  // base + 2 j + 1 its V.
+  auto stage = [&](int i) { return i % S::NST; };
+  auto phase = [&](int i) { return (uint32_t)(i / S::NST) & 1; };
+
+  // Unit i of this CTA, found by warp 11.
+  auto unit_at = [&](int i) {
+    Work u;
+    u.kind = 0;
+    if (warp_wait(&sh.unit_full[i % kUnits], (i / kUnits) & 1, p.c.err, DERR_FULL_WAIT)) {
+      u = sh.unit[i % kUnits];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.unit_free[i % kUnits]);
+    }
+    return u;
+  };
+  // Steps of stream t in a unit, and the key tile of step i.
+  auto steps_of = [](const Work& u, int t) { return u.kind == 2 ? u.tiles : (u.tiles + 1 - t) >> 1; };
+  auto tile_of = [](const Work& u, int t, int i) { return u.kind == 2 ? i : 2 * i + t; };
+
+  constexpr uint32_t id_qk = instr_desc(0, kKeys, 128), id_pv = instr_desc(0, HD, 128, true);
+  auto product_s = [&](int t, int q, int item) {  // S_t = Q tile q, K in ring item
+    const uint32_t a = q_s + q * S::kTile, b = kv_s + stage(item) * S::kTile;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk)
+      mma_f16(s_col(t), smem_desc_sw128(a + (kk >> 2) * S::kHalf + (kk & 3) * 32),
+              smem_desc_sw128(b + (kk >> 2) * 1024 + (kk & 3) * 32, S::kRows8), id_qk, kk > 0);
+  };
+  auto product_o = [&](int t, int item, bool acc) {  // O_t (+)= P_t, V in ring item
+    const uint32_t b = kv_s + stage(item) * S::kTile;
+#pragma unroll
+    for (int kk = 0; kk < kKeys / 16; ++kk)
+      mma_f16_ta(o_col(t), s_col(t) + kk * 8, smem_desc_sw128_mn(b + kk * 2 * S::kRows8, 1024, S::kRows8), id_pv, acc || kk > 0);
+  };
+
+  // Registers go from the four single warps to the softmax warps, which hold a row of
+  // S: 128 x 88 + 256 x 208 is what 384 threads are launched with at 168 each
+  // (launch_t checks that).
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSingle));
+  if (warp == 11) {
+    Plan<G> plan;
+    plan.init(p, gridDim.x);
+    const int me = blockIdx.x, stop = min(plan.total, (me + 1) * plan.each);
+    int i = 0;
+    bool ok = true;
+    for (int at = me * plan.each; ok;) {
+      Work w;
+      w.kind = w.tiles = 0;
+      int end = 0;
+      if (at < stop) {
+        w = plan.at(at, me, &end);
+        at = end;
+        if (w.tiles == 0) continue;
+      }
+      if (i >= kUnits) ok = warp_wait(&sh.unit_free[i % kUnits], (i / kUnits - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+      if (!ok) break;
+      if (lane == 0) {
+        sh.unit[i % kUnits] = w;
+        mbar_arrive(&sh.unit_full[i % kUnits]);
+      }
+      __syncwarp();
+      ++i;
+      if (w.kind == 0) break;
+    }
+  } else if (warp == 8) {
+    Work u = unit_at(0);
+    const int b8 = lane & 7;
+    int issued = 0, loads = 0, ends[2] = {0, 0};
+    bool ok = true;
+    for (int i = 0; u.kind && ok; u = unit_at(++i)) {
+      const int nblk = (u.have + 15) >> 4;
+      const int32_t* bt = p.c.table + (int64_t)u.row * p.c.table_stride + u.first;
+      auto block_id = [&](int j) {  // of block b8 of key tile j
+        const int b = j * 8 + b8;
+        int id = b < nblk ? bt[b] : 0;
+        if (id < 0 || id >= p.c.n_blocks) {
+          report(p.c.err, EE_DERR_BLOCK);
+          id = 0;
+        }
+        return id;
+      };
+      int id = block_id(0);
+      // q_free: the products of the units before have read their Q
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (ok && ends[t] > 0) ok = warp_wait(&sh.q_free[t], (ends[t] - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+        ends[t] += steps_of(u, t) > 0;
+      }
+      if (!ok) break;
+      ++loads;
+      if (lane == 0) {
+        const uint32_t bytes = u.kind == 3 ? G * HD * 2 : u.kind * S::kTile;
+        mbar_arrive_expect_tx(&sh.q_full, bytes);
+        for (int h = 0; h < S::H; ++h) {
+          if (u.kind == 3) tma_load_3d(q_s + h * S::kHalf, &maps.q1, h * 64, u.g * G, u.s, &sh.q_full);
+          else
+            for (int t = 0; t < u.kind; ++t)
+              tma_load_3d(q_s + t * S::kTile + h * S::kHalf, &maps.q, h * 64, u.g * G, u.s + t * (128 / G), &sh.q_full);
+        }
+      }
+      __syncwarp();
+      for (int j = 0; j < u.tiles && ok; ++j) {
+        const int next = block_id(j + 1), here = min(8, nblk - j * 8);
+        for (int kv = 0; kv < 2; ++kv, ++issued) {
+          const int st = stage(issued);
+          if (issued >= S::NST) ok = warp_wait(&sh.kv_empty[st], phase(issued - S::NST), p.c.err, DERR_EMPTY_WAIT);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], (uint32_t)here * 16 * HD * 2);
+          __syncwarp();
+          if (lane < here)
+            tma_load_4d(kv_s + st * S::kTile + lane * 2 * S::kRows8, kv ? &maps.v : &maps.k, 0, 0, 0,
+                        (id * p.c.n_kv_heads + u.g) * 2, &sh.kv_full[st]);
+        }
+        id = next;
+      }
+    }
+    // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
+    for (int i = max(0, issued - S::NST); i < issued; ++i)
+      mbar_wait_bounded(&sh.kv_full[stage(i)], phase(i), p.c.err, DERR_DRAIN_WAIT);
+    if (loads > 0) mbar_wait_bounded(&sh.q_full, (loads - 1) & 1, p.c.err, DERR_DRAIN_WAIT);
+  } else {
+    // Warps 9 and 10.
+    const int me = warp - 9;
+    Work u = unit_at(0);
+    int base = 0, steps[2] = {0, 0}, ends = 0, kind_before = 0;
+    bool ok = true;
+    for (int i = 0; u.kind && ok; u = unit_at(++i)) {
+      const int nk = u.tiles;
+      const bool wide = u.kind == 2;
+      // Stream 1's products go from one warp to the other where wide and narrow units meet:
+      // the first ones wait for the last ones of the other.
+      const bool change = (kind_before == 2) != wide && ends > 0 && me == (wide ? 0 : 1);
+      if (lane == 0) {
+        if (change) ok = mbar_wait_bounded(&sh.o_done[1], (ends - 1) & 1, p.c.err, DERR_FULL_WAIT);
+        if (!wide) {
+          // a stream by itself: each product as soon as its tile is there
+          const int t = me, n = steps_of(u, t);
+          auto landed = [&](int item) {
+            const bool r = mbar_wait_bounded(&sh.kv_full[stage(item)], phase(item), p.c.err, DERR_FULL_WAIT);
+            tc_fence_after();
+            return r;
+          };
+          auto scores = [&](int j) {
+            if (!landed(base + 2 * j)) return false;
+            product_s(t, 0, base + 2 * j);
+            mma_commit(&sh.s_full[t]);
+            mma_commit(&sh.kv_empty[stage(base + 2 * j)]);
+            return true;
+          };
+          if (ok && n > 0) ok = mbar_wait_bounded(&sh.q_full, i & 1, p.c.err, DERR_FULL_WAIT) && scores(t);
+          for (int k = 0; k < n && ok; ++k) {
+            const int j = 2 * k + t;
+            if (!(ok = landed(base + 2 * j + 1))) break;
+            mbar_arrive(&sh.p_ready[t]);
+            if (!(ok = mbar_wait_bounded(&sh.p_ready[t], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
+            ++steps[t];
+            tc_fence_after();
+            product_o(t, base + 2 * j + 1, k > 0);
+            mma_commit(&sh.kv_empty[stage(base + 2 * j + 1)]);
+            if (k + 1 < n) ok = scores(j + 2);
+            else mma_commit(&sh.o_done[t]);
+          }
+        } else if (me == 0) {
+          // One thread issues every product of both streams.  The tensor core takes an MMA
+          // from it when it starts on it, so what the thread does between two products costs
+          // the tensor core time: a step's O and next S products of a stream go out together, each
+          // wait that can be left to another warp is, and commits are few.  The commit behind
+          // S_t(j + 1) also says that O_t has P_t V_j.
+          auto scores = [&](int t, int j) {
+            product_s(t, t, base + 2 * j);
+            mma_commit(&sh.s_full[t]);
+          };
+          ok = ok && mbar_wait_bounded(&sh.q_full, i & 1, p.c.err, DERR_FULL_WAIT) &&
+               mbar_wait_bounded(&sh.kv_full[stage(base)], phase(base), p.c.err, DERR_FULL_WAIT);
+          tc_fence_after();
+          if (ok) {
+            scores(0, 0);
+            scores(1, 0);
+          }
+          for (int j = 0; j < nk && ok; ++j) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              // P_t(j) is in tensor memory, V_j and K_{j + 1} have landed
+              if (!ok || !(ok = mbar_wait_bounded(&sh.p_ready[t], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
+              ++steps[t];
+              tc_fence_after();
+              product_o(t, base + 2 * j + 1, j > 0);
+              if (j + 1 < nk) scores(t, j + 1);
+              else mma_commit(&sh.o_done[t]);
+            }
+          }
+        }
+      }
+      if (wide && me == 1) {
+        // Waits for V_j and K_{j + 1} on behalf of the MMA thread: P_t(j)'s barriers count
+        // this arrival too.
+        for (int j = 0; j < nk && ok; ++j) {
+          const int v = base + 2 * j + 1;
+          ok = warp_wait(&sh.kv_full[stage(v)], phase(v), p.c.err, DERR_FULL_WAIT);
+          if (ok && j + 1 < nk) ok = warp_wait(&sh.kv_full[stage(v + 1)], phase(v + 1), p.c.err, DERR_FULL_WAIT);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            // one phase of p_ready per step: the one before has to be over
+            if (ok && steps[t] + j > 0) ok = warp_wait(&sh.p_ready[t], (steps[t] + j - 1) & 1, p.c.err, DERR_FULL_WAIT);
+            if (ok && lane == 0) mbar_arrive(&sh.p_ready[t]);
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      // both warps count both streams' steps (those that they made themselves are counted)
+      const int n0 = steps_of(u, 0), n1 = steps_of(u, 1);
+      steps[0] = __shfl_sync(0xffffffffu, steps[0], 0) + (me == 0 ? 0 : n0);
+      steps[1] = __shfl_sync(0xffffffffu, steps[1], 0) + ((wide ? me == 0 : me == 1) ? 0 : n1);
+      ends += n1 > 0;
+      kind_before = u.kind;
+      base += 2 * nk;
+    }
+    if (lane == 0) {  // and so are the products, before tensor memory is given back
+      mma_commit(&sh.drained[me]);
+      mbar_wait_bounded(&sh.drained[me], 0, p.c.err, DERR_DRAIN_WAIT);
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int t = warp >> 2, r = tid & 127;  // stream and row
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = s_col(t) + lane_base, o_at = o_col(t) + lane_base;
+    Work u = unit_at(0);
+    int base = 0, steps = 0, ends = 0;
+    bool ok = true;
+    for (int i = 0; u.kind && ok; u = unit_at(++i)) {
+      const bool wide = u.kind == 2;
+      const int n = steps_of(u, t), nk = u.tiles;
+      const int row = r + (wide ? t * 128 : 0);  // of the unit
+      const bool busy = row - lane < u.rows;     // a row of this warp is the unit's
+      // In wide units stream 1's products come last in a step.  (In narrow ones commits
+      // say that a tile is free.)
+      const bool frees = wide && r == 0 && t == 1;
+      float m = -INFINITY, l = 0.0f;
+      for (int k = 0; k < n && ok; ++k) {
+        const int j = tile_of(u, t, k);
+        if (!(ok = warp_wait(&sh.s_full[t], steps & 1, p.c.err, DERR_FULL_WAIT))) break;
+        ++steps;
+        tc_fence_after();
+        if (frees) {  // the tiles of the products before are free
+          if (j > 0) mbar_arrive(&sh.kv_empty[stage(base + 2 * j - 1)]);
+          mbar_arrive(&sh.kv_empty[stage(base + 2 * j)]);
+        }
+        if (r == 0 && k == n - 1) mbar_arrive(&sh.q_free[t]);  // the stream's last product with Q
+        const int lim = u.have - j * kKeys;                 // keys of the tile that exist
+        if (busy) {
+          uint32_t s[kKeys], ph[kKeys / 2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
+          tmem_wait_ld();
+          tmem_pin<kKeys>(s);
+          if (lim < kKeys) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              if (i >= lim) s[i] = 0xff800000u;  // -inf
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 8)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              mx[w] = max3(mx[w], __uint_as_float(s[i + 2 * w]), __uint_as_float(s[i + 2 * w + 1]));
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (k == 0) {
+            m = mt;
+          } else if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
+            // some row's maximum has grown too far: this warp's rows of O and l go over to
+            // the new maxima (O has every product before: S_t came after)
+            const float mn = fmaxf(m, mt);
+            const float a = m == mn ? 1.0f : ex2((m - mn) * c);
+            m = mn;
+            l *= a;
+#pragma unroll 1
+            for (int i = 0; i < HD; i += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + i, o);
+              tmem_wait_ld();
+              tmem_pin<16>(o);
+#pragma unroll
+              for (int w = 0; w < 16; ++w) o[w] = __float_as_uint(__uint_as_float(o[w]) * a);
+              tmem_st16(o_at + i, o);
+            }
+          }
+          // a row that has seen nothing yet has m = -inf: its P is 0
+          const float mc = m == -INFINITY ? 0.0f : m * c;
+          const uint64_t c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 2) {
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2));
+            const float e0 = ex2(x.x), e1 = ex2(x.y);
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(e0, e1));
+            const __half2 h = __floats2half2_rn(e0, e1);
+            ph[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          const float2 st = unpack2(add2(sum[0], sum[1]));
+          l += st.x + st.y;
+#pragma unroll
+          for (int i = 0; i < kKeys / 2; i += 16) tmem_st16(s_at + i, ph + i);
+          tmem_wait_st();
+        }
+        if (lim < kKeys) {
+          // slots behind the last token hold anything: their V becomes zero
+          const int v = base + 2 * j + 1;
+          if (!(ok = warp_wait(&sh.kv_full[stage(v)], phase(v), p.c.err, DERR_FULL_WAIT))) break;
+          uint8_t* tile = tiles + (2 + stage(v)) * S::kTile;
+          for (int i = lim * 8 + r; i < kKeys * 8; i += 128)
+#pragma unroll
+            for (int half = 0; half < S::H; ++half)
+              *reinterpret_cast<uint4*>(tile + (i >> 6) * S::kRows8 + half * 1024 + (i & 63) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.p_ready[t]);
+      }
+      if (ok && n > 0) ok = warp_wait(&sh.o_done[t], ends & 1, p.c.err, DERR_FULL_WAIT);
+      ends += n > 0;
+      tc_fence_after();
+      if (frees) mbar_arrive(&sh.kv_empty[stage(base + 2 * nk - 1)]);
+      // the part: a thread has its row of O, 32 bytes a store
+      if (ok && n > 0 && busy) {
+        const Scratch to = scratch_of<G>(p, u.kind == 3);
+        const int64_t at = u.slot + row + (wide ? 0 : t * u.rows);
+        float* o_to = to.o + at * HD;
+#pragma unroll 1
+        for (int i = 0; i < HD; i += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_at + i, o);
+          tmem_wait_ld();
+          tmem_pin<32>(o);
+          if (row < u.rows) {
+#pragma unroll
+            for (int w = 0; w < 32; w += 8) st_global_v8(o_to + i + w, o + w);
+          }
+        }
+        if (row < u.rows) *reinterpret_cast<float2*>(to.ml + at * 2) = make_float2(m * c, l);
+      }
+      tc_fence_before();
+      base += 2 * nk;
+    }
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// o is a mean of fp16 values and no larger than they are.  P's rounding may take it past the
+// largest one by up to 2^-11 of it, which would be infinite in fp16.
+EE_DEV float within_half(float y) {
+  return fabsf(y) > 65504.0f && fabsf(y) < INFINITY ? copysignf(65504.0f, y) : y;
+}
+
+// The join: a CTA per sequence and query head adds its row's parts, of the prefix and of its own
+// blocks, every fourth one a warp, eight of them in flight.
+template <int HD, int G>
+__global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int pieces) {
+  constexpr int P = HD / 32, U = 8;  // dims per lane; parts in flight
+  __shared__ int64_t from[4 * kMaxPieces];  // rows of the parts; -1: none
+  __shared__ float ms[4], ls[4], outs[4][HD];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s = blockIdx.x / p.n_heads, head = blockIdx.x - s * p.n_heads, g = head / G, h = head % G;
+  Plan<G> plan;
+  plan.init(p, pieces);
+  const int n = plan.of(plan.tokens, s), own_x = plan.pre_end + plan.of(plan.base, s) * plan.hkv + g * plan.of(plan.cost, s);
+  const int own = plan.own_tiles(n), pre = plan.first_own(n) > 0 ? (plan.pre + 7) >> 3 : 0;
+  int count = 0;
+  // the parts of one unit: two a piece (of a wide unit one)
+  auto list = [&](int x, int tiles, int cost, int64_t slot, int64_t step, int rows, int row, bool wide) {
+    if (tiles == 0) return;
+    const int i0 = x / plan.each, i1 = (tiles == 1 ? x : x + kStartCost + (tiles - 1) * cost) / plan.each;
+    for (int i = i0 + tid; i <= i1; i += 128) {
+      const int k = Plan<G>::tile_at((i + 1) * plan.each, x, tiles, cost) - Plan<G>::tile_at(i * plan.each, x, tiles, cost);
+      const int64_t at = slot + i * step + row;
+      from[count + 2 * (i - i0)] = k > 0 ? at : -1;
+      from[count + 2 * (i - i0) + 1] = k > 1 && !wide ? at + rows : -1;
+    }
+    count += 2 * (i1 - i0 + 1);
+  };
+  const int all = s * G + h, rt = all >> 8, R = prefix_rows(p.batch, G);
+  const bool wide = plan.rows_of(rt) > 128;
+  list(rt * plan.hkv * plan.pre_cost[0] + g * plan.pre_cost[rt], pre, wide ? kWideCost : kNarrowCost,
+       (int64_t)(rt * plan.hkv + g) * R, R, plan.rows_of(rt), all & 255, wide);
+  const int n_pre = count;
+  list(own_x, own, kOwnCost, ((int64_t)s * plan.hkv + g) * 2 * G, 2 * G, G, h, false);
+  const Scratch sp = scratch_of<G>(p, false), so = scratch_of<G>(p, true);
+  grid_dep_wait();
+  __syncthreads();
+  float m = -INFINITY, l = 0.0f, o[P] = {};
+  for (int k0 = warp; k0 < count; k0 += 4 * U) {
+    float2 ml[U];
+    float ok[U][P];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 4 * u;
+      const int64_t at = k < count ? from[k] : -1;
+      const Scratch& sc = k < n_pre ? sp : so;
+      ml[u] = at >= 0 ? *reinterpret_cast<const float2*>(sc.ml + at * 2) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) ok[u][i] = at >= 0 ? sc.o[at * HD + i * 32 + lane] : 0.0f;
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+    const float a = l == 0.0f ? 0.0f : m == mn ? 1.0f : ex2(m - mn);
     m = mn;
-    l = l * a + e;
-    for (int i = 0; i < N; ++i) o[i] = o[i] * a + e * __half2float(__ushort_as_half(p.c.v[k * HD + i * 32 + lane]));
+    l *= a;
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] *= a;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // f may go to 0, or be it where nothing was seen: an infinity or NaN of O and l stays
+      const float f = ml[u].y == 0.0f ? 0.0f : ml[u].x == m ? 1.0f : ex2(ml[u].x - m);
+      l = fmaf(f, ml[u].y, l);
+#pragma unroll
+      for (int i = 0; i < P; ++i) o[i] = fmaf(f, ok[u][i], o[i]);
+    }
   }
-  for (int i = 0; i < N; ++i) {
-    const float x = l == 0.0f ? o[i] : o[i] / l;
-    p.o[s * p.o_stride + h * HD + i * 32 + lane] =
-        float_to_half_bits(fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x);
+  if (lane == 0) {
+    ms[warp] = m;
+    ls[warp] = l;
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i) outs[warp][i * 32 + lane] = o[i];
+  __syncthreads();
+  if (tid < HD) {
+    const float mm = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+    float sum = 0.0f, y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = ls[w] == 0.0f ? 0.0f : ms[w] == mm ? 1.0f : ex2(ms[w] - mm);
+      sum = fmaf(f, ls[w], sum);
+      y = fmaf(f, outs[w][tid], y);
+    }
+    const float il = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // NaN stays
+    p.o[s * p.o_stride + head * HD + tid] = float_to_half_bits(within_half(y * il));
+  }
+}
+
+template <int HD, int G>
+cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
+  using S = Shape<HD>;
+  static std::atomic<uint64_t> prepared{0};  // a bit per device
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(k_shared_attention<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    // the exchange of registers above counts on the launch's share
+    cudaFuncAttributes at;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_shared_attention<HD, G>);
+    if (e == cudaSuccess && at.numRegs != kRegs) e = cudaErrorInvalidConfiguration;
+    if (e != cudaSuccess) return e;
+    if (dev < 64) prepared.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  Maps maps;
+  const uint64_t qd[3] = {(uint64_t)HD, (uint64_t)p.n_heads, (uint64_t)p.batch};
+  const uint64_t qs[2] = {(uint64_t)HD * 2, (uint64_t)p.q_stride * 2};
+  const uint32_t qb[3] = {64, (uint32_t)G, 128 / (uint32_t)G}, q1[3] = {64, (uint32_t)G, 1};
+  // a block of K or V at once, as groups of 8 rows: [group][half][8][64]
+  const uint64_t cd[4] = {64, 8, (uint64_t)S::H, (uint64_t)p.c.n_blocks * p.c.n_kv_heads * 2},
+                 cs[3] = {(uint64_t)HD * 2, 128, (uint64_t)HD * 16};
+  const uint32_t cb[4] = {64, 8, (uint32_t)S::H, 2};
+  if (!encode_tensor_map(&maps.q, false, 3, p.q, qd, qs, qb) || !encode_tensor_map(&maps.q1, false, 3, p.q, qd, qs, q1) ||
+      !encode_tensor_map(&maps.k, false, 4, p.c.k, cd, cs, cb) || !encode_tensor_map(&maps.v, false, 4, p.c.v, cd, cs, cb))
+    return cudaErrorInvalidValue;
+  // a CTA per SM, but none without a tile
+  const int64_t own = (int64_t)p.batch * p.c.n_kv_heads * ((p.c.max_ctx + kKeys - 1) / kKeys);
+  const int64_t pre = (int64_t)((p.batch * G + 255) / 256) * p.c.n_kv_heads * ((p.prefix + kKeys - 1) / kKeys);
+  const int pieces = (int)std::min<int64_t>(std::min(sms, kMaxPieces), own + pre);
+  k_shared_attention<HD, G><<<pieces, kThreads, S::kSmem, st>>>(p, maps, make_exponent(HD).c);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(p.batch * p.n_heads));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join<HD, G>, p, pieces);
 }
 
 }  // namespace
 
 cudaError_t launch_shared_attention(const DecodeParams& p, cudaStream_t st) {
-  const unsigned n = (unsigned)(p.batch * p.n_heads + 3) / 4;
-  if (p.c.head_dim == 64) k_shared_attention<64><<<n, 128, 0, st>>>(p);
-  else k_shared_attention<128><<<n, 128, 0, st>>>(p);
-  return cudaGetLastError();
+  const int G = p.n_heads / p.c.n_kv_heads, hd = p.c.head_dim;
+#define EE_SHARED_CASE(HD_, G_) \
+  if (hd == HD_ && G == G_) return launch_t<HD_, G_>(p, st);
+  EE_SHARED_CASE(64, 1)
+  EE_SHARED_CASE(64, 2)
+  EE_SHARED_CASE(64, 4)
+  EE_SHARED_CASE(64, 8)
+  EE_SHARED_CASE(128, 1)
+  EE_SHARED_CASE(128, 2)
+  EE_SHARED_CASE(128, 4)
+  EE_SHARED_CASE(128, 8)
+#undef EE_SHARED_CASE
+  return cudaErrorInvalidValue;
 }
 
-size_t shared_attention_scratch(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) { return 16; }
+size_t shared_attention_scratch(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t, int32_t prefix) {
+  const int64_t rows = scratch_rows(batch, n_heads / n_kv_heads, n_kv_heads, prefix >= EE_KV_BLOCK ? prefix : 0);
+  return (size_t)rows * (head_dim + 2) * 4 + 32;
+}
 
 }  // namespace ee
