@@ -53,6 +53,7 @@ struct Shape {
   static constexpr uint32_t kHalf = 128 * 128;     // a 64-column half of Q's
   static constexpr uint32_t kRows8 = H * 1024;     // 8 tokens of K or V: [half][8][64]
   static constexpr int NST = HD == 128 ? 5 : 9;    // ring tiles: as many as fit
+  static constexpr int D = (NST - 1) / 4;          // K tiles, and V tiles, of a stream in narrow units
   static constexpr size_t kSmem = 1024 + (2 + NST) * (size_t)kTile;
 };
 
@@ -66,6 +67,8 @@ struct Work {
   int kind;  // 0: no more, 1: narrow, 2: wide; 3: a sequence's own (narrow)
   int s, g, row, first, tiles, have, rows;
   int64_t slot;  // of its part's first row
+  uint32_t par;  // bit i: of place i's tiles before this unit, odd or even
+  int start;     // of a wide unit in the ring
 };
 
 // The parts in the scratch: rows of O and of (m, l), first the prefix's.
@@ -193,7 +196,7 @@ constexpr int kUnits = 4;  // units known ahead
 template <int HD>
 struct Shared {
   static constexpr int NST = Shape<HD>::NST;
-  uint64_t q_full, q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full[2], q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
   uint64_t unit_full[kUnits], unit_free[kUnits];
   uint64_t drained[2];  // every MMA issued is over
   Work unit[kUnits];
@@ -210,7 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dep_launch();
   if (tid == 0) {
-    mbar_init(&sh.q_full, 1);
     for (int i = 0; i < S::NST; ++i) {
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 1);
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
       mbar_init(&sh.p_ready[t], 129);  // its warpgroup, and the tiles that the products need
+      mbar_init(&sh.q_full[t], 1);
       mbar_init(&sh.q_free[t], 1);   // the stream's last product with it
       mbar_init(&sh.o_done[t], 1);
       mbar_init(&sh.drained[t], 1);
@@ -237,11 +240,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tensor memory: S_t (128 columns, P_t over its first 64), then O_t
   auto s_col = [&](int t) { return tmem + t * 128; };
   auto o_col = [&](int t) { return tmem + 256 + t * HD; };
-  // Ring items count on over the units: item base + 2 j is K of the unit's key tile j, item
-  // base + 2 j + 1 its V.
-  auto stage = [&](int i) { return i % S::NST; };
-  auto phase = [&](int i) { return (uint32_t)(i / S::NST) & 1; };
-
   // Unit i of this CTA, found by warp 11.
   auto unit_at = [&](int i) {
     Work u;
@@ -253,20 +251,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return u;
   };
-  // Steps of stream t in a unit, and the key tile of step i.
+  // Steps of stream t in a unit, and the key tile of step k.
   auto steps_of = [](const Work& u, int t) { return u.kind == 2 ? u.tiles : (u.tiles + 1 - t) >> 1; };
-  auto tile_of = [](const Work& u, int t, int i) { return u.kind == 2 ? i : 2 * i + t; };
+  auto tile_of = [](const Work& u, int t, int k) { return u.kind == 2 ? k : 2 * k + t; };
+  // Places in the ring.  A wide unit's K and V follow each other through all of it.  In
+  // narrow units each stream has places of its own: then a place's tiles are waited for by one
+  // thread, one after another, and however far a stream falls behind, the other cannot take
+  // a phase of its barriers for the next one.
+  struct Place {
+    int at;
+    uint32_t phase;
+  };
+  auto narrow_place = [](const Work& u, int t, int k, int kv) {
+    Place x;
+    x.at = t * 2 * S::D + k % S::D * 2 + kv;
+    x.phase = (u.par >> x.at ^ (uint32_t)(k / S::D)) & 1;
+    return x;
+  };
+  auto wide_place = [](const Work& u, int j, int kv) {
+    Place x;
+    x.at = (u.start + 2 * j + kv) % S::NST;
+    x.phase = (u.par >> x.at ^ (uint32_t)((2 * j + kv) / S::NST)) & 1;
+    return x;
+  };
+  auto landed = [&](const Place& x) {
+    const bool r = mbar_wait_bounded(&sh.kv_full[x.at], x.phase, p.c.err, DERR_FULL_WAIT);
+    tc_fence_after();
+    return r;
+  };
 
   constexpr uint32_t id_qk = instr_desc(0, kKeys, 128), id_pv = instr_desc(0, HD, 128, true);
-  auto product_s = [&](int t, int q, int item) {  // S_t = Q tile q, K in ring item
-    const uint32_t a = q_s + q * S::kTile, b = kv_s + stage(item) * S::kTile;
+  auto product_s = [&](int t, const Place& k) {  // S_t = Q_t K at a place
+    const uint32_t a = q_s + t * S::kTile, b = kv_s + k.at * S::kTile;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk)
       mma_f16(s_col(t), smem_desc_sw128(a + (kk >> 2) * S::kHalf + (kk & 3) * 32),
               smem_desc_sw128(b + (kk >> 2) * 1024 + (kk & 3) * 32, S::kRows8), id_qk, kk > 0);
   };
-  auto product_o = [&](int t, int item, bool acc) {  // O_t (+)= P_t, V in ring item
-    const uint32_t b = kv_s + stage(item) * S::kTile;
+  auto product_o = [&](int t, const Place& v, bool acc) {  // O_t (+)= P_t, V at a place
+    const uint32_t b = kv_s + v.at * S::kTile;
 #pragma unroll
     for (int kk = 0; kk < kKeys / 16; ++kk)
       mma_f16_ta(o_col(t), s_col(t) + kk * 8, smem_desc_sw128_mn(b + kk * 2 * S::kRows8, 1024, S::kRows8), id_pv, acc || kk > 0);
@@ -281,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Plan<G> plan;
     plan.init(p, gridDim.x);
     const int me = blockIdx.x, stop = min(plan.total, (me + 1) * plan.each);
-    int i = 0;
+    int i = 0, start = 0;
+    uint32_t par = 0;
     bool ok = true;
     for (int at = me * plan.each; ok;) {
       Work w;
@@ -291,6 +315,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         w = plan.at(at, me, &end);
         at = end;
         if (w.tiles == 0) continue;
+      }
+      w.par = par;
+      w.start = start;
+      if (w.kind == 2) {
+#pragma unroll
+        for (int x = 0; x < S::NST; ++x) {
+          const int first = (x - start + S::NST) % S::NST;
+          par ^= first < 2 * w.tiles ? (uint32_t)((2 * w.tiles - first + S::NST - 1) / S::NST & 1) << x : 0;
+        }
+        start = (start + 2 * w.tiles) % S::NST;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4 * S::D; ++x) {
+          const int first = x % (2 * S::D) / 2, n = steps_of(w, x / (2 * S::D));
+          par ^= first < n ? (uint32_t)((n - first + S::D - 1) / S::D & 1) << x : 0;
+        }
       }
       if (i >= kUnits) ok = warp_wait(&sh.unit_free[i % kUnits], (i / kUnits - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
       if (!ok) break;
@@ -305,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 8) {
     Work u = unit_at(0);
     const int b8 = lane & 7;
-    int issued = 0, loads = 0, ends[2] = {0, 0};
+    int start = 0, ends[2] = {0, 0};
+    uint32_t par = 0;  // as in Work, but for every tile
     bool ok = true;
     for (int i = 0; u.kind && ok; u = unit_at(++i)) {
       const int nblk = (u.have + 15) >> 4;
@@ -319,85 +360,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return id;
       };
-      int id = block_id(0);
-      // q_free: the products of the units before have read their Q
+      // of the next two key tiles
+      int id0 = block_id(0), id1 = block_id(1);
+      start = u.start;
+      // each stream's Q, in a wide unit its rows; q_free: the stream's products before have read theirs
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
+        if (steps_of(u, t) == 0) continue;
         if (ok && ends[t] > 0) ok = warp_wait(&sh.q_free[t], (ends[t] - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
-        ends[t] += steps_of(u, t) > 0;
+        if (!ok) break;
+        ++ends[t];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.q_full[t], u.kind == 3 ? G * HD * 2 : S::kTile);
+          for (int h = 0; h < S::H; ++h)
+            tma_load_3d(q_s + t * S::kTile + h * S::kHalf, u.kind == 3 ? &maps.q1 : &maps.q, h * 64, u.g * G,
+                        u.s + (u.kind == 2 ? t * (128 / G) : 0), &sh.q_full[t]);
+        }
+        __syncwarp();
       }
       if (!ok) break;
-      ++loads;
-      if (lane == 0) {
-        const uint32_t bytes = u.kind == 3 ? G * HD * 2 : u.kind * S::kTile;
-        mbar_arrive_expect_tx(&sh.q_full, bytes);
-        for (int h = 0; h < S::H; ++h) {
-          if (u.kind == 3) tma_load_3d(q_s + h * S::kHalf, &maps.q1, h * 64, u.g * G, u.s, &sh.q_full);
-          else
-            for (int t = 0; t < u.kind; ++t)
-              tma_load_3d(q_s + t * S::kTile + h * S::kHalf, &maps.q, h * 64, u.g * G, u.s + t * (128 / G), &sh.q_full);
+      auto load = [&](int j, int kv, int id, int at) {
+        const int here = min(8, nblk - j * 8);
+        if (!ok || !(ok = warp_wait(&sh.kv_empty[at], (par >> at ^ 1) & 1, p.c.err, DERR_EMPTY_WAIT))) return;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at], (uint32_t)here * 16 * HD * 2);
+        __syncwarp();
+        if (lane < here)
+          tma_load_4d(kv_s + at * S::kTile + lane * 2 * S::kRows8, kv ? &maps.v : &maps.k, 0, 0, 0,
+                      (id * p.c.n_kv_heads + u.g) * 2, &sh.kv_full[at]);
+        par ^= 1u << at;
+      };
+      for (int j = 0; j < u.tiles && ok; j += 2) {
+        const int a = id0, b = id1;
+        id0 = block_id(j + 2);
+        id1 = block_id(j + 3);
+        if (u.kind == 2) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (j + (x >> 1) < u.tiles) {
+              load(j + (x >> 1), x & 1, x < 2 ? a : b, start);
+              start = start + 1 == S::NST ? 0 : start + 1;
+            }
+          }
+        } else {
+          // K of both streams before their V, whose places are free later
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (j + (x & 1) < u.tiles) load(j + (x & 1), x >> 1, x & 1 ? b : a, narrow_place(u, x & 1, j >> 1, x >> 1).at);
         }
-      }
-      __syncwarp();
-      for (int j = 0; j < u.tiles && ok; ++j) {
-        const int next = block_id(j + 1), here = min(8, nblk - j * 8);
-        for (int kv = 0; kv < 2; ++kv, ++issued) {
-          const int st = stage(issued);
-          if (issued >= S::NST) ok = warp_wait(&sh.kv_empty[st], phase(issued - S::NST), p.c.err, DERR_EMPTY_WAIT);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], (uint32_t)here * 16 * HD * 2);
-          __syncwarp();
-          if (lane < here)
-            tma_load_4d(kv_s + st * S::kTile + lane * 2 * S::kRows8, kv ? &maps.v : &maps.k, 0, 0, 0,
-                        (id * p.c.n_kv_heads + u.g) * 2, &sh.kv_full[st]);
-        }
-        id = next;
       }
     }
     // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
-    for (int i = max(0, issued - S::NST); i < issued; ++i)
-      mbar_wait_bounded(&sh.kv_full[stage(i)], phase(i), p.c.err, DERR_DRAIN_WAIT);
-    if (loads > 0) mbar_wait_bounded(&sh.q_full, (loads - 1) & 1, p.c.err, DERR_DRAIN_WAIT);
+    for (int x = 0; x < S::NST; ++x) mbar_wait_bounded(&sh.kv_full[x], (par >> x ^ 1) & 1, p.c.err, DERR_DRAIN_WAIT);
+    for (int t = 0; t < 2; ++t)
+      if (ends[t] > 0) mbar_wait_bounded(&sh.q_full[t], (ends[t] - 1) & 1, p.c.err, DERR_DRAIN_WAIT);
   } else {
     // Warps 9 and 10.
     const int me = warp - 9;
     Work u = unit_at(0);
-    int base = 0, steps[2] = {0, 0}, ends = 0, kind_before = 0;
+    int steps[2] = {0, 0}, ends[2] = {0, 0}, kind_before = 0;
     bool ok = true;
     for (int i = 0; u.kind && ok; u = unit_at(++i)) {
       const int nk = u.tiles;
       const bool wide = u.kind == 2;
-      // Stream 1's products go from one warp to the other where wide and narrow units meet:
-      // the first ones wait for the last ones of the other.
-      const bool change = (kind_before == 2) != wide && ends > 0 && me == (wide ? 0 : 1);
+      // Behind the wide units stream 1's products go from warp 9 to warp 10: the first ones
+      // wait for the last ones there (and for P first: then no older O is taken for the last).
+      const bool change = me == 1 && kind_before == 2 && !wide;
       if (lane == 0) {
-        if (change) ok = mbar_wait_bounded(&sh.o_done[1], (ends - 1) & 1, p.c.err, DERR_FULL_WAIT);
+        if (change)
+          ok = mbar_wait_bounded(&sh.p_ready[1], (steps[1] - 1) & 1, p.c.err, DERR_FULL_WAIT) &&
+               mbar_wait_bounded(&sh.o_done[1], (ends[1] - 1) & 1, p.c.err, DERR_FULL_WAIT);
+        auto q_there = [&](int t) {
+          const bool r = mbar_wait_bounded(&sh.q_full[t], ends[t] & 1, p.c.err, DERR_FULL_WAIT);
+          tc_fence_after();
+          return r;
+        };
         if (!wide) {
           // a stream by itself: each product as soon as its tile is there
           const int t = me, n = steps_of(u, t);
-          auto landed = [&](int item) {
-            const bool r = mbar_wait_bounded(&sh.kv_full[stage(item)], phase(item), p.c.err, DERR_FULL_WAIT);
-            tc_fence_after();
-            return r;
-          };
-          auto scores = [&](int j) {
-            if (!landed(base + 2 * j)) return false;
-            product_s(t, 0, base + 2 * j);
+          auto scores = [&](int k) {
+            const Place x = narrow_place(u, t, k, 0);
+            if (!landed(x)) return false;
+            product_s(t, x);
             mma_commit(&sh.s_full[t]);
-            mma_commit(&sh.kv_empty[stage(base + 2 * j)]);
+            mma_commit(&sh.kv_empty[x.at]);
             return true;
           };
-          if (ok && n > 0) ok = mbar_wait_bounded(&sh.q_full, i & 1, p.c.err, DERR_FULL_WAIT) && scores(t);
+          if (ok && n > 0) ok = q_there(t) && scores(0);
           for (int k = 0; k < n && ok; ++k) {
-            const int j = 2 * k + t;
-            if (!(ok = landed(base + 2 * j + 1))) break;
+            const Place v = narrow_place(u, t, k, 1);
+            if (!(ok = landed(v))) break;
             mbar_arrive(&sh.p_ready[t]);
             if (!(ok = mbar_wait_bounded(&sh.p_ready[t], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
             ++steps[t];
             tc_fence_after();
-            product_o(t, base + 2 * j + 1, k > 0);
-            mma_commit(&sh.kv_empty[stage(base + 2 * j + 1)]);
-            if (k + 1 < n) ok = scores(j + 2);
+            product_o(t, v, k > 0);
+            mma_commit(&sh.kv_empty[v.at]);
+            if (k + 1 < n) ok = scores(k + 1);
             else mma_commit(&sh.o_done[t]);
           }
         } else if (me == 0) {
@@ -407,12 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // wait that can be left to another warp is, and commits are few.  The commit behind
           // S_t(j + 1) also says that O_t has P_t V_j.
           auto scores = [&](int t, int j) {
-            product_s(t, t, base + 2 * j);
+            product_s(t, wide_place(u, j, 0));
             mma_commit(&sh.s_full[t]);
           };
-          ok = ok && mbar_wait_bounded(&sh.q_full, i & 1, p.c.err, DERR_FULL_WAIT) &&
-               mbar_wait_bounded(&sh.kv_full[stage(base)], phase(base), p.c.err, DERR_FULL_WAIT);
-          tc_fence_after();
+          ok = ok && q_there(0) && q_there(1) && landed(wide_place(u, 0, 0));
           if (ok) {
             scores(0, 0);
             scores(1, 0);
@@ -424,20 +480,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok || !(ok = mbar_wait_bounded(&sh.p_ready[t], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
               ++steps[t];
               tc_fence_after();
-              product_o(t, base + 2 * j + 1, j > 0);
+              product_o(t, wide_place(u, j, 1), j > 0);
               if (j + 1 < nk) scores(t, j + 1);
               else mma_commit(&sh.o_done[t]);
             }
           }
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
       if (wide && me == 1) {
         // Waits for V_j and K_{j + 1} on behalf of the MMA thread: P_t(j)'s barriers count
         // this arrival too.
         for (int j = 0; j < nk && ok; ++j) {
-          const int v = base + 2 * j + 1;
-          ok = warp_wait(&sh.kv_full[stage(v)], phase(v), p.c.err, DERR_FULL_WAIT);
-          if (ok && j + 1 < nk) ok = warp_wait(&sh.kv_full[stage(v + 1)], phase(v + 1), p.c.err, DERR_FULL_WAIT);
+          const Place v = wide_place(u, j, 1), k = wide_place(u, j + 1, 0);
+          ok = warp_wait(&sh.kv_full[v.at], v.phase, p.c.err, DERR_FULL_WAIT);
+          if (ok && j + 1 < nk) ok = warp_wait(&sh.kv_full[k.at], k.phase, p.c.err, DERR_FULL_WAIT);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             // one phase of p_ready per step: the one before has to be over
@@ -451,9 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = steps_of(u, 0), n1 = steps_of(u, 1);
       steps[0] = __shfl_sync(0xffffffffu, steps[0], 0) + (me == 0 ? 0 : n0);
       steps[1] = __shfl_sync(0xffffffffu, steps[1], 0) + ((wide ? me == 0 : me == 1) ? 0 : n1);
-      ends += n1 > 0;
+      ends[0] += n0 > 0;
+      ends[1] += n1 > 0;
       kind_before = u.kind;
-      base += 2 * nk;
     }
     if (lane == 0) {  // and so are the products, before tensor memory is given back
       mma_commit(&sh.drained[me]);
@@ -467,11 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = s_col(t) + lane_base, o_at = o_col(t) + lane_base;
     Work u = unit_at(0);
-    int base = 0, steps = 0, ends = 0;
+    int steps = 0, ends = 0;
     bool ok = true;
     for (int i = 0; u.kind && ok; u = unit_at(++i)) {
       const bool wide = u.kind == 2;
-      const int n = steps_of(u, t), nk = u.tiles;
+      const int n = steps_of(u, t);
       const int row = r + (wide ? t * 128 : 0);  // of the unit
       const bool busy = row - lane < u.rows;     // a row of this warp is the unit's
       // In wide units stream 1's products come last in a step.  (In narrow ones commits
@@ -484,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++steps;
         tc_fence_after();
         if (frees) {  // the tiles of the products before are free
-          if (j > 0) mbar_arrive(&sh.kv_empty[stage(base + 2 * j - 1)]);
-          mbar_arrive(&sh.kv_empty[stage(base + 2 * j)]);
+          if (j > 0) mbar_arrive(&sh.kv_empty[wide_place(u, j - 1, 1).at]);
+          mbar_arrive(&sh.kv_empty[wide_place(u, j, 0).at]);
         }
         if (r == 0 && k == n - 1) mbar_arrive(&sh.q_free[t]);  // the stream's last product with Q
         const int lim = u.have - j * kKeys;                 // keys of the tile that exist
@@ -509,8 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           if (k == 0) {
             m = mt;
-          } else if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
-            // some row's maximum has grown too far: this warp's rows of O and l go over to
+          } else if (__any_sync(0xffffffffu, row < u.rows && (mt - m) * c > 8.0f)) {
+            // some row's maximum has grown too far (rows that are not the unit's have no say: what
+            // they hold depends on what was there before): this warp's rows of O and l go over to
             // the new maxima (O has every product before: S_t came after)
             const float mn = fmaxf(m, mt);
             const float a = m == mn ? 1.0f : ex2((m - mn) * c);
@@ -547,9 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lim < kKeys) {
           // slots behind the last token hold anything: their V becomes zero
-          const int v = base + 2 * j + 1;
-          if (!(ok = warp_wait(&sh.kv_full[stage(v)], phase(v), p.c.err, DERR_FULL_WAIT))) break;
-          uint8_t* tile = tiles + (2 + stage(v)) * S::kTile;
+          const Place v = wide ? wide_place(u, j, 1) : narrow_place(u, t, k, 1);
+          if (!(ok = warp_wait(&sh.kv_full[v.at], v.phase, p.c.err, DERR_FULL_WAIT))) break;
+          uint8_t* tile = tiles + (2 + v.at) * S::kTile;
           for (int i = lim * 8 + r; i < kKeys * 8; i += 128)
 #pragma unroll
             for (int half = 0; half < S::H; ++half)
@@ -562,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && n > 0) ok = warp_wait(&sh.o_done[t], ends & 1, p.c.err, DERR_FULL_WAIT);
       ends += n > 0;
       tc_fence_after();
-      if (frees) mbar_arrive(&sh.kv_empty[stage(base + 2 * nk - 1)]);
+      if (frees) mbar_arrive(&sh.kv_empty[wide_place(u, u.tiles - 1, 1).at]);
       // the part: a thread has its row of O, 32 bytes a store
       if (ok && n > 0 && busy) {
         const Scratch to = scratch_of<G>(p, u.kind == 3);
@@ -582,7 +640,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row < u.rows) *reinterpret_cast<float2*>(to.ml + at * 2) = make_float2(m * c, l);
       }
       tc_fence_before();
-      base += 2 * nk;
     }
   }
   __syncthreads();

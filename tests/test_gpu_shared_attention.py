@@ -95,6 +95,25 @@ def test_long_prefix(hq, hkv, hd):
     h.check(q, hq, max_ctx=16384)
 
 
+@pytest.mark.parametrize("hq,hkv,hd,prefix,most", [(64, 8, 128, 1000, 400), (64, 8, 64, 520, 300), (32, 8, 128, 700, 500), (16, 16, 64, 300, 700)])
+def test_many_units(hq, hkv, hd, prefix, most):
+    """64 sequences: row tiles of all sizes, and CTAs that go through many sequences' own tiles, one
+    or few each, behind a share of the prefix; the same bits every time."""
+    rng = np.random.default_rng(hq + hd)
+    ctxs = [prefix + int(x) for x in np.exp(rng.uniform(0, np.log(most), 64))]
+    ctxs[5], ctxs[20], ctxs[63] = 0, prefix // 2, prefix // 16 * 16
+    h = Shared(11, ctxs, prefix, hkv, hd)
+    q = h.rng.standard_normal((64, hq, hd)).astype(np.float16)
+    h.check(q, hq)
+    args = (dev(q.reshape(64, -1)), dev(h.k), dev(h.v), dev(h.table), dev(np.array(ctxs, np.int32) - 1), prefix, hq, hkv, hd, max(ctxs))
+    err, first = i32(0), None
+    for _ in range(20):
+        o = ee.shared_attention(*args, err=err)
+        first = o if first is None else first
+        assert torch.equal(o, first)
+    assert err.item() == 0
+
+
 def test_prefix_behind_the_longest_sequence():
     """A prefix longer than max_ctx: as much of it as there is."""
     h = Shared(4, [100, 40], 112, 2, 64)
