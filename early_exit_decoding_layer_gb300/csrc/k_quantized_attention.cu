@@ -480,14 +480,19 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
   if (!ok) __nanosleep(1000000);  // what this CTA no longer waited for may be on its way
 }
 
-// The join: a CTA per sequence and query head adds the parts of its pair, where there are
-// any: every fourth one a warp, eight of them in flight, then the four warps' sums.
-template <int HD, int G>
-__global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int pieces, const int least) {
-  constexpr int P = HD / 32, U = 8;  // dims per lane; parts in flight
-  __shared__ float ms[4], ls[4], outs[4][HD];
+// The join: a CTA adds the parts of J query heads of a sequence, where there are any: 8 / J warps
+// each, eight parts in flight a warp.  J is all heads of a kv head where there are many -- CTAs
+// start 6 ns after one another, whatever they do -- and one where there are few (one sequence of
+// 16384 tokens: 13 us, with J = G 17).
+constexpr int kJoinThreads = 256;
+
+template <int HD, int G, int J>
+__global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, const int pieces, const int least) {
+  constexpr int P = HD / 32, U = 8, kStripes = 8 / J;  // dims per lane; parts in flight
+  __shared__ float ms[8], ls[8], outs[8][HD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.x / p.n_heads, head = blockIdx.x - s * p.n_heads, g = head / G, h = head % G;
+  const int s = blockIdx.x / (p.n_heads / J), first = (blockIdx.x - s * (p.n_heads / J)) * J;  // its heads
+  const int g = first / G, h = first % G + warp % J;
   DecodePlan plan;
   plan.init(p, pieces, least, false, 0);
   const int nb = __shfl_sync(0xffffffffu, s < 32 ? plan.blocks[0] : plan.blocks[1], s & 31);
@@ -498,16 +503,25 @@ __global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int pi
   // the first CTA has the pair as its last one, unless it begins with it
   const int late = from > w0 * plan.each;
   float m = -INFINITY, l = 0.0f, o[P] = {};
-  for (int k0 = warp; k0 < n; k0 += 4 * U) {
-    float mk[U], lk[U], ok[U][P];
+  for (int k0 = warp / J; k0 < n; k0 += kStripes * U) {
+    float mk[U], lk[U], x[U][P];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + 4 * u;
-      const float* x = part<HD, G>(p, 2 * (w0 + k) + (k == 0 ? late : 0));
-      mk[u] = k < n ? x[G * HD + h] : -INFINITY;
-      lk[u] = k < n ? x[G * HD + G + h] : 0.0f;
+      const int k = k0 + kStripes * u;
+      const float* y = part<HD, G>(p, 2 * (w0 + k) + (k == 0 ? late : 0));
+      mk[u] = -INFINITY;
+      lk[u] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < P; ++i) ok[u][i] = k < n ? x[h * HD + i * 32 + lane] : 0.0f;
+      for (int i = 0; i < P; ++i) x[u][i] = 0.0f;
+      if (k < n) {
+        mk[u] = y[G * HD + h];
+        lk[u] = y[G * HD + G + h];
+        if constexpr (P == 4 && G > 1) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(y + h * HD + lane * P);
+        else
+#pragma unroll
+          for (int i = 0; i < P; i += 2)
+            *reinterpret_cast<float2*>(x[u] + i) = *reinterpret_cast<const float2*>(y + h * HD + lane * P + i);
+      }
     }
     float mn = m;
 #pragma unroll
@@ -523,7 +537,7 @@ __global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int pi
       const float f = mk[u] == m ? 1.0f : ex2(mk[u] - m);
       l = fmaf(f, lk[u], l);
 #pragma unroll
-      for (int i = 0; i < P; ++i) o[i] = fmaf(f, ok[u][i], o[i]);
+      for (int i = 0; i < P; ++i) o[i] = fmaf(f, x[u][i], o[i]);
     }
   }
   if (lane == 0) {
@@ -531,18 +545,21 @@ __global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int pi
     ls[warp] = l;
   }
 #pragma unroll
-  for (int i = 0; i < P; ++i) outs[warp][i * 32 + lane] = o[i];
+  for (int i = 0; i < P; ++i) outs[warp][lane * P + i] = o[i];
   __syncthreads();
-  if (tid < HD) {
-    const float mm = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-    float sum = 0.0f, y = 0.0f;
+  for (int i = tid; i < J * HD; i += kJoinThreads) {
+    const int head = i / HD, d = i % HD;
+    float mm = -INFINITY, sum = 0.0f, y = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = ms[w] == mm ? 1.0f : ex2(ms[w] - mm);
-      sum = fmaf(f, ls[w], sum);
-      y = fmaf(f, outs[w][tid], y);
+    for (int w = 0; w < kStripes; ++w) mm = fmaxf(mm, ms[w * J + head]);
+#pragma unroll
+    for (int w = 0; w < kStripes; ++w) {
+      const int at = w * J + head;
+      const float f = ms[at] == mm ? 1.0f : ex2(ms[at] - mm);
+      sum = fmaf(f, ls[at], sum);
+      y = fmaf(f, outs[at][d], y);
     }
-    p.o[s * p.o_stride + head * HD + tid] = float_to_half_bits(within_half(__fdividef(y, sum)));
+    p.o[s * p.o_stride + (first + head) * HD + d] = float_to_half_bits(within_half(__fdividef(y, sum)));
   }
 }
 
@@ -576,12 +593,14 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(p.batch * p.n_heads));
-  cfg.blockDim = dim3(128);
+  const bool few = p.batch * p.n_heads <= 2 * sms;
+  cfg.gridDim = dim3((unsigned)(p.batch * (few ? p.n_heads : p.c.n_kv_heads)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_join<HD, G>, p, pieces, least);
+  return few ? cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, pieces, least)
+             : cudaLaunchKernelEx(&cfg, k_join<HD, G, G>, p, pieces, least);
 }
 
 }  // namespace

@@ -982,27 +982,32 @@ EE_DEV float within_half(float y) {
   return fabsf(y) > 65504.0f && fabsf(y) < INFINITY ? copysignf(65504.0f, y) : y;
 }
 
-// The join: a CTA per sequence and query head adds its row's parts, of the prefix and of its own
-// blocks, every fourth one a warp, eight of them in flight.
-template <int HD, int G>
-__global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int sms) {
-  constexpr int P = HD / 32, U = 8;  // dims per lane; parts in flight
-  __shared__ int64_t ml_at[4 * kMaxPieces], o_at[4 * kMaxPieces];  // where the parts are; -1: none
-  __shared__ float ms[4], ls[4], outs[4][HD];
+// The join: a CTA adds the parts, of the prefix and of its own blocks, of J query heads of a
+// sequence: 8 / J warps each, eight parts in flight a warp.  J is all heads of a kv head where
+// there are many -- CTAs start 6 ns after one another, whatever they do: one for each of 4096 rows
+// took 20 us -- and one where there are few.
+constexpr int kJoinThreads = 256;
+
+template <int HD, int G, int J>
+__global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, const int sms) {
+  constexpr int P = HD / 32, U = 8, kStripes = 8 / J;  // dims per lane; parts in flight
+  __shared__ int64_t ml_at[4 * kMaxPieces], o_at[4 * kMaxPieces];  // where head 0's parts are; -1: none
+  __shared__ float ms[8], ls[8], outs[8][HD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.x / p.n_heads, head = blockIdx.x - s * p.n_heads, g = head / G, h = head % G;
+  const int s = blockIdx.x / (p.n_heads / J), first = (blockIdx.x - s * (p.n_heads / J)) * J;  // its heads
+  const int g = first / G, h = first % G + warp % J;
   Plan<G> plan;
   plan.init(p, sms);
   const int n = plan.of(plan.tokens, s), own_x = plan.of(plan.base, s) * plan.hkv + g * plan.of(plan.size, s);
   const int own = plan.own_blocks(n), pre = plan.first_own(n) > 0 ? (plan.pre + 7) >> 3 : 0;
-  const int all = s * G + h, rt = all >> 8, row = all & 255, rows = plan.rows_of(rt), R = prefix_rows(p.batch, G);
+  const int all = s * G, rt = all >> 8, row = all & 255, rows = plan.rows_of(rt), R = prefix_rows(p.batch, G);
   const bool wide = rows > 128;
   int n_pre = 0, count = 0;
   // the prefix's parts: one a piece of a wide unit, of a narrow one two
   if (pre > 0) {
     const int cost = wide ? kWideCost : kNarrowCost, x = rt * plan.hkv * plan.pre_cost[0] + g * plan.pre_cost[rt];
     const int i0 = x / plan.each_pre, i1 = (pre == 1 ? x : x + kStartCost + (pre - 1) * cost) / plan.each_pre;
-    for (int i = i0 + tid; i <= i1; i += 128) {
+    for (int i = i0 + tid; i <= i1; i += kJoinThreads) {
       const int k = Plan<G>::item_at((i + 1) * plan.each_pre, x, pre, kStartCost, cost) -
                     Plan<G>::item_at(i * plan.each_pre, x, pre, kStartCost, cost);
       const int64_t slot = rt * plan.hkv + g + i;
@@ -1019,32 +1024,37 @@ __global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int sm
   // and those of its own blocks
   if (own > 0) {
     const int i0 = own_x / plan.each_own, i1 = (own == 1 ? own_x : own_x + kOwnStart + own - 1) / plan.each_own;
-    for (int i = i0 + tid; i <= i1; i += 128) {
+    for (int i = i0 + tid; i <= i1; i += kJoinThreads) {
       const bool has = Plan<G>::item_at((i + 1) * plan.each_own, own_x, own, kOwnStart, 1) >
                        Plan<G>::item_at(i * plan.each_own, own_x, own, kOwnStart, 1);
-      const int64_t at = ((int64_t)s * plan.hkv + g + i) * G + h;
+      const int64_t at = ((int64_t)s * plan.hkv + g + i) * G;
       ml_at[n_pre + i - i0] = has ? at : -1;
       o_at[n_pre + i - i0] = at * HD;
     }
     count += i1 - i0 + 1;
   }
+  // this lane's dims, lane * P and on: eight floats of a prefix row lie together
   const Scratch sp = scratch_of<G>(p, false), so = scratch_of<G>(p, true);
+  const float *pre_o = sp.o + h * 8 + (int64_t)(lane * P / 8) * R * 8 + lane * P % 8, *own_o = so.o + h * HD + lane * P;
   grid_dep_wait();
   __syncthreads();
   float m = -INFINITY, l = 0.0f, o[P] = {};
-  for (int k0 = warp; k0 < count; k0 += 4 * U) {
+  for (int k0 = warp / J; k0 < count; k0 += kStripes * U) {
     float2 ml[U];
-    float ok[U][P];
+    float x[U][P];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + 4 * u;
+      const int k = k0 + kStripes * u;
       const int64_t at = k < count ? ml_at[k] : -1;
-      const Scratch& sc = k < n_pre ? sp : so;
-      const float* x = sc.o + (at >= 0 ? o_at[k] : 0) + (lane & 7);
-      const int chunk = k < n_pre ? R * 8 : 8;
-      ml[u] = at >= 0 ? *reinterpret_cast<const float2*>(sc.ml + at * 2) : make_float2(-INFINITY, 0.0f);
+      ml[u] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-      for (int i = 0; i < P; ++i) ok[u][i] = at >= 0 ? x[(i * 4 + (lane >> 3)) * chunk] : 0.0f;
+      for (int i = 0; i < P; ++i) x[u][i] = 0.0f;
+      if (at >= 0) {
+        ml[u] = *reinterpret_cast<const float2*>((k < n_pre ? sp.ml : so.ml) + (at + h) * 2);
+        const float* from = (k < n_pre ? pre_o : own_o) + o_at[k];
+        if constexpr (P == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(from);
+        else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(from);
+      }
     }
     float mn = m;
 #pragma unroll
@@ -1060,7 +1070,7 @@ __global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int sm
       const float f = ml[u].y == 0.0f ? 0.0f : ml[u].x == m ? 1.0f : ex2(ml[u].x - m);
       l = fmaf(f, ml[u].y, l);
 #pragma unroll
-      for (int i = 0; i < P; ++i) o[i] = fmaf(f, ok[u][i], o[i]);
+      for (int i = 0; i < P; ++i) o[i] = fmaf(f, x[u][i], o[i]);
     }
   }
   if (lane == 0) {
@@ -1068,19 +1078,22 @@ __global__ void __launch_bounds__(128) k_join(const DecodeParams p, const int sm
     ls[warp] = l;
   }
 #pragma unroll
-  for (int i = 0; i < P; ++i) outs[warp][i * 32 + lane] = o[i];
+  for (int i = 0; i < P; ++i) outs[warp][lane * P + i] = o[i];
   __syncthreads();
-  if (tid < HD) {
-    const float mm = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-    float sum = 0.0f, y = 0.0f;
+  for (int i = tid; i < J * HD; i += kJoinThreads) {
+    const int head = i / HD, d = i % HD;
+    float mm = -INFINITY, sum = 0.0f, y = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = ls[w] == 0.0f ? 0.0f : ms[w] == mm ? 1.0f : ex2(ms[w] - mm);
-      sum = fmaf(f, ls[w], sum);
-      y = fmaf(f, outs[w][tid], y);
+    for (int w = 0; w < kStripes; ++w) mm = fmaxf(mm, ms[w * J + head]);
+#pragma unroll
+    for (int w = 0; w < kStripes; ++w) {
+      const int at = w * J + head;
+      const float f = ls[at] == 0.0f ? 0.0f : ms[at] == mm ? 1.0f : ex2(ms[at] - mm);
+      sum = fmaf(f, ls[at], sum);
+      y = fmaf(f, outs[at][d], y);
     }
     const float il = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // NaN stays
-    p.o[s * p.o_stride + head * HD + tid] = float_to_half_bits(within_half(y * il));
+    p.o[s * p.o_stride + (first + head) * HD + d] = float_to_half_bits(within_half(y * il));
   }
 }
 
@@ -1136,10 +1149,11 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   e = cudaLaunchKernelEx(&cfg, k_own<HD, G>, p, maps, c, sms);
   if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)(p.batch * p.n_heads));
-  cfg.blockDim = dim3(128);
+  const bool few = p.batch * p.n_heads <= 2 * sms;
+  cfg.gridDim = dim3((unsigned)(p.batch * (few ? p.n_heads : p.c.n_kv_heads)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_join<HD, G>, p, sms);
+  return few ? cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, sms) : cudaLaunchKernelEx(&cfg, k_join<HD, G, G>, p, sms);
 }
 
 }  // namespace
