@@ -20,7 +20,6 @@
 //   warp 10              narrow: stream 1's products.  wide: waits for K and V tiles in warp
 //                        9's place, which has none of the tensor core's time to lose
 //   warp 8               Q, K and V by TMA, a box per 16-slot block, into a ring
-//   warp 11              finds the CTA's next units of work
 //
 // k_own, two CTAs per SM: S^T = K Q^T and O^T = V^T P with the cache as the big operand, 128 tokens x 16
 // columns, a unit being (sequence, kv head).  With rows as M as above, G of 128 would be
@@ -166,22 +165,28 @@ struct Plan {
   }
   EE_DEV int of(const int (&a)[2], int s) const { return s < 32 ? __shfl_sync(0xffffffffu, a[0], s) : __shfl_sync(0xffffffffu, a[1], s - 32); }
 
-  // The prefix unit that holds place c < pre_end, as far as it lies in piece `me`; *end: its end.
-  EE_DEV Work prefix_at(int c, int me, int* end) const {
+  // The share of CTA `me` of the prefix unit that holds place *c, or of the next one that has any;
+  // *c: behind the unit.
+  EE_DEV Work prefix_at(int* c, int me) const {
     Work w;
-    const int rt = c < hkv * pre_cost[0] ? 0 : 1, c0 = rt * hkv * pre_cost[0];
-    w.g = (c - c0) / pre_cost[rt];
-    const int x = c0 + w.g * pre_cost[rt], tiles = (pre + 7) >> 3;
-    *end = x + pre_cost[rt];
-    w.rows = rows_of(rt);
-    w.kind = w.rows > 128 ? 2 : 1;
-    w.s = rt * 256 / G;
-    w.slot = rt * hkv + w.g + me;
-    const int cost = w.kind == 2 ? kWideCost : kNarrowCost;
-    const int k0 = item_at(me * each_pre, x, tiles, kStartCost, cost), k1 = item_at((me + 1) * each_pre, x, tiles, kStartCost, cost);
-    w.first = k0 * 8;
-    w.have = min(pre * 16, k1 * kKeys) - k0 * kKeys;
-    w.tiles = k1 - k0;
+    const int begin = me * each_pre, stop = min(pre_end, begin + each_pre), tiles = (pre + 7) >> 3;
+    w.kind = w.tiles = 0;
+    while (*c < stop) {
+      const int rt = *c < hkv * pre_cost[0] ? 0 : 1, c0 = rt * hkv * pre_cost[0];
+      w.g = (*c - c0) / pre_cost[rt];
+      const int x = c0 + w.g * pre_cost[rt], cost = rows_of(rt) > 128 ? kWideCost : kNarrowCost;
+      *c = x + pre_cost[rt];
+      const int k0 = item_at(begin, x, tiles, kStartCost, cost), k1 = item_at(stop, x, tiles, kStartCost, cost);
+      if (k1 == k0) continue;
+      w.rows = rows_of(rt);
+      w.kind = w.rows > 128 ? 2 : 1;
+      w.s = rt * 256 / G;
+      w.slot = rt * hkv + w.g + me;
+      w.first = k0 * 8;
+      w.have = min(pre * 16, k1 * kKeys) - k0 * kKeys;
+      w.tiles = k1 - k0;
+      break;
+    }
     return w;
   }
   // The share of CTA `me` of the pair that holds place *c, or of the next one that has any;
@@ -223,17 +228,12 @@ EE_DEV Scratch scratch_of(const DecodeParams& p, bool own) {
   return r;
 }
 
-constexpr int kUnits = 4;  // units known ahead
-
 template <int HD>
 struct Shared {
   static constexpr int NST = Shape<HD>::NST;
   uint64_t q_full[2], q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
-  uint64_t unit_full[kUnits], unit_free[kUnits];
   uint64_t drained[2];  // every MMA issued is over
-  Work unit[kUnits];
   uint32_t tmem;
-  bool idle;  // no piece of the prefix is this CTA's
 };
 
 template <int HD, int G>
@@ -245,17 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* tiles = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dep_launch();
-  Plan<G> plan;
-  if (warp >= 11 || warp == 0) plan.init(p, gridDim.x);
-  if (tid == 0) sh.idle = (int)blockIdx.x >= plan.n_pre;
-  if (warp == 1) {
+  // The loads begin before anything else is ready: their warp makes the barriers, and
+  // does not wait for the others.
+  if (warp == 8) {
     if (lane < S::NST) {
       mbar_init(&sh.kv_full[lane], 1);
       mbar_init(&sh.kv_empty[lane], 1);
-    }
-    if (lane < kUnits) {
-      mbar_init(&sh.unit_full[lane], 1);
-      mbar_init(&sh.unit_free[lane], 11);  // every warp but the one that finds them
     }
     if (lane < 2) {
       mbar_init(&sh.s_full[lane], 1);
@@ -266,31 +261,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.drained[lane], 1);
     }
     fence_mbar_init();
+    __syncwarp();
   }
-  if (warp == 9) tmem_alloc(&sh.tmem, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (sh.idle) {
-    if (warp == 9) tmem_free(sh.tmem, 512);
-    return;
+  Plan<G> plan;
+  plan.init(p, gridDim.x);
+  if ((int)blockIdx.x >= plan.n_pre) return;
+  if (warp == 8) {
+    asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+  } else {
+    if (warp == 9) {
+      tmem_alloc(&sh.tmem, 512);
+      tc_fence_before();
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    tc_fence_after();
   }
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = warp == 8 ? 0 : sh.tmem;
   const uint32_t q_s = smem_addr(tiles), kv_s = q_s + 2 * S::kTile;
   // tensor memory: S_t (128 columns, P_t over its first 64), then O_t
   auto s_col = [&](int t) { return tmem + t * 128; };
   auto o_col = [&](int t) { return tmem + 256 + t * HD; };
-  // Unit i of this CTA, found by warp 11.
-  auto unit_at = [&](int i) {
-    Work u;
-    u.kind = 0;
-    if (warp_wait(&sh.unit_full[i % kUnits], (i / kUnits) & 1, p.c.err, DERR_FULL_WAIT)) {
-      u = sh.unit[i % kUnits];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.unit_free[i % kUnits]);
-    }
-    return u;
-  };
   // Steps of stream t in a unit, and the key tile of step k.
   auto steps_of = [](const Work& u, int t) { return u.kind == 2 ? u.tiles : (u.tiles + 1 - t) >> 1; };
   auto tile_of = [](const Work& u, int t, int k) { return u.kind == 2 ? k : 2 * k + t; };
@@ -313,6 +303,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     x.at = (u.start + 2 * j + kv) % S::NST;
     x.phase = (u.par >> x.at ^ (uint32_t)((2 * j + kv) / S::NST)) & 1;
     return x;
+  };
+  // This CTA's next unit.
+  int c0 = blockIdx.x * plan.each_pre, start = 0;
+  uint32_t par = 0;
+  auto next_unit = [&]() {
+    Work w = plan.prefix_at(&c0, blockIdx.x);
+    w.par = par;
+    w.start = start;
+    if (w.kind == 2) {
+#pragma unroll
+      for (int x = 0; x < S::NST; ++x) {
+        const int first = (x - start + S::NST) % S::NST;
+        par ^= first < 2 * w.tiles ? (uint32_t)((2 * w.tiles - first + S::NST - 1) / S::NST & 1) << x : 0;
+      }
+      start = (start + 2 * w.tiles) % S::NST;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4 * S::D; ++x) {
+        const int first = x % (2 * S::D) / 2, n = steps_of(w, x / (2 * S::D));
+        par ^= first < n ? (uint32_t)((n - first + S::D - 1) / S::D & 1) << x : 0;
+      }
+    }
+    return w;
   };
   auto landed = [&](const Place& x) {
     const bool r = mbar_wait_bounded(&sh.kv_full[x.at], x.phase, p.c.err, DERR_FULL_WAIT);
@@ -340,53 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (launch_t checks that).
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSingle));
-  if (warp == 11) {
-    const int me = blockIdx.x, stop = min(plan.pre_end, (me + 1) * plan.each_pre);
-    int i = 0, start = 0;
-    uint32_t par = 0;
-    bool ok = true;
-    for (int at = me * plan.each_pre; ok;) {
-      Work w;
-      w.kind = w.tiles = 0;
-      int end = 0;
-      if (at < stop) {
-        w = plan.prefix_at(at, me, &end);
-        at = end;
-        if (w.tiles == 0) continue;
-      }
-      w.par = par;
-      w.start = start;
-      if (w.kind == 2) {
-#pragma unroll
-        for (int x = 0; x < S::NST; ++x) {
-          const int first = (x - start + S::NST) % S::NST;
-          par ^= first < 2 * w.tiles ? (uint32_t)((2 * w.tiles - first + S::NST - 1) / S::NST & 1) << x : 0;
-        }
-        start = (start + 2 * w.tiles) % S::NST;
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4 * S::D; ++x) {
-          const int first = x % (2 * S::D) / 2, n = steps_of(w, x / (2 * S::D));
-          par ^= first < n ? (uint32_t)((n - first + S::D - 1) / S::D & 1) << x : 0;
-        }
-      }
-      if (i >= kUnits) ok = warp_wait(&sh.unit_free[i % kUnits], (i / kUnits - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
-      if (!ok) break;
-      if (lane == 0) {
-        sh.unit[i % kUnits] = w;
-        mbar_arrive(&sh.unit_full[i % kUnits]);
-      }
-      __syncwarp();
-      ++i;
-      if (w.kind == 0) break;
-    }
-  } else if (warp == 8) {
-    Work u = unit_at(0);
+  if (warp == 8) {
+    Work u = next_unit();
     const int b8 = lane & 7;
-    int start = 0, ends[2] = {0, 0};
-    uint32_t par = 0;  // as in Work, but for every tile
+    int at0 = 0, ends[2] = {0, 0};  // the next place of a wide unit
+    uint32_t loaded = 0;  // as Work's par, but for every tile
     bool ok = true;
-    for (int i = 0; u.kind && ok; u = unit_at(++i)) {
+    for (; u.kind && ok; u = next_unit()) {
       const int nblk = (u.have + 15) >> 4;
       const int32_t* bt = p.c.table + u.first;  // the first row's
       auto block_id = [&](int j) {  // of block b8 of key tile j
@@ -400,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // of the next two key tiles
       int id0 = block_id(0), id1 = block_id(1);
-      start = u.start;
+      at0 = u.start;
       // each stream's Q, in a wide unit its rows; q_free: the stream's products before have read theirs
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -419,13 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       auto load = [&](int j, int kv, int id, int at) {
         const int here = min(8, nblk - j * 8);
-        if (!ok || !(ok = warp_wait(&sh.kv_empty[at], (par >> at ^ 1) & 1, p.c.err, DERR_EMPTY_WAIT))) return;
+        if (!ok || !(ok = warp_wait(&sh.kv_empty[at], (loaded >> at ^ 1) & 1, p.c.err, DERR_EMPTY_WAIT))) return;
         if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at], (uint32_t)here * 16 * HD * 2);
         __syncwarp();
         if (lane < here)
           tma_load_4d(kv_s + at * S::kTile + lane * 2 * S::kRows8, kv ? &maps.v : &maps.k, 0, 0, 0,
                       (id * p.c.n_kv_heads + u.g) * 2, &sh.kv_full[at]);
-        par ^= 1u << at;
+        loaded ^= 1u << at;
       };
       for (int j = 0; j < u.tiles && ok; j += 2) {
         const int a = id0, b = id1;
@@ -435,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             if (j + (x >> 1) < u.tiles) {
-              load(j + (x >> 1), x & 1, x < 2 ? a : b, start);
-              start = start + 1 == S::NST ? 0 : start + 1;
+              load(j + (x >> 1), x & 1, x < 2 ? a : b, at0);
+              at0 = at0 + 1 == S::NST ? 0 : at0 + 1;
             }
           }
         } else {
@@ -448,16 +421,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
-    for (int x = 0; x < S::NST; ++x) mbar_wait_bounded(&sh.kv_full[x], (par >> x ^ 1) & 1, p.c.err, DERR_DRAIN_WAIT);
+    for (int x = 0; x < S::NST; ++x) mbar_wait_bounded(&sh.kv_full[x], (loaded >> x ^ 1) & 1, p.c.err, DERR_DRAIN_WAIT);
     for (int t = 0; t < 2; ++t)
       if (ends[t] > 0) mbar_wait_bounded(&sh.q_full[t], (ends[t] - 1) & 1, p.c.err, DERR_DRAIN_WAIT);
-  } else {
+  } else if (warp < 11) {
     // Warps 9 and 10.
     const int me = warp - 9;
-    Work u = unit_at(0);
+    Work u = next_unit();
     int steps[2] = {0, 0}, ends[2] = {0, 0}, kind_before = 0;
     bool ok = true;
-    for (int i = 0; u.kind && ok; u = unit_at(++i)) {
+    for (; u.kind && ok; u = next_unit()) {
       const int nk = u.tiles;
       const bool wide = u.kind == 2;
       // Behind the wide units stream 1's products go from warp 9 to warp 10: the first ones
@@ -561,10 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, r = tid & 127;  // stream and row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = s_col(t) + lane_base, o_at = o_col(t) + lane_base;
-    Work u = unit_at(0);
+    Work u = next_unit();
     int steps = 0, ends = 0;
     bool ok = true;
-    for (int i = 0; u.kind && ok; u = unit_at(++i)) {
+    for (; u.kind && ok; u = next_unit()) {
       const bool wide = u.kind == 2;
       const int n = steps_of(u, t);
       const int row = r + (wide ? t * 128 : 0);  // of the unit
@@ -585,23 +558,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r == 0 && k == n - 1) mbar_arrive(&sh.q_free[t]);  // the stream's last product with Q
         const int lim = u.have - j * kKeys;                 // keys of the tile that exist
         if (busy) {
-          uint32_t s[kKeys], ph[kKeys / 2];
+          // In pieces of 32 keys, by loops that stay loops: a CTA has few steps, and its
+          // instructions come from L2, or from DRAM behind everybody's tiles.  (All 128 keys in
+          // registers: the first step took 6000 to 40000 cycles, now XXX; the others 1700, now YYY.)
+          uint32_t s[32];
+          auto load = [&](int q) {
+            tmem_ld32(s_at + 32 * q, s);
+            tmem_wait_ld();
+            tmem_pin<32>(s);
+            if (lim < kKeys) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
-          tmem_wait_ld();
-          tmem_pin<kKeys>(s);
-          if (lim < kKeys) {
+              for (int i = 0; i < 32; ++i)
+                if (32 * q + i >= lim) s[i] = 0xff800000u;  // -inf
+            }
+          };
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < kKeys / 32; ++q) {
+            load(q);
+            float mx[2] = {mt, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i)
-              if (i >= lim) s[i] = 0xff800000u;  // -inf
+            for (int i = 0; i < 32; i += 4)
+#pragma unroll
+              for (int w = 0; w < 2; ++w)
+                mx[w] = max3(mx[w], __uint_as_float(s[i + 2 * w]), __uint_as_float(s[i + 2 * w + 1]));
+            mt = fmaxf(mx[0], mx[1]);
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < kKeys; i += 8)
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              mx[w] = max3(mx[w], __uint_as_float(s[i + 2 * w]), __uint_as_float(s[i + 2 * w + 1]));
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           if (k == 0) {
             m = mt;
           } else if (__any_sync(0xffffffffu, row < u.rows && (mt - m) * c > 8.0f)) {
@@ -626,19 +608,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a row that has seen nothing yet has m = -inf: its P is 0
           const float mc = m == -INFINITY ? 0.0f : m * c;
           const uint64_t c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
-          uint64_t sum[2] = {0, 0};
+          uint64_t sum = 0;
+#pragma unroll 1
+          for (int q = 0; q < kKeys / 32; ++q) {
+            load(q);
+            uint32_t ph[16];
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 2) {
-            const float2 x = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2));
-            const float e0 = ex2(x.x), e1 = ex2(x.y);
-            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(e0, e1));
-            const __half2 h = __floats2half2_rn(e0, e1);
-            ph[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2));
+              const float e0 = ex2(x.x), e1 = ex2(x.y);
+              sum = add2(sum, pack2(e0, e1));
+              const __half2 h = __floats2half2_rn(e0, e1);
+              ph[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            tmem_st16(s_at + 16 * q, ph);
           }
-          const float2 st = unpack2(add2(sum[0], sum[1]));
+          const float2 st = unpack2(sum);
           l += st.x + st.y;
-#pragma unroll
-          for (int i = 0; i < kKeys / 2; i += 16) tmem_st16(s_at + i, ph + i);
           tmem_wait_st();
         }
         if (lim < kKeys) {
@@ -748,6 +734,7 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnCtas)
   bool ok = true;
   Own u = plan.own_at(&c0, me);
   if (warp == 4) {
+    const uint64_t once = l2_evict_first_policy();
     int item = 0, r = 0;
     for (; u.s >= 0 && ok; u = plan.own_at(&c0, me)) {
       const int32_t* table = p.c.table + (int64_t)u.row * p.c.table_stride + u.first;
@@ -776,8 +763,8 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnCtas)
           if (lane == 0) mbar_arrive_expect_tx(&sh.full[at], (uint32_t)here * 16 * HD * 2);
           __syncwarp();
           if (lane < here)
-            tma_load_4d(smem_addr(ring + at * S::kTile + lane * 2 * S::kRows8), kv ? &maps.v : &maps.k, 0, 0, 0,
-                        (id * p.c.n_kv_heads + u.g) * 2, &sh.full[at]);
+            tma_stream_4d(smem_addr(ring + at * S::kTile + lane * 2 * S::kRows8), kv ? &maps.v : &maps.k, 0, 0, 0,
+                          (id * p.c.n_kv_heads + u.g) * 2, &sh.full[at], once);
         }
       }
     }
