@@ -4,11 +4,10 @@
 // The shared blocks are read once for all rows: of a kv head there are B G of them
 // (every sequence's query heads), 128 to an M tile, and what a decode step is bound
 // by, bytes, becomes flops there.  The blocks behind the prefix have G rows each to read
-// them, and are bound by bytes.  So there is a kernel for each, which run side by side, on as
-// many SMs each as the lengths (which are on the device) make the work even: CTAs that have
-// no part in it end at once.
+// them, and are bound by bytes.  So the CTAs, one to an SM, are of two kinds that run side by
+// side, as many of each as the lengths (which are on the device) make the times even.
 //
-// k_prefix, a CTA per SM: S = Q K^T with 128 rows to an M tile, a unit being (row tile, kv head) and a CTA's
+// Prefix: S = Q K^T with 128 rows to an M tile, a unit being (row tile, kv head) and a CTA's
 // piece a share of the units' key tiles.  Two streams, each with a softmax warpgroup; while
 // one is busy with its probabilities the tensor core works for the other:
 //   wide (a unit of 129 to 256 rows)  each stream has 128 rows, both see every key tile
@@ -21,12 +20,13 @@
 //                        9's place, which has none of the tensor core's time to lose
 //   warp 8               Q, K and V by TMA, a box per 16-slot block, into a ring
 //
-// k_own, two CTAs per SM: S^T = K Q^T and O^T = V^T P with the cache as the big operand, 128 tokens x 16
+// Own blocks: S^T = K Q^T and O^T = V^T P with the cache as the big operand, 128 tokens x 16
 // columns, a unit being (sequence, kv head).  With rows as M as above, G of 128 would be
 // used and a tile take a thread 128 exponentials in a row: 3600 cycles instead of 1300.
-//   warps 0-3  a thread per token: scores, maximum, P into shared memory
-//   warp 4     Q, K and V by TMA
-//   warp 5     (one thread) the products
+// Two streams that know nothing of each other, each with a piece of all units' blocks:
+//   warps 4t .. 4t + 3   a thread per token: scores, maximum, P into shared memory
+//   warps 9, 10          (one thread) the products of stream 0 and 1
+//   warps 8, 11          Q, K and V of stream 0 and 1
 //
 // A unit's result comes in parts, (O, m, l) in fp32 in the scratch; k_join adds each row's
 // parts in the order of the pieces.  Maxima may lag behind by up to 8 (in log2), so
@@ -45,14 +45,13 @@ namespace {
 
 constexpr int kKeys = 128;     // of a tile, eight blocks
 constexpr int kThreads = 384;  // two softmax warpgroups, TMA, two for MMA, units
-constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsSingle = 88;  // at launch, and after
-static_assert(256 * kRegsSoftmax + 128 * kRegsSingle <= kThreads * kRegs, "no more than the launch has");
 constexpr int kMaxPieces = 160;
-// What a prefix tile costs and a unit's first loads and its parts' way out, in 200 cycles; a
-// pair's own, in blocks, and what these cost an SM with its two CTAs.
-constexpr int kWideCost = 16, kNarrowCost = 9, kStartCost = 12, kOwnStart = 10;
-constexpr float kOwnCost = 0.5f;
-constexpr int kOwnCtas = 2;  // per SM
+// Times in 200 cycles, by which the CTAs are shared out: a prefix tile, a unit's first loads and
+// its part's way out, a CTA's beginning; an own block of a stream, a pair's beginning in blocks, a
+// stream's, and a block (of hd 128) where all SMs together are as fast as the memory.
+constexpr int kWideCost = 20, kNarrowCost = 9, kStartCost = 30, kPrefixBegin = 25;
+constexpr float kOwnCost = 0.9f, kOwnBegin = 40.0f, kOwnShare = 0.0126f;
+constexpr int kOwnStart = 10;
 
 template <int HD>
 struct Shape {
@@ -62,17 +61,17 @@ struct Shape {
   static constexpr uint32_t kRows8 = H * 1024;     // 8 tokens of K or V: [half][8][64]
   static constexpr int NST = HD == 128 ? 5 : 9;    // ring tiles: as many as fit
   static constexpr int D = (NST - 1) / 4;          // K tiles, and V tiles, of a stream in narrow units
-  static constexpr size_t kPrefixSmem = 1024 + (2 + NST) * (size_t)kTile;
-  // own blocks: a ring of K and V tiles, Q twice (16 rows of 128 bytes for every 64 columns),
-  // P (a row of 32 bytes for every token)
+  // own blocks: each stream's ring of K and V tiles, Q twice (16 rows of 128 bytes for every 64
+  // columns), P (a row of 32 bytes for every token)
   static constexpr int NR = HD == 128 ? 3 : 6;
   static constexpr uint32_t kQ = H * 2048, kP = kKeys * 32;
-  static constexpr uint32_t oQ = NR * kTile, oP = oQ + 2 * kQ;
-  static constexpr size_t kOwnSmem = 1024 + oP + kP;
+  static constexpr uint32_t oQ = NR * kTile, oP = oQ + 2 * kQ, kStream = oP + kP;
+  static_assert(kStream % 1024 == 0, "both streams' tiles are aligned");
+  static constexpr size_t kSmem = 1024 + ((2 + NST) * kTile > 2 * kStream ? (2 + NST) * kTile : 2 * kStream);
 };
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, q1, k, v;  // q1: the rows of one sequence
 };
 
 // A prefix unit's share of a CTA: `tiles` key tiles, `have` tokens in them, from block `first`
@@ -85,7 +84,7 @@ struct Work {
   int start;     // of a wide unit in the ring
 };
 
-// A CTA's share of a (sequence, kv head): `blocks` from block `first` of table row `row` on,
+// A stream's share of a (sequence, kv head): `blocks` from block `first` of table row `row` on,
 // `have` tokens in them.
 struct Own {
   int s, g, row, first, blocks, have;  // s = -1: no more
@@ -103,7 +102,7 @@ __host__ __device__ inline int64_t prefix_slots(int batch, int G, int hkv, int p
   return prefix > 0 ? (int64_t)(batch * G + 255) / 256 * hkv + kMaxPieces : 0;
 }
 __host__ __device__ inline int64_t scratch_rows(int batch, int G, int hkv, int prefix) {
-  return prefix_slots(batch, G, hkv, prefix) * prefix_rows(batch, G) + ((int64_t)batch * hkv + kOwnCtas * kMaxPieces) * G;
+  return prefix_slots(batch, G, hkv, prefix) * prefix_rows(batch, G) + ((int64_t)batch * hkv + 2 * kMaxPieces) * G;
 }
 
 // Where the pieces' borders lie.  A prefix unit of n tiles has the places [x, x + kStartCost + n
@@ -113,14 +112,15 @@ template <int G>
 struct Plan {
   int tokens[2], base[2], size[2];  // of sequences lane and lane + 32: their own blocks' places, and those before them
   int hkv, batch, prefix, pre, pre_cost[2], pre_end, own_end;
-  int n_pre, n_own, each_pre, each_own;  // CTAs, and the places of their pieces
+  int n_pre, each_pre, each_own;  // CTAs for the prefix; places of a CTA's piece, and of a stream's
 
   EE_DEV static int places(int n, int start, int cost) { return n > 0 ? start + n * cost : 0; }
   EE_DEV int first_own(int n) const { return pre > 0 && n >= pre * 16 ? pre : 0; }  // block
   EE_DEV int own_blocks(int n) const { return ((n + 15) >> 4) - first_own(n); }
   EE_DEV int rows_of(int rt) const { return min(256, batch * G - rt * 256); }
 
-  EE_DEV void init(const DecodeParams& p, int sms) {
+  EE_DEV void init(const DecodeParams& p, int ctas) {
+    static_assert(kMaxPieces < 256, "a number of CTAs in eight bits");
     static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
     static_assert((kOwnStart + kCacheMaxCtx / 16) * 32 < 1 << 16, "two sums in a word");
     const int lane = threadIdx.x & 31;
@@ -153,11 +153,23 @@ struct Plan {
     for (int rt = 0; rt < 2; ++rt)
       pre_cost[rt] = rows_of(rt) > 0 ? places(tiles, kStartCost, rows_of(rt) > 128 ? kWideCost : kNarrowCost) : 0;
     pre_end = hkv * (pre_cost[0] + pre_cost[1]);
-    const float a = (float)pre_end, b = kOwnCost * (float)own_end;
-    n_pre = pre_end == 0 ? 0 : max(1, min(sms - (own_end > 0), (int)(sms * (a / (a + b)) + 0.5f)));
-    each_pre = max(kStartCost + kNarrowCost, (pre_end + max(1, n_pre) - 1) / max(1, n_pre));
-    n_own = kOwnCtas * (sms - n_pre);
-    each_own = max(kOwnStart + 8, (own_end + max(1, n_own) - 1) / max(1, n_own));
+    // of all numbers of prefix CTAs the one with which the slower kind is done first
+    auto pre_piece = [&](int n) { return max(kStartCost + kNarrowCost, (pre_end + n - 1) / n); };
+    auto own_piece = [&](int n) { return max(kOwnStart + 8, (own_end + 2 * n - 1) / (2 * n)); };
+    n_pre = 0;
+    if (pre_end > 0 && own_end > 0) {
+      unsigned best = 0xffffffffu;
+      const float share = kOwnShare / 128 * p.c.head_dim * own_end;
+      for (int n = lane + 1; n < ctas; n += 32) {
+        const float a = (float)(kPrefixBegin + pre_piece(n)), b = kOwnBegin + fmaxf(kOwnCost * own_piece(ctas - n), share);
+        best = min(best, (unsigned)fminf(fmaxf(a, b) * 8.0f, 16777215.0f) << 8 | (unsigned)n);
+      }
+      n_pre = (int)(__reduce_min_sync(0xffffffffu, best) & 255u);
+    } else if (pre_end > 0) {
+      n_pre = ctas;
+    }
+    each_pre = pre_piece(max(1, n_pre));
+    each_own = own_piece(max(1, ctas - n_pre));
   }
   // The first tile (or block) of a unit at x that stands at place c or behind it.
   EE_DEV static int item_at(int c, int x, int n, int start, int cost) {
@@ -189,7 +201,7 @@ struct Plan {
     }
     return w;
   }
-  // The share of CTA `me` of the pair that holds place *c, or of the next one that has any;
+  // The share of stream `me` of the pair that holds place *c, or of the next one that has any;
   // *c: behind the pair.
   EE_DEV Own own_at(int* c, int me) const {
     Own w;
@@ -228,55 +240,329 @@ EE_DEV Scratch scratch_of(const DecodeParams& p, bool own) {
   return r;
 }
 
-template <int HD>
+// A stream of own blocks.
+template <int HD, int G>
+struct Stream {
+  static constexpr int NR = Shape<HD>::NR;
+  uint64_t full[NR], empty[NR], q_full[2], q_free[2], s_full[2], p_ready, o_done;  // Q by share & 1
+  uint64_t drained;  // every MMA issued is over
+  float red[4][G], sum[4][G];
+};
+
+template <int HD, int G>
 struct Shared {
   static constexpr int NST = Shape<HD>::NST;
   uint64_t q_full[2], q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
   uint64_t drained[2];  // every MMA issued is over
+  Stream<HD, G> own[2];
   uint32_t tmem;
 };
 
+// The CTA's two streams of own blocks, `first` and the next of all.
+template <int HD, int G>
+EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const Plan<G>& plan, Stream<HD, G>* streams, uint8_t* memory,
+                       uint32_t tmem, int first) {
+  using S = Shape<HD>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
+  const int t = warp < 8 ? warp >> 2 : warp >= 10;  // the stream
+  Stream<HD, G>& sh = streams[t];
+  const int me = first + t;
+  uint8_t* ring = memory + t * S::kStream;
+  uint8_t *qs = ring + S::oQ, *ps = ring + S::oP;
+  auto s_col = [&](int k) { return tmem + t * 64 + (k & 1) * 16; };
+  auto o_col = [&](int r) { return tmem + t * 64 + 32 + (r & 1) * 16; };
+  // Tile k's K is ring item 2 k, its V item 2 k + 1; tiles and shares count on.  Where most SMs
+  // have own blocks two thirds of the ring are enough to keep the memory busy; with all of it
+  // loads queue up, and everybody's first ones wait 4 us (32 sequences of 500 to 2000 behind 256:
+  // 50 us, now 42).  After a wait
+  // that gave up the softmax warps go on without waiting: they still meet each other.
+  const bool deep = 2 * plan.n_pre >= (int)gridDim.x;
+  auto place = [&](int item) { return deep ? item % S::NR : item % (S::NR / 3 * 2); };
+  auto turn = [&](int item) { return deep ? item / S::NR : item / (S::NR / 3 * 2); };
+  int c0 = me * plan.each_own;
+  bool ok = true;
+  Own u = plan.own_at(&c0, me);
+  if (warp == 8 || warp == 11) {
+    const uint64_t once = l2_evict_first_policy();
+    int item = 0, r = 0;
+    for (; u.s >= 0 && ok; u = plan.own_at(&c0, me)) {
+      const int32_t* table = p.c.table + (int64_t)u.row * p.c.table_stride + u.first;
+      int ids = lane < u.blocks ? table[lane] : 0;  // 32 at a time
+      if (r >= 2) ok = warp_wait(&sh.q_free[r & 1], (r / 2 - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh.q_full[r & 1], G * HD * 2);
+        for (int h = 0; h < S::H; ++h)
+          tma_load_3d(smem_addr(qs + (r & 1) * S::kQ + h * 2048), &maps.q1, h * 64, u.g * G, u.s, &sh.q_full[r & 1]);
+      }
+      __syncwarp();
+      ++r;
+      for (int j = 0; j < u.blocks && ok; j += 8) {
+        if (j > 0 && (j & 31) == 0) ids = j + lane < u.blocks ? table[j + lane] : 0;
+        const int here = min(8, u.blocks - j);
+        int id = __shfl_sync(0xffffffffu, ids, (j & 31) + (lane & 7));
+        if (id < 0 || id >= p.c.n_blocks) {
+          if (lane < here) report(p.c.err, EE_DERR_BLOCK);
+          id = 0;
+        }
+        for (int kv = 0; kv < 2; ++kv, ++item) {
+          const int at = place(item);
+          if (turn(item) > 0) ok = warp_wait(&sh.empty[at], (turn(item) - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[at], (uint32_t)here * 16 * HD * 2);
+          __syncwarp();
+          if (lane < here)
+            tma_stream_4d(smem_addr(ring + at * S::kTile + lane * 2 * S::kRows8), kv ? &maps.v : &maps.k, 0, 0, 0,
+                          (id * p.c.n_kv_heads + u.g) * 2, &sh.full[at], once);
+        }
+      }
+    }
+    // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
+    for (int i = max(0, item - (deep ? S::NR : S::NR / 3 * 2)); i < item; ++i)
+      mbar_wait_bounded(&sh.full[place(i)], (uint32_t)turn(i) & 1, p.c.err, DERR_DRAIN_WAIT);
+    for (int i = max(0, r - 2); i < r; ++i) mbar_wait_bounded(&sh.q_full[i & 1], (i >> 1) & 1, p.c.err, DERR_DRAIN_WAIT);
+  } else if (warp >= 9) {
+    constexpr uint32_t id_s = instr_desc(0, 16, kKeys), id_o = instr_desc(0, 16, HD, true, true);
+    auto there = [&](int item) { return mbar_test(&sh.full[place(item)], turn(item) & 1); };
+    auto scores = [&](int k, int r, bool last) {  // of a tile of share r
+      tc_fence_after();
+      const uint64_t a = smem_desc_sw128(smem_addr(ring + place(2 * k) * S::kTile), S::kRows8),
+                     b = smem_desc_sw128(smem_addr(qs + (r & 1) * S::kQ));
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+        mma_f16(s_col(k), a + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), b + (((kk >> 2) * 2048 + (kk & 3) * 32) >> 4), id_s, kk > 0);
+      mma_commit(&sh.s_full[k & 1]);
+      mma_commit(&sh.empty[place(2 * k)]);
+      if (last) mma_commit(&sh.q_free[r & 1]);
+    };
+    int k = 0;
+    bool out = false;  // tile k's scores
+    for (int r = 0; u.s >= 0 && ok; ++r) {
+      const Own then = plan.own_at(&c0, me);
+      const int tiles = (u.blocks + 7) >> 3;
+      if (lane == 0) {
+        for (int j = 0; j < tiles && ok; ++j, ++k) {
+          if (!out) {
+            if (!(ok = mbar_wait_bounded(&sh.q_full[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT) &&
+                       mbar_wait_bounded(&sh.full[place(2 * k)], turn(2 * k) & 1, p.c.err, DERR_FULL_WAIT)))
+              break;
+            scores(k, r, j + 1 == tiles);
+          }
+          // The next tile's scores as soon as it is there, of this share or of the next; but the
+          // product with P does not wait for them: places of the ring are free behind it.
+          const int rn = j + 1 < tiles ? r : r + 1;
+          const bool more = j + 1 < tiles || then.s >= 0, last = j + 1 < tiles ? j + 2 == tiles : then.blocks <= 8;
+          out = false;
+          uint64_t since = 0;
+          for (int i = 1; !(mbar_test(&sh.p_ready, k & 1) && there(2 * k + 1)); ++i) {
+            if (more && !out && mbar_test(&sh.q_full[rn & 1], (rn >> 1) & 1) && there(2 * k + 2)) {
+              scores(k + 1, rn, last);
+              out = true;
+            }
+            if ((i & 255) == 0) {
+              const uint64_t now = globaltimer();
+              if (since == 0) since = now;
+              if (now - since > kWaitTimeoutNs) {
+                if (p.c.err) atomicCAS(p.c.err, 0, DERR_FULL_WAIT);
+                ok = false;
+                break;
+              }
+            }
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v = smem_desc_sw128_mn(smem_addr(ring + place(2 * k + 1) * S::kTile), 1024, S::kRows8),
+                         x = smem_desc_rows<32>(smem_addr(ps), 256);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_f16(o_col(r), v + kk * (2 * S::kRows8 >> 4), x + kk * (512 >> 4), id_o, j > 0 || kk > 0);
+          mma_commit(&sh.empty[place(2 * k + 1)]);
+          mma_commit(&sh.o_done);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      k = __shfl_sync(0xffffffffu, k, 0);
+      u = then;
+    }
+    if (lane == 0) {  // and so are the products, before tensor memory is given back
+      mma_commit(&sh.drained);
+      mbar_wait_bounded(&sh.drained, 0, p.c.err, DERR_DRAIN_WAIT);
+    }
+    __syncwarp();
+  } else {
+    const int w4 = warp & 3, bar = 1 + t;
+    const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+    // M = 64: rows 16 w .. 16 w + 15 in the first lanes of warp w's part of tensor memory
+    const int dim = HD == 128 ? tid : w4 * 16 + (lane & 15);
+    const bool has_dim = HD == 128 || lane < 16;
+    int k = 0;
+    for (int r = 0; u.s >= 0; u = plan.own_at(&c0, me), ++r) {
+      const int tiles = (u.blocks + 7) >> 3;
+      float m[G], l[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.0f;
+      }
+#pragma unroll 1
+      for (int j = 0; j < tiles; ++j, ++k) {
+        if (ok) ok = warp_wait(&sh.s_full[k & 1], (k >> 1) & 1, p.c.err, DERR_FULL_WAIT);
+        tc_fence_after();
+        uint32_t v[16];
+        tmem_ld16(s_col(k) + lane_base, v);
+        tmem_wait_ld();
+        tmem_pin<16>(v);
+        const int left = u.have - j * kKeys;  // tokens from this tile on
+        const bool live = tid < left;
+        float z[G], a[G];
+        int grow = 0;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          z[h] = live ? __uint_as_float(v[h]) * c : -INFINITY;
+          grow |= z[h] - m[h] > 8.0f;
+          a[h] = 1.0f;
+        }
+        asm volatile(
+            "{ .reg .pred p, q; setp.ne.s32 p, %0, 0; barrier.cta.red.or.pred q, %1, 128, p; selp.s32 %0, 1, 0, q; }"
+            : "+r"(grow)
+            : "r"(bar)
+            : "memory");
+        if (grow) {  // the first tile, and rarely later
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float x = warp_max(z[h]);
+            if (lane == 0) sh.red[w4][h] = x;
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mn = fmaxf(fmaxf(fmaxf(sh.red[0][h], sh.red[1][h]), fmaxf(sh.red[2][h], sh.red[3][h])), m[h]);
+            a[h] = m[h] == mn ? 1.0f : ex2(m[h] - mn);
+            m[h] = mn;
+            l[h] *= a[h];
+          }
+        }
+        uint32_t x4[4] = {};  // the token's row of P
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float e = ex2(z[h] - (m[h] == -INFINITY ? 0.0f : m[h]));
+          l[h] += e;
+          x4[h >> 1] |= (uint32_t)float_to_half_bits(e) << (16 * (h & 1));
+        }
+        // the product before has read P and is in O
+        if (k > 0 && ok) ok = warp_wait(&sh.o_done, (k - 1) & 1, p.c.err, DERR_FULL_WAIT);
+        *reinterpret_cast<uint4*>(ps + (tid >> 3) * 256 + row_chunk<32>(tid & 7, 0)) = make_uint4(x4[0], x4[1], x4[2], x4[3]);
+        if (left < kKeys) {
+          // slots behind the last token hold anything: their V becomes zero
+          const int item = 2 * k + 1;
+          if (ok) ok = warp_wait(&sh.full[place(item)], turn(item) & 1, p.c.err, DERR_FULL_WAIT);
+          uint8_t* tile = ring + place(item) * S::kTile;
+          for (int i = left * 8 + tid; i < kKeys * 8; i += 128)
+#pragma unroll
+            for (int half = 0; half < S::H; ++half)
+              *reinterpret_cast<uint4*>(tile + (i >> 6) * S::kRows8 + half * 1024 + (i & 63) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        if (grow && j > 0) {
+          tc_fence_after();
+          uint32_t o[16];
+          tmem_ld16(o_col(r) + lane_base, o);
+          tmem_wait_ld();
+          tmem_pin<16>(o);
+#pragma unroll
+          for (int h = 0; h < G; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * a[h]);
+          tmem_st16(o_col(r) + lane_base, o);
+          tmem_wait_st();
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&sh.p_ready);
+      }
+      // the share's end: l of all warps, O of this thread's dim
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float x = warp_sum(l[h]);
+        if (lane == 0) sh.sum[w4][h] = x;
+      }
+      if (ok) ok = warp_wait(&sh.o_done, (k - 1) & 1, p.c.err, DERR_FULL_WAIT);
+      tc_fence_after();
+      uint32_t o[16];
+      tmem_ld16(o_col(r) + lane_base, o);
+      asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+      tmem_wait_ld();
+      tmem_pin<16>(o);
+      const Scratch to = scratch_of<G>(p, true);
+#pragma unroll
+      for (int h = 0; h < G; ++h)
+        if (has_dim) to.o[(u.slot * G + h) * HD + dim] = __uint_as_float(o[h]);
+#pragma unroll
+      for (int h = 0; h < G; ++h)
+        if (tid == h)
+          *reinterpret_cast<float2*>(to.ml + (u.slot * G + h) * 2) =
+              make_float2(m[h], (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]));
+      // sum is read before the next share's is written: its first tile's barrier is between
+      tc_fence_before();
+    }
+  }
+  if (!ok) __nanosleep(1000000);  // what this CTA no longer waited for may be on its way
+}
+
 template <int HD, int G>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_prefix(const DecodeParams p, const __grid_constant__ Maps maps, const float c) {
+    k_shared_attention(const DecodeParams p, const __grid_constant__ Maps maps, const float c) {
   using S = Shape<HD>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Shared<HD> sh;
+  __shared__ Shared<HD, G> sh;
   uint8_t* tiles = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dep_launch();
-  // The loads begin before anything else is ready: their warp makes the barriers, and
-  // does not wait for the others.
-  if (warp == 8) {
-    if (lane < S::NST) {
-      mbar_init(&sh.kv_full[lane], 1);
-      mbar_init(&sh.kv_empty[lane], 1);
+  // The loads begin before anything else is ready: their warps make the barriers, and do not
+  // wait for the others.
+  const bool loads = warp == 8 || warp == 11;
+  if (loads) {
+    Stream<HD, G>& own = sh.own[warp == 11];
+    if (lane < S::NR) {
+      mbar_init(&own.full[lane], 1);
+      mbar_init(&own.empty[lane], 1);
     }
     if (lane < 2) {
-      mbar_init(&sh.s_full[lane], 1);
-      mbar_init(&sh.p_ready[lane], 129);  // its warpgroup, and the tiles that the products need
-      mbar_init(&sh.q_full[lane], 1);
-      mbar_init(&sh.q_free[lane], 1);  // the stream's last product with it
-      mbar_init(&sh.o_done[lane], 1);
-      mbar_init(&sh.drained[lane], 1);
+      mbar_init(&own.q_full[lane], 1);
+      mbar_init(&own.q_free[lane], 1);
+      mbar_init(&own.s_full[lane], 1);
+    }
+    if (lane == 0) {
+      mbar_init(&own.p_ready, 128);
+      mbar_init(&own.o_done, 1);
+      mbar_init(&own.drained, 1);
+    }
+    if (warp == 8) {
+      if (lane < S::NST) {
+        mbar_init(&sh.kv_full[lane], 1);
+        mbar_init(&sh.kv_empty[lane], 1);
+      }
+      if (lane < 2) {
+        mbar_init(&sh.s_full[lane], 1);
+        mbar_init(&sh.p_ready[lane], 129);  // its warpgroup, and the tiles that the products need
+        mbar_init(&sh.q_full[lane], 1);
+        mbar_init(&sh.q_free[lane], 1);  // the stream's last product with it
+        mbar_init(&sh.o_done[lane], 1);
+        mbar_init(&sh.drained[lane], 1);
+      }
     }
     fence_mbar_init();
     __syncwarp();
+    asm volatile("bar.arrive 3, %0;" ::"n"(kThreads) : "memory");
   }
   Plan<G> plan;
   plan.init(p, gridDim.x);
-  if ((int)blockIdx.x >= plan.n_pre) return;
-  if (warp == 8) {
-    asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
-  } else {
+  if (!loads) {
     if (warp == 9) {
       tmem_alloc(&sh.tmem, 512);
       tc_fence_before();
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
     tc_fence_after();
   }
-  const uint32_t tmem = warp == 8 ? 0 : sh.tmem;
+  const uint32_t tmem = loads ? 0 : sh.tmem;
   const uint32_t q_s = smem_addr(tiles), kv_s = q_s + 2 * S::kTile;
   // tensor memory: S_t (128 columns, P_t over its first 64), then O_t
   auto s_col = [&](int t) { return tmem + t * 128; };
@@ -348,12 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_f16_ta(o_col(t), s_col(t) + kk * 8, smem_desc_sw128_mn(b + kk * 2 * S::kRows8, 1024, S::kRows8), id_pv, acc || kk > 0);
   };
 
-  // Registers go from the four single warps to the softmax warps, which hold a row of
-  // S: 128 x 88 + 256 x 208 is what 384 threads are launched with at 168 each
-  // (launch_t checks that).
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSingle));
-  if (warp == 8) {
+  if ((int)blockIdx.x >= plan.n_pre) {
+    own_blocks<HD, G>(p, maps, c, plan, sh.own, tiles, tmem, ((int)blockIdx.x - plan.n_pre) * 2);
+  } else if (warp == 8) {
     Work u = next_unit();
     const int b8 = lane & 7;
     int at0 = 0, ends[2] = {0, 0};  // the next place of a wide unit
@@ -424,8 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = 0; x < S::NST; ++x) mbar_wait_bounded(&sh.kv_full[x], (loaded >> x ^ 1) & 1, p.c.err, DERR_DRAIN_WAIT);
     for (int t = 0; t < 2; ++t)
       if (ends[t] > 0) mbar_wait_bounded(&sh.q_full[t], (ends[t] - 1) & 1, p.c.err, DERR_DRAIN_WAIT);
-  } else if (warp < 11) {
-    // Warps 9 and 10.
+  } else if (warp == 9 || warp == 10) {
     const int me = warp - 9;
     Work u = next_unit();
     int steps[2] = {0, 0}, ends[2] = {0, 0}, kind_before = 0;
@@ -528,9 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(&sh.drained[me], 0, p.c.err, DERR_DRAIN_WAIT);
     }
     __syncwarp();
-  }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+  } else if (warp < 8) {
     const int t = warp >> 2, r = tid & 127;  // stream and row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = s_col(t) + lane_base, o_at = o_col(t) + lane_base;
@@ -673,296 +953,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-constexpr int kOwnThreads = 192;
-
-template <int HD, int G>
-struct OwnShared {
-  static constexpr int NR = Shape<HD>::NR;
-  uint64_t full[NR], empty[NR], q_full[2], q_free[2], s_full[2], p_ready, o_done;  // Q by share & 1
-  uint64_t drained;  // every MMA issued is over
-  uint32_t tmem;
-  float red[4][G], sum[4][G];
-};
-
-template <int HD, int G>
-__global__ void __launch_bounds__(kOwnThreads, kOwnCtas)
-    k_own(const DecodeParams p, const __grid_constant__ Maps maps, const float c, const int sms) {
-  using S = Shape<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ OwnShared<HD, G> sh;
-  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *qs = ring + S::oQ, *ps = ring + S::oP;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = blockIdx.x;
-  grid_dep_launch();
-  // The loads begin before anything else is ready: their warp makes the barriers, and
-  // does not wait for the others.
-  if (warp == 4) {
-    if (lane < S::NR) {
-      mbar_init(&sh.full[lane], 1);
-      mbar_init(&sh.empty[lane], 1);
-    }
-    if (lane < 2) {
-      mbar_init(&sh.q_full[lane], 1);
-      mbar_init(&sh.q_free[lane], 1);
-      mbar_init(&sh.s_full[lane], 1);
-    }
-    if (lane == 0) {
-      mbar_init(&sh.p_ready, 128);
-      mbar_init(&sh.o_done, 1);
-      mbar_init(&sh.drained, 1);
-    }
-    fence_mbar_init();
-    __syncwarp();
-    asm volatile("bar.arrive 2, %0;" ::"n"(kOwnThreads) : "memory");
-  }
-  Plan<G> plan;
-  plan.init(p, sms);
-  if (warp != 4) {
-    if (warp == 5) {
-      tmem_alloc(&sh.tmem, 64);
-      tc_fence_before();
-    }
-    asm volatile("bar.sync 2, %0;" ::"n"(kOwnThreads) : "memory");
-    tc_fence_after();
-  }
-  const uint32_t tmem = warp == 4 ? 0 : sh.tmem;
-  auto s_col = [&](int k) { return tmem + (k & 1) * 16; };
-  auto o_col = [&](int r) { return tmem + 32 + (r & 1) * 16; };
-  // Tile k's K is ring item 2 k, its V item 2 k + 1; tiles and shares count on.  After a wait
-  // that gave up the softmax warps go on without waiting: they still meet each other.
-  int c0 = me < plan.n_own ? me * plan.each_own : INT_MAX;
-  bool ok = true;
-  Own u = plan.own_at(&c0, me);
-  if (warp == 4) {
-    const uint64_t once = l2_evict_first_policy();
-    int item = 0, r = 0;
-    for (; u.s >= 0 && ok; u = plan.own_at(&c0, me)) {
-      const int32_t* table = p.c.table + (int64_t)u.row * p.c.table_stride + u.first;
-      int ids = lane < u.blocks ? table[lane] : 0;  // 32 at a time
-      if (r >= 2) ok = warp_wait(&sh.q_free[r & 1], (r / 2 - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full[r & 1], G * HD * 2);
-        for (int h = 0; h < S::H; ++h)
-          tma_load_3d(smem_addr(qs + (r & 1) * S::kQ + h * 2048), &maps.q, h * 64, u.g * G, u.s, &sh.q_full[r & 1]);
-      }
-      __syncwarp();
-      ++r;
-      for (int j = 0; j < u.blocks && ok; j += 8) {
-        if (j > 0 && (j & 31) == 0) ids = j + lane < u.blocks ? table[j + lane] : 0;
-        const int here = min(8, u.blocks - j);
-        int id = __shfl_sync(0xffffffffu, ids, (j & 31) + (lane & 7));
-        if (id < 0 || id >= p.c.n_blocks) {
-          if (lane < here) report(p.c.err, EE_DERR_BLOCK);
-          id = 0;
-        }
-        for (int kv = 0; kv < 2; ++kv, ++item) {
-          const int at = item % S::NR;
-          if (item >= S::NR) ok = warp_wait(&sh.empty[at], (item / S::NR - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[at], (uint32_t)here * 16 * HD * 2);
-          __syncwarp();
-          if (lane < here)
-            tma_stream_4d(smem_addr(ring + at * S::kTile + lane * 2 * S::kRows8), kv ? &maps.v : &maps.k, 0, 0, 0,
-                          (id * p.c.n_kv_heads + u.g) * 2, &sh.full[at], once);
-        }
-      }
-    }
-    // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
-    for (int i = max(0, item - S::NR); i < item; ++i)
-      mbar_wait_bounded(&sh.full[i % S::NR], (uint32_t)(i / S::NR) & 1, p.c.err, DERR_DRAIN_WAIT);
-    for (int i = max(0, r - 2); i < r; ++i) mbar_wait_bounded(&sh.q_full[i & 1], (i >> 1) & 1, p.c.err, DERR_DRAIN_WAIT);
-  } else if (warp == 5) {
-    constexpr uint32_t id_s = instr_desc(0, 16, kKeys), id_o = instr_desc(0, 16, HD, true, true);
-    auto there = [&](int item) { return mbar_test(&sh.full[item % S::NR], (item / S::NR) & 1); };
-    auto scores = [&](int k, int r, bool last) {  // of a tile of share r
-      tc_fence_after();
-      const uint64_t a = smem_desc_sw128(smem_addr(ring + 2 * k % S::NR * S::kTile), S::kRows8),
-                     b = smem_desc_sw128(smem_addr(qs + (r & 1) * S::kQ));
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk)
-        mma_f16(s_col(k), a + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), b + (((kk >> 2) * 2048 + (kk & 3) * 32) >> 4), id_s, kk > 0);
-      mma_commit(&sh.s_full[k & 1]);
-      mma_commit(&sh.empty[2 * k % S::NR]);
-      if (last) mma_commit(&sh.q_free[r & 1]);
-    };
-    int k = 0;
-    bool out = false;  // tile k's scores
-    for (int r = 0; u.s >= 0 && ok; ++r) {
-      const Own then = plan.own_at(&c0, me);
-      const int tiles = (u.blocks + 7) >> 3;
-      if (lane == 0) {
-        for (int j = 0; j < tiles && ok; ++j, ++k) {
-          if (!out) {
-            if (!(ok = mbar_wait_bounded(&sh.q_full[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT) &&
-                       mbar_wait_bounded(&sh.full[2 * k % S::NR], (2 * k / S::NR) & 1, p.c.err, DERR_FULL_WAIT)))
-              break;
-            scores(k, r, j + 1 == tiles);
-          }
-          // The next tile's scores as soon as it is there, of this share or of the next; but the
-          // product with P does not wait for them: places of the ring are free behind it.
-          const int rn = j + 1 < tiles ? r : r + 1;
-          const bool more = j + 1 < tiles || then.s >= 0, last = j + 1 < tiles ? j + 2 == tiles : then.blocks <= 8;
-          out = false;
-          uint64_t since = 0;
-          for (int i = 1; !(mbar_test(&sh.p_ready, k & 1) && there(2 * k + 1)); ++i) {
-            if (more && !out && mbar_test(&sh.q_full[rn & 1], (rn >> 1) & 1) && there(2 * k + 2)) {
-              scores(k + 1, rn, last);
-              out = true;
-            }
-            if ((i & 255) == 0) {
-              const uint64_t now = globaltimer();
-              if (since == 0) since = now;
-              if (now - since > kWaitTimeoutNs) {
-                if (p.c.err) atomicCAS(p.c.err, 0, DERR_FULL_WAIT);
-                ok = false;
-                break;
-              }
-            }
-          }
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t v = smem_desc_sw128_mn(smem_addr(ring + (2 * k + 1) % S::NR * S::kTile), 1024, S::kRows8),
-                         x = smem_desc_rows<32>(smem_addr(ps), 256);
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_f16(o_col(r), v + kk * (2 * S::kRows8 >> 4), x + kk * (512 >> 4), id_o, j > 0 || kk > 0);
-          mma_commit(&sh.empty[(2 * k + 1) % S::NR]);
-          mma_commit(&sh.o_done);
-        }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      k = __shfl_sync(0xffffffffu, k, 0);
-      u = then;
-    }
-    if (lane == 0) {  // and so are the products, before tensor memory is given back
-      mma_commit(&sh.drained);
-      mbar_wait_bounded(&sh.drained, 0, p.c.err, DERR_DRAIN_WAIT);
-    }
-    __syncwarp();
-  } else {
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    // M = 64: rows 16 w .. 16 w + 15 in the first lanes of warp w's part of tensor memory
-    const int dim = HD == 128 ? tid : warp * 16 + (lane & 15);
-    const bool has_dim = HD == 128 || lane < 16;
-    int k = 0;
-    for (int r = 0; u.s >= 0; u = plan.own_at(&c0, me), ++r) {
-      const int tiles = (u.blocks + 7) >> 3;
-      float m[G], l[G];
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.0f;
-      }
-#pragma unroll 1
-      for (int j = 0; j < tiles; ++j, ++k) {
-        if (ok) ok = warp_wait(&sh.s_full[k & 1], (k >> 1) & 1, p.c.err, DERR_FULL_WAIT);
-        tc_fence_after();
-        uint32_t v[16];
-        tmem_ld16(s_col(k) + lane_base, v);
-        tmem_wait_ld();
-        tmem_pin<16>(v);
-        const int left = u.have - j * kKeys;  // tokens from this tile on
-        const bool live = tid < left;
-        float z[G], a[G];
-        int grow = 0;
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          z[h] = live ? __uint_as_float(v[h]) * c : -INFINITY;
-          grow |= z[h] - m[h] > 8.0f;
-          a[h] = 1.0f;
-        }
-        asm volatile(
-            "{ .reg .pred p, q; setp.ne.s32 p, %0, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.s32 %0, 1, 0, q; }"
-            : "+r"(grow)
-            :
-            : "memory");
-        if (grow) {  // the first tile, and rarely later
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float x = warp_max(z[h]);
-            if (lane == 0) sh.red[warp][h] = x;
-          }
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float mn = fmaxf(fmaxf(fmaxf(sh.red[0][h], sh.red[1][h]), fmaxf(sh.red[2][h], sh.red[3][h])), m[h]);
-            a[h] = m[h] == mn ? 1.0f : ex2(m[h] - mn);
-            m[h] = mn;
-            l[h] *= a[h];
-          }
-        }
-        uint32_t x4[4] = {};  // the token's row of P
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          const float e = ex2(z[h] - (m[h] == -INFINITY ? 0.0f : m[h]));
-          l[h] += e;
-          x4[h >> 1] |= (uint32_t)float_to_half_bits(e) << (16 * (h & 1));
-        }
-        // the product before has read P and is in O
-        if (k > 0 && ok) ok = warp_wait(&sh.o_done, (k - 1) & 1, p.c.err, DERR_FULL_WAIT);
-        *reinterpret_cast<uint4*>(ps + (tid >> 3) * 256 + row_chunk<32>(tid & 7, 0)) = make_uint4(x4[0], x4[1], x4[2], x4[3]);
-        if (left < kKeys) {
-          // slots behind the last token hold anything: their V becomes zero
-          const int item = 2 * k + 1;
-          if (ok) ok = warp_wait(&sh.full[item % S::NR], (item / S::NR) & 1, p.c.err, DERR_FULL_WAIT);
-          uint8_t* tile = ring + item % S::NR * S::kTile;
-          for (int i = left * 8 + tid; i < kKeys * 8; i += 128)
-#pragma unroll
-            for (int half = 0; half < S::H; ++half)
-              *reinterpret_cast<uint4*>(tile + (i >> 6) * S::kRows8 + half * 1024 + (i & 63) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        if (grow && j > 0) {
-          tc_fence_after();
-          uint32_t o[16];
-          tmem_ld16(o_col(r) + lane_base, o);
-          tmem_wait_ld();
-          tmem_pin<16>(o);
-#pragma unroll
-          for (int h = 0; h < G; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * a[h]);
-          tmem_st16(o_col(r) + lane_base, o);
-          tmem_wait_st();
-        }
-        fence_proxy_async();
-        tc_fence_before();
-        mbar_arrive(&sh.p_ready);
-      }
-      // the share's end: l of all warps, O of this thread's dim
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        const float x = warp_sum(l[h]);
-        if (lane == 0) sh.sum[warp][h] = x;
-      }
-      if (ok) ok = warp_wait(&sh.o_done, (k - 1) & 1, p.c.err, DERR_FULL_WAIT);
-      tc_fence_after();
-      uint32_t o[16];
-      tmem_ld16(o_col(r) + lane_base, o);
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      tmem_wait_ld();
-      tmem_pin<16>(o);
-      const Scratch to = scratch_of<G>(p, true);
-#pragma unroll
-      for (int h = 0; h < G; ++h)
-        if (has_dim) to.o[(u.slot * G + h) * HD + dim] = __uint_as_float(o[h]);
-#pragma unroll
-      for (int h = 0; h < G; ++h)
-        if (tid == h)
-          *reinterpret_cast<float2*>(to.ml + (u.slot * G + h) * 2) =
-              make_float2(m[h], (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]));
-      // sum is read before the next share's is written: its first tile's barrier is between
-      tc_fence_before();
-    }
-  }
-  // k_join comes behind this kernel; k_prefix, which may still run, has to be over too
-  if (tid == 0) grid_dep_wait();
-  __syncthreads();
-  if (warp == 5) {
-    tc_fence_after();
-    tmem_free(tmem, 64);
-  }
-  if (!ok) __nanosleep(1000000);  // what this CTA no longer waited for may be on its way
-}
-
 // o is a mean of fp16 values and no larger than they are.  P's rounding may take it past the
 // largest one by up to 2^-11 of it, which would be infinite in fp16.
 EE_DEV float within_half(float y) {
@@ -976,7 +966,7 @@ EE_DEV float within_half(float y) {
 constexpr int kJoinThreads = 256;
 
 template <int HD, int G, int J>
-__global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, const int sms) {
+__global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, const int ctas) {
   constexpr int P = HD / 32, U = 8, kStripes = 8 / J;  // dims per lane; parts in flight
   __shared__ int64_t ml_at[4 * kMaxPieces], o_at[4 * kMaxPieces];  // where head 0's parts are; -1: none
   __shared__ float ms[8], ls[8], outs[8][HD];
@@ -984,7 +974,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   const int s = blockIdx.x / (p.n_heads / J), first = (blockIdx.x - s * (p.n_heads / J)) * J;  // its heads
   const int g = first / G, h = first % G + warp % J;
   Plan<G> plan;
-  plan.init(p, sms);
+  plan.init(p, ctas);
   const int n = plan.of(plan.tokens, s), own_x = plan.of(plan.base, s) * plan.hkv + g * plan.of(plan.size, s);
   const int own = plan.own_blocks(n), pre = plan.first_own(n) > 0 ? (plan.pre + 7) >> 3 : 0;
   const int all = s * G, rt = all >> 8, row = all & 255, rows = plan.rows_of(rt), R = prefix_rows(p.batch, G);
@@ -1093,12 +1083,7 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(prepared.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_prefix<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kPrefixSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_own<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kOwnSmem);
-    // the exchange of registers above counts on the launch's share
-    cudaFuncAttributes at;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_prefix<HD, G>);
-    if (e == cudaSuccess && at.numRegs != kRegs) e = cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(k_shared_attention<HD, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) prepared.fetch_or(1ull << dev, std::memory_order_release);
   }
@@ -1110,37 +1095,27 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   const uint64_t cd[4] = {64, 8, (uint64_t)S::H, (uint64_t)p.c.n_blocks * p.c.n_kv_heads * 2},
                  cs[3] = {(uint64_t)HD * 2, 128, (uint64_t)HD * 16};
   const uint32_t cb[4] = {64, 8, (uint32_t)S::H, 2};
-  if (!encode_tensor_map(&maps.q, false, 3, p.q, qd, qs, many) || !encode_tensor_map(&maps.k, false, 4, p.c.k, cd, cs, cb) ||
+  if (!encode_tensor_map(&maps.q, false, 3, p.q, qd, qs, many) || !encode_tensor_map(&maps.q1, false, 3, p.q, qd, qs, one) || !encode_tensor_map(&maps.k, false, 4, p.c.k, cd, cs, cb) ||
       !encode_tensor_map(&maps.v, false, 4, p.c.v, cd, cs, cb))
     return cudaErrorInvalidValue;
-  sms = std::min(sms, kMaxPieces);
-  const float c = make_exponent(HD).c;
+  // a CTA per SM, but not many more than there are tiles
+  const int64_t own = (int64_t)p.batch * p.c.n_kv_heads * ((p.c.max_ctx + kKeys - 1) / kKeys);
+  const int64_t pre = (int64_t)((p.batch * G + 255) / 256) * p.c.n_kv_heads * ((p.prefix + kKeys - 1) / kKeys);
+  const int ctas = (int)std::min<int64_t>(std::min(sms, kMaxPieces), own + pre);
+  k_shared_attention<HD, G><<<ctas, kThreads, S::kSmem, st>>>(p, maps, make_exponent(HD).c);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.gridDim = dim3((unsigned)sms);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kPrefixSmem;
-  if (p.prefix > 0) {
-    e = cudaLaunchKernelEx(&cfg, k_prefix<HD, G>, p, maps, c);
-    if (e != cudaSuccess) return e;
-    cfg.numAttrs = 1;
-  }
-  if (!encode_tensor_map(&maps.q, false, 3, p.q, qd, qs, one)) return cudaErrorInvalidValue;
-  cfg.gridDim = dim3((unsigned)(kOwnCtas * sms));
-  cfg.blockDim = dim3(kOwnThreads);
-  cfg.dynamicSmemBytes = S::kOwnSmem;
-  e = cudaLaunchKernelEx(&cfg, k_own<HD, G>, p, maps, c, sms);
-  if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
   const bool few = p.batch * p.n_heads <= 2 * sms;
   cfg.gridDim = dim3((unsigned)(p.batch * (few ? p.n_heads : p.c.n_kv_heads)));
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = 0;
-  return few ? cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, sms) : cudaLaunchKernelEx(&cfg, k_join<HD, G, G>, p, sms);
+  return few ? cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, ctas) : cudaLaunchKernelEx(&cfg, k_join<HD, G, G>, p, ctas);
 }
 
 }  // namespace
