@@ -49,9 +49,9 @@ constexpr int kMaxPieces = 160;
 // Times in 200 cycles, by which the CTAs are shared out: a prefix tile, a unit's first loads and
 // its part's way out, a CTA's beginning; an own block of a stream, a pair's beginning in blocks, a
 // stream's, and a block (of hd 128) where all SMs together are as fast as the memory.
-constexpr int kWideCost = 20, kNarrowCost = 9, kStartCost = 30, kPrefixBegin = 25;
-constexpr float kOwnCost = 0.9f, kOwnBegin = 40.0f, kOwnShare = 0.0126f;
-constexpr int kOwnStart = 10;
+constexpr int kWideCost = 18, kNarrowCost = 9, kStartCost = 25;
+constexpr float kPrefixBegin = 60.0f, kOwnCost = 2.0f, kOwnBegin = 45.0f, kOwnShare = 0.0126f;
+constexpr int kOwnStart = 4;
 
 template <int HD>
 struct Shape {
@@ -154,22 +154,23 @@ struct Plan {
       pre_cost[rt] = rows_of(rt) > 0 ? places(tiles, kStartCost, rows_of(rt) > 128 ? kWideCost : kNarrowCost) : 0;
     pre_end = hkv * (pre_cost[0] + pre_cost[1]);
     // of all numbers of prefix CTAs the one with which the slower kind is done first
-    auto pre_piece = [&](int n) { return max(kStartCost + kNarrowCost, (pre_end + n - 1) / n); };
-    auto own_piece = [&](int n) { return max(kOwnStart + 8, (own_end + 2 * n - 1) / (2 * n)); };
     n_pre = 0;
     if (pre_end > 0 && own_end > 0) {
       unsigned best = 0xffffffffu;
       const float share = kOwnShare / 128 * p.c.head_dim * own_end;
+#pragma unroll 1
       for (int n = lane + 1; n < ctas; n += 32) {
-        const float a = (float)(kPrefixBegin + pre_piece(n)), b = kOwnBegin + fmaxf(kOwnCost * own_piece(ctas - n), share);
+        const float a = kPrefixBegin + fmaxf(kNarrowCost, __fdividef(pre_end, n));
+        const float b = kOwnBegin + fmaxf(kOwnCost * fmaxf(kOwnStart + 4, __fdividef(own_end, 2 * (ctas - n))), share);
         best = min(best, (unsigned)fminf(fmaxf(a, b) * 8.0f, 16777215.0f) << 8 | (unsigned)n);
       }
       n_pre = (int)(__reduce_min_sync(0xffffffffu, best) & 255u);
     } else if (pre_end > 0) {
       n_pre = ctas;
     }
-    each_pre = pre_piece(max(1, n_pre));
-    each_own = own_piece(max(1, ctas - n_pre));
+    const int n = max(1, n_pre), streams = 2 * max(1, ctas - n_pre);
+    each_pre = max(kNarrowCost, (pre_end + n - 1) / n);
+    each_own = max(kOwnStart + 4, (own_end + streams - 1) / streams);
   }
   // The first tile (or block) of a unit at x that stands at place c or behind it.
   EE_DEV static int item_at(int c, int x, int n, int start, int cost) {
@@ -240,33 +241,71 @@ EE_DEV Scratch scratch_of(const DecodeParams& p, bool own) {
   return r;
 }
 
+// Units or shares on their way from the warp that finds (and loads) them to those that work on
+// them: code that stands once in the kernel, because a CTA's first instructions take as
+// long to come as its first tiles.
+template <typename T>
+struct Ring {
+  static constexpr int kDepth = 4;
+  uint64_t full[kDepth], free[kDepth];
+  T at[kDepth];
+
+  EE_DEV void init(int readers) {  // one lane per place
+    const int lane = threadIdx.x & 31;
+    if (lane < kDepth) {
+      mbar_init(&full[lane], 1);
+      mbar_init(&free[lane], readers);
+    }
+  }
+  EE_DEV bool put(int i, const T& x, int32_t* err) {
+    if (i >= kDepth && !warp_wait(&free[i % kDepth], (i / kDepth - 1) & 1, err, DERR_EMPTY_WAIT)) return false;
+    if ((threadIdx.x & 31) == 0) {
+      at[i % kDepth] = x;
+      mbar_arrive(&full[i % kDepth]);
+    }
+    __syncwarp();
+    return true;
+  }
+  EE_DEV bool get(int i, T* x, int32_t* err) {
+    if (!warp_wait(&full[i % kDepth], (i / kDepth) & 1, err, DERR_FULL_WAIT)) return false;
+    *x = at[i % kDepth];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&free[i % kDepth]);
+    return true;
+  }
+};
+
 // A stream of own blocks.
 template <int HD, int G>
 struct Stream {
   static constexpr int NR = Shape<HD>::NR;
   uint64_t full[NR], empty[NR], q_full[2], q_free[2], s_full[2], p_ready, o_done;  // Q by share & 1
   uint64_t drained;  // every MMA issued is over
+  Ring<Own> shares;
   float red[4][G], sum[4][G];
 };
+
+constexpr int kPrefix = 1, kDeep = 2;
 
 template <int HD, int G>
 struct Shared {
   static constexpr int NST = Shape<HD>::NST;
   uint64_t q_full[2], q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
   uint64_t drained[2];  // every MMA issued is over
+  Ring<Work> units;
   Stream<HD, G> own[2];
+  int role;  // kPrefix: this CTA has a piece of it; kDeep
   uint32_t tmem;
 };
 
 // The CTA's two streams of own blocks, `first` and the next of all.
 template <int HD, int G>
 EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const Plan<G>& plan, Stream<HD, G>* streams, uint8_t* memory,
-                       uint32_t tmem, int first) {
+                       uint32_t tmem, bool deep) {
   using S = Shape<HD>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
   const int t = warp < 8 ? warp >> 2 : warp >= 10;  // the stream
   Stream<HD, G>& sh = streams[t];
-  const int me = first + t;
   uint8_t* ring = memory + t * S::kStream;
   uint8_t *qs = ring + S::oQ, *ps = ring + S::oP;
   auto s_col = [&](int k) { return tmem + t * 64 + (k & 1) * 16; };
@@ -276,16 +315,24 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
   // loads queue up, and everybody's first ones wait 4 us (32 sequences of 500 to 2000 behind 256:
   // 50 us, now 42).  After a wait
   // that gave up the softmax warps go on without waiting: they still meet each other.
-  const bool deep = 2 * plan.n_pre >= (int)gridDim.x;
   auto place = [&](int item) { return deep ? item % S::NR : item % (S::NR / 3 * 2); };
   auto turn = [&](int item) { return deep ? item / S::NR : item / (S::NR / 3 * 2); };
-  int c0 = me * plan.each_own;
   bool ok = true;
-  Own u = plan.own_at(&c0, me);
+  Own u;
   if (warp == 8 || warp == 11) {
+    const int me = ((int)blockIdx.x - plan.n_pre) * 2 + t;
+    int c0 = me * plan.each_own, n = 0;
+    auto next = [&]() {
+      const Own w = plan.own_at(&c0, me);
+      ok = ok && sh.shares.put(n++, w, p.c.err);
+      return w;
+    };
+    u = next();
     const uint64_t once = l2_evict_first_policy();
     int item = 0, r = 0;
-    for (; u.s >= 0 && ok; u = plan.own_at(&c0, me)) {
+    while (u.s >= 0 && ok) {
+      const Own then = next();  // known before this one's last tile is issued
+      if (!ok) break;
       const int32_t* table = p.c.table + (int64_t)u.row * p.c.table_stride + u.first;
       int ids = lane < u.blocks ? table[lane] : 0;  // 32 at a time
       if (r >= 2) ok = warp_wait(&sh.q_free[r & 1], (r / 2 - 1) & 1, p.c.err, DERR_EMPTY_WAIT);
@@ -316,6 +363,7 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
                           (id * p.c.n_kv_heads + u.g) * 2, &sh.full[at], once);
         }
       }
+      u = then;
     }
     // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
     for (int i = max(0, item - (deep ? S::NR : S::NR / 3 * 2)); i < item; ++i)
@@ -337,8 +385,10 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
     };
     int k = 0;
     bool out = false;  // tile k's scores
-    for (int r = 0; u.s >= 0 && ok; ++r) {
-      const Own then = plan.own_at(&c0, me);
+    ok = sh.shares.get(0, &u, p.c.err);
+    for (int r = 0; ok && u.s >= 0; ++r) {
+      Own then;
+      if (!(ok = sh.shares.get(r + 1, &then, p.c.err))) break;
       const int tiles = (u.blocks + 7) >> 3;
       if (lane == 0) {
         for (int j = 0; j < tiles && ok; ++j, ++k) {
@@ -396,7 +446,15 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
     const int dim = HD == 128 ? tid : w4 * 16 + (lane & 15);
     const bool has_dim = HD == 128 || lane < 16;
     int k = 0;
-    for (int r = 0; u.s >= 0; u = plan.own_at(&c0, me), ++r) {
+    for (int r = 0;; ++r) {
+      // the four warps go on together or not at all
+      int go = sh.shares.get(r, &u, p.c.err) && u.s >= 0;
+      asm volatile(
+          "{ .reg .pred p, q; setp.ne.s32 p, %0, 0; barrier.cta.red.and.pred q, %1, 128, p; selp.s32 %0, 1, 0, q; }"
+          : "+r"(go)
+          : "r"(bar)
+          : "memory");
+      if (!go) break;
       const int tiles = (u.blocks + 7) >> 3;
       float m[G], l[G];
 #pragma unroll
@@ -529,12 +587,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&own.q_free[lane], 1);
       mbar_init(&own.s_full[lane], 1);
     }
+    own.shares.init(5);  // four softmax warps and the one that issues
     if (lane == 0) {
       mbar_init(&own.p_ready, 128);
       mbar_init(&own.o_done, 1);
       mbar_init(&own.drained, 1);
     }
     if (warp == 8) {
+      sh.units.init(10);  // eight softmax warps and the two that issue
       if (lane < S::NST) {
         mbar_init(&sh.kv_full[lane], 1);
         mbar_init(&sh.kv_empty[lane], 1);
@@ -553,14 +613,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("bar.arrive 3, %0;" ::"n"(kThreads) : "memory");
   }
   Plan<G> plan;
-  plan.init(p, gridDim.x);
-  if (!loads) {
+  int role;
+  if (loads) {
+    plan.init(p, gridDim.x);
+    role = ((int)blockIdx.x < plan.n_pre ? kPrefix : 0) | (2 * plan.n_pre >= (int)gridDim.x ? kDeep : 0);
+    if (warp == 8) {
+      if (lane == 0) sh.role = role;
+      __syncwarp();
+      asm volatile("bar.arrive 4, %0;" ::"n"(kThreads - 32) : "memory");
+    }
+  } else {
     if (warp == 9) {
       tmem_alloc(&sh.tmem, 512);
       tc_fence_before();
     }
     asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
     tc_fence_after();
+    asm volatile("bar.sync 4, %0;" ::"n"(kThreads - 32) : "memory");
+    role = sh.role;
   }
   const uint32_t tmem = loads ? 0 : sh.tmem;
   const uint32_t q_s = smem_addr(tiles), kv_s = q_s + 2 * S::kTile;
@@ -590,29 +660,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     x.phase = (u.par >> x.at ^ (uint32_t)((2 * j + kv) / S::NST)) & 1;
     return x;
   };
-  // This CTA's next unit.
-  int c0 = blockIdx.x * plan.each_pre, start = 0;
-  uint32_t par = 0;
-  auto next_unit = [&]() {
-    Work w = plan.prefix_at(&c0, blockIdx.x);
-    w.par = par;
-    w.start = start;
-    if (w.kind == 2) {
-#pragma unroll
-      for (int x = 0; x < S::NST; ++x) {
-        const int first = (x - start + S::NST) % S::NST;
-        par ^= first < 2 * w.tiles ? (uint32_t)((2 * w.tiles - first + S::NST - 1) / S::NST & 1) << x : 0;
-      }
-      start = (start + 2 * w.tiles) % S::NST;
-    } else {
-#pragma unroll
-      for (int x = 0; x < 4 * S::D; ++x) {
-        const int first = x % (2 * S::D) / 2, n = steps_of(w, x / (2 * S::D));
-        par ^= first < n ? (uint32_t)((n - first + S::D - 1) / S::D & 1) << x : 0;
-      }
-    }
-    return w;
-  };
   auto landed = [&](const Place& x) {
     const bool r = mbar_wait_bounded(&sh.kv_full[x.at], x.phase, p.c.err, DERR_FULL_WAIT);
     tc_fence_after();
@@ -634,14 +681,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_f16_ta(o_col(t), s_col(t) + kk * 8, smem_desc_sw128_mn(b + kk * 2 * S::kRows8, 1024, S::kRows8), id_pv, acc || kk > 0);
   };
 
-  if ((int)blockIdx.x >= plan.n_pre) {
-    own_blocks<HD, G>(p, maps, c, plan, sh.own, tiles, tmem, ((int)blockIdx.x - plan.n_pre) * 2);
+  if (!(role & kPrefix)) {
+    own_blocks<HD, G>(p, maps, c, plan, sh.own, tiles, tmem, role & kDeep);
   } else if (warp == 8) {
+    // this CTA's next unit
+    int c0 = blockIdx.x * plan.each_pre, start = 0, n = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    auto next_unit = [&]() {
+      Work w = plan.prefix_at(&c0, blockIdx.x);
+      w.par = par;
+      w.start = start;
+      if (w.kind == 2) {
+#pragma unroll 1
+        for (int x = 0; x < S::NST; ++x) {
+          const int first = (x - start + S::NST) % S::NST;
+          par ^= first < 2 * w.tiles ? (uint32_t)((2 * w.tiles - first + S::NST - 1) / S::NST & 1) << x : 0;
+        }
+        start = (start + 2 * w.tiles) % S::NST;
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < 4 * S::D; ++x) {
+          const int first = x % (2 * S::D) / 2, n = steps_of(w, x / (2 * S::D));
+          par ^= first < n ? (uint32_t)((n - first + S::D - 1) / S::D & 1) << x : 0;
+        }
+      }
+      ok = ok && sh.units.put(n++, w, p.c.err);
+      return w;
+    };
     Work u = next_unit();
     const int b8 = lane & 7;
     int at0 = 0, ends[2] = {0, 0};  // the next place of a wide unit
     uint32_t loaded = 0;  // as Work's par, but for every tile
-    bool ok = true;
     for (; u.kind && ok; u = next_unit()) {
       const int nblk = (u.have + 15) >> 4;
       const int32_t* bt = p.c.table + u.first;  // the first row's
@@ -709,10 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ends[t] > 0) mbar_wait_bounded(&sh.q_full[t], (ends[t] - 1) & 1, p.c.err, DERR_DRAIN_WAIT);
   } else if (warp == 9 || warp == 10) {
     const int me = warp - 9;
-    Work u = next_unit();
+    Work u;
     int steps[2] = {0, 0}, ends[2] = {0, 0}, kind_before = 0;
     bool ok = true;
-    for (; u.kind && ok; u = next_unit()) {
+    for (int i = 0; ok && sh.units.get(i, &u, p.c.err) && u.kind; ++i) {
       const int nk = u.tiles;
       const bool wide = u.kind == 2;
       // Behind the wide units stream 1's products go from warp 9 to warp 10: the first ones
@@ -814,10 +885,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, r = tid & 127;  // stream and row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = s_col(t) + lane_base, o_at = o_col(t) + lane_base;
-    Work u = next_unit();
+    Work u;
     int steps = 0, ends = 0;
     bool ok = true;
-    for (; u.kind && ok; u = next_unit()) {
+    for (int i = 0; ok && sh.units.get(i, &u, p.c.err) && u.kind; ++i) {
       const bool wide = u.kind == 2;
       const int n = steps_of(u, t);
       const int row = r + (wide ? t * 128 : 0);  // of the unit
