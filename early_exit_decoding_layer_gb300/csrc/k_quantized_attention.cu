@@ -481,9 +481,9 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
 }
 
 // The join: a CTA adds the parts of J query heads of a sequence, where there are any: 8 / J warps
-// each, eight parts in flight a warp.  J is all heads of a kv head where there are many -- CTAs
-// start 6 ns after one another, whatever they do -- and one where there are few (one sequence of
-// 16384 tokens: 13 us, with J = G 17).
+// each, eight parts in flight a warp.  J is as small as two CTAs per SM allow: CTAs start 6 ns after
+// one another, whatever they do, but a warp that walks many parts takes long too (one sequence
+// of 16384 tokens, 57 parts: 13 us, with J = G = 4 17).
 constexpr int kJoinThreads = 256;
 
 template <int HD, int G, int J>
@@ -593,14 +593,20 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  const bool few = p.batch * p.n_heads <= 2 * sms;
-  cfg.gridDim = dim3((unsigned)(p.batch * (few ? p.n_heads : p.c.n_kv_heads)));
+  int J = 1;
+  while (J < G && p.batch * p.n_heads > 2 * sms * J) J *= 2;
+  cfg.gridDim = dim3((unsigned)(p.batch * (p.n_heads / J)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, pieces, least)
-             : cudaLaunchKernelEx(&cfg, k_join<HD, G, G>, p, pieces, least);
+  if constexpr (G >= 8)
+    if (J == 8) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 8>, p, pieces, least);
+  if constexpr (G >= 4)
+    if (J == 4) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 4>, p, pieces, least);
+  if constexpr (G >= 2)
+    if (J == 2) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 2>, p, pieces, least);
+  return cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, pieces, least);
 }
 
 }  // namespace

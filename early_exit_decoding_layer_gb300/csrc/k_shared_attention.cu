@@ -1031,9 +1031,9 @@ EE_DEV float within_half(float y) {
 }
 
 // The join: a CTA adds the parts, of the prefix and of its own blocks, of J query heads of a
-// sequence: 8 / J warps each, eight parts in flight a warp.  J is all heads of a kv head where
-// there are many -- CTAs start 6 ns after one another, whatever they do: one for each of 4096 rows
-// took 20 us -- and one where there are few.
+// sequence: 8 / J warps each, eight parts in flight a warp.  J is as small as two CTAs per SM allow:
+// CTAs start 6 ns after one another, whatever they do (one for each of 4096 rows took 20 us), but
+// a warp that walks many parts takes long too.
 constexpr int kJoinThreads = 256;
 
 template <int HD, int G, int J>
@@ -1183,10 +1183,17 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const bool few = p.batch * p.n_heads <= 2 * sms;
-  cfg.gridDim = dim3((unsigned)(p.batch * (few ? p.n_heads : p.c.n_kv_heads)));
+  int J = 1;
+  while (J < G && p.batch * p.n_heads > 2 * sms * J) J *= 2;
+  cfg.gridDim = dim3((unsigned)(p.batch * (p.n_heads / J)));
   cfg.blockDim = dim3(kJoinThreads);
-  return few ? cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, ctas) : cudaLaunchKernelEx(&cfg, k_join<HD, G, G>, p, ctas);
+  if constexpr (G >= 8)
+    if (J == 8) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 8>, p, ctas);
+  if constexpr (G >= 4)
+    if (J == 4) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 4>, p, ctas);
+  if constexpr (G >= 2)
+    if (J == 2) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 2>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, ctas);
 }
 
 }  // namespace
