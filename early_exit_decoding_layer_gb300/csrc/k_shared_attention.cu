@@ -49,9 +49,8 @@ constexpr int kMaxPieces = 160;
 // Times in 200 cycles, by which the CTAs are shared out: a prefix tile, a unit's first loads and
 // its part's way out, a CTA's beginning; an own block of a stream, a pair's beginning in blocks, a
 // stream's, and a block (of hd 128) where all SMs together are as fast as the memory.
-constexpr int kWideCost = 18, kNarrowCost = 9, kStartCost = 25;
-constexpr float kPrefixBegin = 60.0f, kOwnCost = 2.0f, kOwnBegin = 45.0f, kOwnShare = 0.0126f;
-constexpr int kOwnStart = 4;
+constexpr int kWideCost = 18, kNarrowCost = 12, kStartCost = 25, kOwnStart = 11;
+constexpr float kPrefixBegin = 85.0f, kOwnCost = 2.1f, kOwnBegin = 50.0f, kOwnShare = 0.0126f;
 
 template <int HD>
 struct Shape {
@@ -153,24 +152,21 @@ struct Plan {
     for (int rt = 0; rt < 2; ++rt)
       pre_cost[rt] = rows_of(rt) > 0 ? places(tiles, kStartCost, rows_of(rt) > 128 ? kWideCost : kNarrowCost) : 0;
     pre_end = hkv * (pre_cost[0] + pre_cost[1]);
-    // of all numbers of prefix CTAs the one with which the slower kind is done first
+    // of 32 numbers of prefix CTAs, one a lane, the one with which the slower kind is done first
     n_pre = 0;
     if (pre_end > 0 && own_end > 0) {
-      unsigned best = 0xffffffffu;
-      const float share = kOwnShare / 128 * p.c.head_dim * own_end;
-#pragma unroll 1
-      for (int n = lane + 1; n < ctas; n += 32) {
-        const float a = kPrefixBegin + fmaxf(kNarrowCost, __fdividef(pre_end, n));
-        const float b = kOwnBegin + fmaxf(kOwnCost * fmaxf(kOwnStart + 4, __fdividef(own_end, 2 * (ctas - n))), share);
-        best = min(best, (unsigned)fminf(fmaxf(a, b) * 8.0f, 16777215.0f) << 8 | (unsigned)n);
-      }
-      n_pre = (int)(__reduce_min_sync(0xffffffffu, best) & 255u);
+      const int n = 1 + lane * max(0, ctas - 2) / 31;
+      const int pairs = hkv * (__popc(__ballot_sync(0xffffffffu, size[0] > 0)) + __popc(__ballot_sync(0xffffffffu, size[1] > 0)));
+      const float a = kPrefixBegin + fmaxf(kNarrowCost, __fdividef(pre_end, n));
+      const float b = kOwnBegin + fmaxf(kOwnCost * fmaxf(kOwnStart + 1, __fdividef(own_end, 2 * max(1, ctas - n))),
+                                        kOwnShare / 128 * p.c.head_dim * (own_end - kOwnStart * pairs));
+      n_pre = (int)(__reduce_min_sync(0xffffffffu, (unsigned)fminf(fmaxf(a, b) * 8.0f, 16777215.0f) << 8 | (unsigned)n) & 255u);
     } else if (pre_end > 0) {
       n_pre = ctas;
     }
     const int n = max(1, n_pre), streams = 2 * max(1, ctas - n_pre);
     each_pre = max(kNarrowCost, (pre_end + n - 1) / n);
-    each_own = max(kOwnStart + 4, (own_end + streams - 1) / streams);
+    each_own = max(kOwnStart + 1, (own_end + streams - 1) / streams);
   }
   // The first tile (or block) of a unit at x that stands at place c or behind it.
   EE_DEV static int item_at(int c, int x, int n, int start, int cost) {
@@ -758,19 +754,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int a = id0, b = id1;
         id0 = block_id(j + 2);
         id1 = block_id(j + 3);
-        if (u.kind == 2) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (j + (x >> 1) < u.tiles) {
-              load(j + (x >> 1), x & 1, x < 2 ? a : b, at0);
-              at0 = at0 + 1 == S::NST ? 0 : at0 + 1;
-            }
-          }
-        } else {
-          // K of both streams before their V, whose places are free later
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (j + (x & 1) < u.tiles) load(j + (x & 1), x >> 1, x & 1 ? b : a, narrow_place(u, x & 1, j >> 1, x >> 1).at);
+        // wide: K and V of a tile, then of the next; narrow: K of both streams before their V,
+        // whose places are free later
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          const bool wide = u.kind == 2;
+          const int second = wide ? x >> 1 : x & 1, kv = wide ? x & 1 : x >> 1;
+          if (j + second >= u.tiles) continue;
+          load(j + second, kv, second ? b : a, wide ? at0 : narrow_place(u, second, j >> 1, kv).at);
+          at0 = at0 + 1 == S::NST ? 0 : at0 + 1;
         }
       }
     }
