@@ -1,14 +1,15 @@
 // How the decode attentions with fp16 rows share their work: the blocks of all
 // (sequence, kv head) pairs in a row, cut into equal pieces, one for each CTA.
 //
-// Lengths are on the device, so every warp that needs the plan makes it (two lengths a lane
-// and a scan).  A piece may begin and end within a pair: what a CTA finds there is a
+// Lengths are on the device, so a warp of each CTA makes the plan (two lengths a lane and a
+// scan).  A piece may begin and end within a pair: what a CTA finds there is a
 // part, (O, m, l) in the scratch, and the join adds a pair's parts in the order of the
 // CTAs.  A CTA has at most two of them, of its first pair and of its last; pairs that lie
 // within a piece are finished where they are.
 #pragma once
 
 #include "ee_cache_ops.cuh"
+#include "ee_tcgen05.cuh"
 
 namespace ee {
 
@@ -83,6 +84,40 @@ struct DecodePlan {
     r.have = min(n - r.first * 16, r.blocks * 16);
     if (r.blocks < nb) r.slot = 2 * me + (c > begin);
     return r;
+  }
+};
+
+// Units or shares on their way from the warp that finds (and loads) them to those that work on
+// them: code that stands once in the kernel, because a CTA's first instructions take as
+// long to come as its first tiles.
+template <typename T>
+struct Ring {
+  static constexpr int kDepth = 4;
+  uint64_t full[kDepth], free[kDepth];
+  T at[kDepth];
+
+  EE_DEV void init(int readers) {  // one lane per place
+    const int lane = threadIdx.x & 31;
+    if (lane < kDepth) {
+      mbar_init(&full[lane], 1);
+      mbar_init(&free[lane], readers);
+    }
+  }
+  EE_DEV bool put(int i, const T& x, int32_t* err) {
+    if (i >= kDepth && !warp_wait(&free[i % kDepth], (i / kDepth - 1) & 1, err, DERR_EMPTY_WAIT)) return false;
+    if ((threadIdx.x & 31) == 0) {
+      at[i % kDepth] = x;
+      mbar_arrive(&full[i % kDepth]);
+    }
+    __syncwarp();
+    return true;
+  }
+  EE_DEV bool get(int i, T* x, int32_t* err) {
+    if (!warp_wait(&full[i % kDepth], (i / kDepth) & 1, err, DERR_FULL_WAIT)) return false;
+    *x = at[i % kDepth];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&free[i % kDepth]);
+    return true;
   }
 };
 

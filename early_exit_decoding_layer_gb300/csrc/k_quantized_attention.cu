@@ -65,6 +65,7 @@ struct Shared {
   uint64_t q_ready[2], q_free[2];  // by share & 1
   uint64_t drained;                // every MMA issued is over
   uint32_t tmem;
+  Ring<Share> shares;
   float unscale[2][G], red[4][G], sum[4][G];
 };
 
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
   // The loads begin before anything else is ready: their warp makes the barriers, and
   // does not wait for the others.
   if (warp == 4) {
+    sh.shares.init(7);
     if (lane == 0) {
       for (int i = 0; i < NS; ++i) {
         mbar_init(&sh.full[i], 33);  // the copies' bytes; 32 lanes' exponents
@@ -148,8 +150,6 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
     __syncwarp();
     asm volatile("bar.arrive 2, 256;" ::: "memory");
   }
-  DecodePlan plan;
-  plan.init(p, gridDim.x, least, whole, me);
   if (warp != 4) {
     if (warp == 5) {
       tmem_alloc(&sh.tmem, 4 * N);
@@ -163,9 +163,20 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
   auto o_col = [&](int r) { return tmem + 2 * N + (r & 1) * N; };
 
   if (warp == 4) {
-    int t = 0;
-    for (int at = plan.begin; at < plan.end && ok;) {
-      const Share u = plan.at(at, me);
+    DecodePlan plan;
+    plan.init(p, gridDim.x, least, whole, me);
+    const uint64_t once = l2_evict_first_policy();
+    int t = 0, n = 0, at = plan.begin;
+    auto next = [&]() {
+      const Share w = plan.at(at, me);
+      at += w.blocks;
+      ok = ok && sh.shares.put(n++, w, p.c.err);
+      return w;
+    };
+    Share u = next();
+    while (u.s >= 0 && ok) {
+      const Share then = next();  // known before this one's last tile is issued
+      if (!ok) break;
       const int32_t* table = p.c.table + (int64_t)u.s * p.c.table_stride + u.first;
       int ids = 0;
       for (int j = 0; j < u.blocks && ok; j += 8, ++t) {
@@ -183,14 +194,19 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], (uint32_t)here * Lay::kBlock);
         __syncwarp();
         if (lane < here)
-          tma_load_5d(smem_addr(ring + st * Lay::kTile + lane * Lay::kBlock), &map, 0, 0, 0, 0, id * p.c.n_kv_heads + u.g,
-                      &sh.full[st]);
+          tma_stream_5d(smem_addr(ring + st * Lay::kTile + lane * Lay::kBlock), &map, 0, 0, 0, 0, id * p.c.n_kv_heads + u.g,
+                        &sh.full[st], once);
         if ((lane >> 2) < here)
           copy8(smem_addr(es + st * 256 + lane * 8), p.exponents + ((int64_t)eid * p.c.n_kv_heads + u.g) * 32 + (lane & 3) * 8);
         copies_arrive(&sh.full[st]);
       }
-      at += u.blocks;
+      u = then;
     }
+    // empty sequences
+    for (int s = me; s < p.batch; s += gridDim.x)
+      if (__shfl_sync(0xffffffffu, s < 32 ? plan.tokens[0] : plan.tokens[1], s & 31) == 0)
+        for (int i = lane * 8; i < p.n_heads * HD; i += 256)
+          *reinterpret_cast<uint4*>(p.o + s * p.o_stride + i) = make_uint4(0, 0, 0, 0);
     // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
     for (int i = max(0, t - NS); i < t; ++i)
       mbar_wait_bounded(&sh.full[i % NS], (uint32_t)(i / NS) & 1, p.c.err, DERR_DRAIN_WAIT);
@@ -205,12 +221,13 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
       mma_commit(&sh.s_full[t & 1]);
       if (last) mma_commit(&sh.q_free[r & 1]);
     };
-    int t = 0, r = 0, at = plan.begin;
-    Share u = plan.at(at, me);
+    int t = 0;
     bool out = false;  // tile t's scores
-    for (; u.s >= 0 && ok; ++r) {
-      at += u.blocks;
-      const Share then = plan.at(at, me);
+    Share u;
+    ok = sh.shares.get(0, &u, p.c.err);
+    for (int r = 0; ok && u.s >= 0; ++r) {
+      Share then;
+      if (!(ok = sh.shares.get(r + 1, &then, p.c.err))) break;
       const int tiles = (u.blocks + 7) >> 3;
       if (lane == 0) {
         for (int j = 0; j < tiles && ok; ++j, ++t) {
@@ -264,17 +281,9 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
     }
     __syncwarp();
   } else if (warp >= 6) {
-    // empty sequences
-    for (int s = me; s < p.batch; s += gridDim.x) {
-      const int n = __shfl_sync(0xffffffffu, s < 32 ? plan.tokens[0] : plan.tokens[1], s & 31);
-      if (n == 0)
-        for (int i = (warp - 6) * 32 + lane; i < p.n_heads * HD; i += 64) p.o[s * p.o_stride + i] = 0;
-    }
     constexpr int kHeads = (G + 1) / 2, kPer = HD / 32;
-    int r = 0;
-    for (int at = plan.begin; at < plan.end && ok; ++r) {
-      const Share u = plan.at(at, me);
-      at += u.blocks;
+    Share u;
+    for (int r = 0; ok && sh.shares.get(r, &u, p.c.err) && u.s >= 0; ++r) {
       const uint16_t* q = p.q + u.s * p.q_stride + (int64_t)u.g * G * HD;
       float x[kHeads][kPer];
 #pragma unroll
@@ -333,10 +342,17 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
     // M = 64: rows 16 w .. 16 w + 15 in the first lanes of warp w's part of tensor memory
     const int dim = HD == 128 ? tid : warp * 16 + (lane & 15);
     const bool has_dim = HD == 128 || lane < 16;
-    int t = 0, r = 0;
-    for (int at = plan.begin; at < plan.end; ++r) {
-      const Share u = plan.at(at, me);
-      at += u.blocks;
+    int t = 0;
+    Share u;
+    for (int r = 0;; ++r) {
+      // the four warps go on together or not at all
+      int go = sh.shares.get(r, &u, p.c.err) && u.s >= 0;
+      asm volatile(
+          "{ .reg .pred p, q; setp.ne.s32 p, %0, 0; barrier.cta.red.and.pred q, 1, 128, p; selp.s32 %0, 1, 0, q; }"
+          : "+r"(go)
+          :
+          : "memory");
+      if (!go) break;
       const int tiles = (u.blocks + 7) >> 3;
       if (ok) ok = warp_wait(&sh.q_ready[r & 1], (r >> 1) & 1, p.c.err, DERR_FULL_WAIT);
       float unscale[G], m[G], l[G];

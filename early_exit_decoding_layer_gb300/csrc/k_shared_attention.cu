@@ -37,7 +37,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "ee_cache_ops.cuh"
+#include "ee_decode_plan.cuh"
 #include "ee_tcgen05.cuh"
 
 namespace ee {
@@ -236,40 +236,6 @@ EE_DEV Scratch scratch_of(const DecodeParams& p, bool own) {
   r.o += before * p.c.head_dim;
   return r;
 }
-
-// Units or shares on their way from the warp that finds (and loads) them to those that work on
-// them: code that stands once in the kernel, because a CTA's first instructions take as
-// long to come as its first tiles.
-template <typename T>
-struct Ring {
-  static constexpr int kDepth = 4;
-  uint64_t full[kDepth], free[kDepth];
-  T at[kDepth];
-
-  EE_DEV void init(int readers) {  // one lane per place
-    const int lane = threadIdx.x & 31;
-    if (lane < kDepth) {
-      mbar_init(&full[lane], 1);
-      mbar_init(&free[lane], readers);
-    }
-  }
-  EE_DEV bool put(int i, const T& x, int32_t* err) {
-    if (i >= kDepth && !warp_wait(&free[i % kDepth], (i / kDepth - 1) & 1, err, DERR_EMPTY_WAIT)) return false;
-    if ((threadIdx.x & 31) == 0) {
-      at[i % kDepth] = x;
-      mbar_arrive(&full[i % kDepth]);
-    }
-    __syncwarp();
-    return true;
-  }
-  EE_DEV bool get(int i, T* x, int32_t* err) {
-    if (!warp_wait(&full[i % kDepth], (i / kDepth) & 1, err, DERR_FULL_WAIT)) return false;
-    *x = at[i % kDepth];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&free[i % kDepth]);
-    return true;
-  }
-};
 
 // A stream of own blocks.
 template <int HD, int G>
