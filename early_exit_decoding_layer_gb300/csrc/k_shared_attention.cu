@@ -869,7 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (busy) {
           // In pieces of 32 keys, by loops that stay loops: a CTA has few steps, and its
           // instructions come from L2, or from DRAM behind everybody's tiles.  (All 128 keys in
-          // registers: the first step took 6000 to 40000 cycles, now XXX; the others 1700, now YYY.)
+          // registers: the first step took 9000 cycles, and 40000 beside CTAs that kept the memory
+          // busy, now 4500; the others 1700, now 1900.)
           uint32_t s[32];
           auto load = [&](int q) {
             tmem_ld32(s_at + 32 * q, s);
