@@ -168,8 +168,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
     const uint64_t once = l2_evict_first_policy();
     int t = 0, n = 0, at = plan.begin;
     auto next = [&]() {
-      const Share w = plan.at(at, me);
-      at += w.blocks;
+      const Share w = plan.at(&at, me);
       ok = ok && sh.shares.put(n++, w, p.c.err);
       return w;
     };
@@ -511,9 +510,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   const int g = first / G, h = first % G + warp % J;
   DecodePlan plan;
   plan.init(p, pieces, least, false, 0);
-  const int nb = __shfl_sync(0xffffffffu, s < 32 ? plan.blocks[0] : plan.blocks[1], s & 31);
-  const int from = __shfl_sync(0xffffffffu, s < 32 ? plan.base[0] : plan.base[1], s & 31) * plan.hkv + g * nb;
-  const int w0 = from / plan.each, n = nb == 0 ? 0 : (from + nb - 1) / plan.each - w0 + 1;
+  const int nb = (__shfl_sync(0xffffffffu, s < 32 ? plan.tokens[0] : plan.tokens[1], s & 31) + 15) >> 4;
+  const int from = __shfl_sync(0xffffffffu, s < 32 ? plan.base[0] : plan.base[1], s & 31) * plan.hkv +
+                   g * __shfl_sync(0xffffffffu, s < 32 ? plan.size[0] : plan.size[1], s & 31);
+  const int last = nb < 2 ? from : from + plan.start + nb - 1;  // the last block's place
+  const int w0 = from / plan.each, n = nb == 0 ? 0 : last / plan.each - w0 + 1;
   grid_dep_wait();
   if (n < 2) return;
   // the first CTA has the pair as its last one, unless it begins with it
@@ -598,7 +599,7 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
                  s[4] = {(uint64_t)HD, (uint64_t)HD * 16, (uint64_t)HD * 8, (uint64_t)HD * 32};
   const uint32_t b[5] = {(uint32_t)HD, 8, 2, 2, 1};
   if (!encode_tensor_map_bytes(&map, 5, p.codes, d, s, b)) return cudaErrorInvalidValue;
-  const int64_t most = (int64_t)p.batch * p.c.n_kv_heads * ((p.c.max_ctx + 15) / 16);
+  const int64_t most = (int64_t)p.batch * p.c.n_kv_heads * (DecodePlan::kStart + (p.c.max_ctx + 15) / 16);
   const int least = 8;
   const bool whole = p.c.max_ctx <= kTokens;
   const int pieces = (int)std::min<int64_t>(std::min(Lay::kCtas * sms, kMaxCtas), (most + least - 1) / least);
