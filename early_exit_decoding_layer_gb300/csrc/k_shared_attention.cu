@@ -13,11 +13,13 @@
 //   wide (a unit of 129 to 256 rows)  each stream has 128 rows, both see every key tile
 //   narrow (up to 128 rows)  both have the same rows, and every second key tile
 //   warps 4t .. 4t + 3   a thread per row: S_t to registers, running maximum and sum,
-//                        P_t = exp2(c S - c m) as fp16 over S_t's columns
+//                        P_t = exp2(c S - c m) as fp16 over S_t's columns, in two halves
+//                        of 64 keys, so that half of P V is done before the other is there
 //   warp 9 (one thread)  the products, O_t += P_t V_j and S_t = Q K_j'^T; in narrow units
 //                        stream 0's
 //   warp 10              narrow: stream 1's products.  wide: waits for K and V tiles in warp
-//                        9's place, which has none of the tensor core's time to lose
+//                        9's place, which has none of the tensor core's time to lose, and
+//                        frees those that are done with
 //   warp 8               Q, K and V by TMA, a box per 16-slot block, into a ring
 //
 // Own blocks: S^T = K Q^T and O^T = V^T P with the cache as the big operand, 128 tokens x 16
@@ -252,7 +254,7 @@ constexpr int kPrefix = 1, kDeep = 2;
 template <int HD, int G>
 struct Shared {
   static constexpr int NST = Shape<HD>::NST;
-  uint64_t q_full[2], q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full[2], q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2][2], o_done[2];  // P in halves
   uint64_t drained[2];  // every MMA issued is over
   Ring<Work> units;
   Stream<HD, G> own[2];
@@ -563,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane < 2) {
         mbar_init(&sh.s_full[lane], 1);
-        mbar_init(&sh.p_ready[lane], 129);  // its warpgroup, and the tiles that the products need
+        mbar_init(&sh.p_ready[lane][0], 129);  // its warpgroup, and the tiles that the products need
+        mbar_init(&sh.p_ready[lane][1], 128);
         mbar_init(&sh.q_full[lane], 1);
         mbar_init(&sh.q_free[lane], 1);  // the stream's last product with it
         mbar_init(&sh.o_done[lane], 1);
@@ -629,18 +632,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   constexpr uint32_t id_qk = instr_desc(0, kKeys, 128), id_pv = instr_desc(0, HD, 128, true);
-  auto product_s = [&](int t, const Place& k) {  // S_t = Q_t K at a place
-    const uint32_t a = q_s + t * S::kTile, b = kv_s + k.at * S::kTile;
+  const uint64_t q_desc = smem_desc_sw128(q_s), k_desc = smem_desc_sw128(kv_s, S::kRows8),
+                 v_desc = smem_desc_sw128_mn(kv_s, 1024, S::kRows8);
+  auto product_s = [&](int t, int at) {  // S_t = Q_t K at a place
+    const uint64_t a = q_desc + t * (S::kTile >> 4), b = k_desc + at * (S::kTile >> 4);
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk)
-      mma_f16(s_col(t), smem_desc_sw128(a + (kk >> 2) * S::kHalf + (kk & 3) * 32),
-              smem_desc_sw128(b + (kk >> 2) * 1024 + (kk & 3) * 32, S::kRows8), id_qk, kk > 0);
+      mma_f16(s_col(t), a + (((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4), b + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
   };
-  auto product_o = [&](int t, const Place& v, bool acc) {  // O_t (+)= P_t, V at a place
-    const uint32_t b = kv_s + v.at * S::kTile;
+  auto product_o = [&](int t, int h, int at, bool acc) {  // O_t (+)= half h of P_t, V at a place
+    const uint64_t b = v_desc + at * (S::kTile >> 4);
 #pragma unroll
-    for (int kk = 0; kk < kKeys / 16; ++kk)
-      mma_f16_ta(o_col(t), s_col(t) + kk * 8, smem_desc_sw128_mn(b + kk * 2 * S::kRows8, 1024, S::kRows8), id_pv, acc || kk > 0);
+    for (int kk = h * kKeys / 32; kk < (h + 1) * kKeys / 32; ++kk)
+      mma_f16_ta(o_col(t), s_col(t) + kk * 8, b + (kk * 2 * S::kRows8 >> 4), id_pv, acc || kk > h * kKeys / 32);
   };
 
   if (!(role & kPrefix)) {
@@ -739,18 +743,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9 || warp == 10) {
     const int me = warp - 9;
     Work u;
-    int steps[2] = {0, 0}, ends[2] = {0, 0}, kind_before = 0;
+    int steps[2] = {0, 0}, ends[2] = {0, 0};
     bool ok = true;
     for (int i = 0; ok && sh.units.get(i, &u, p.c.err) && u.kind; ++i) {
       const int nk = u.tiles;
       const bool wide = u.kind == 2;
-      // Behind the wide units stream 1's products go from warp 9 to warp 10: the first ones
-      // wait for the last ones there (and for P first: then no older O is taken for the last).
-      const bool change = me == 1 && kind_before == 2 && !wide;
       if (lane == 0) {
-        if (change)
-          ok = mbar_wait_bounded(&sh.p_ready[1], (steps[1] - 1) & 1, p.c.err, DERR_FULL_WAIT) &&
-               mbar_wait_bounded(&sh.o_done[1], (ends[1] - 1) & 1, p.c.err, DERR_FULL_WAIT);
         auto q_there = [&](int t) {
           const bool r = mbar_wait_bounded(&sh.q_full[t], ends[t] & 1, p.c.err, DERR_FULL_WAIT);
           tc_fence_after();
@@ -762,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto scores = [&](int k) {
             const Place x = narrow_place(u, t, k, 0);
             if (!landed(x)) return false;
-            product_s(t, x);
+            product_s(t, x.at);
             mma_commit(&sh.s_full[t]);
             mma_commit(&sh.kv_empty[x.at]);
             return true;
@@ -771,11 +769,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < n && ok; ++k) {
             const Place v = narrow_place(u, t, k, 1);
             if (!(ok = landed(v))) break;
-            mbar_arrive(&sh.p_ready[t]);
-            if (!(ok = mbar_wait_bounded(&sh.p_ready[t], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
+            mbar_arrive(&sh.p_ready[t][0]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!ok || !(ok = mbar_wait_bounded(&sh.p_ready[t][h], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
+              tc_fence_after();
+              product_o(t, h, v.at, k > 0 || h > 0);
+            }
+            if (!ok) break;
             ++steps[t];
-            tc_fence_after();
-            product_o(t, v, k > 0);
             mma_commit(&sh.kv_empty[v.at]);
             if (k + 1 < n) ok = scores(k + 1);
             else mma_commit(&sh.o_done[t]);
@@ -786,24 +788,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the tensor core time: a step's O and next S products of a stream go out together, each
           // wait that can be left to another warp is, and commits are few.  The commit behind
           // S_t(j + 1) also says that O_t has P_t V_j.
-          auto scores = [&](int t, int j) {
-            product_s(t, wide_place(u, j, 0));
+          auto scores = [&](int t, int at) {
+            product_s(t, at);
             mma_commit(&sh.s_full[t]);
           };
+          int at = u.start;
           ok = ok && q_there(0) && q_there(1) && landed(wide_place(u, 0, 0));
           if (ok) {
-            scores(0, 0);
-            scores(1, 0);
+            scores(0, at);
+            scores(1, at);
           }
           for (int j = 0; j < nk && ok; ++j) {
+            const int v = at + 1 == S::NST ? 0 : at + 1;
+            at = v + 1 == S::NST ? 0 : v + 1;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               // P_t(j) is in tensor memory, V_j and K_{j + 1} have landed
-              if (!ok || !(ok = mbar_wait_bounded(&sh.p_ready[t], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (!ok || !(ok = mbar_wait_bounded(&sh.p_ready[t][h], steps[t] & 1, p.c.err, DERR_FULL_WAIT))) break;
+                tc_fence_after();
+                product_o(t, h, v, j > 0 || h > 0);
+              }
+              if (!ok) break;
               ++steps[t];
-              tc_fence_after();
-              product_o(t, wide_place(u, j, 1), j > 0);
-              if (j + 1 < nk) scores(t, j + 1);
+              if (j + 1 < nk) scores(t, at);
               else mma_commit(&sh.o_done[t]);
             }
           }
@@ -811,19 +820,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (wide && me == 1) {
-        // Waits for V_j and K_{j + 1} on behalf of the MMA thread: P_t(j)'s barriers count
-        // this arrival too.
+        // Waits for V_j and K_{j + 1} on behalf of the MMA thread (P_t(j)'s barriers count this
+        // arrival too), and frees the tiles of products that are over: stream 1's come last in a
+        // step.  (Its S_1(j + 1) waits for this warp, which so misses no phase of s_full.)
         for (int j = 0; j < nk && ok; ++j) {
           const Place v = wide_place(u, j, 1), k = wide_place(u, j + 1, 0);
           ok = warp_wait(&sh.kv_full[v.at], v.phase, p.c.err, DERR_FULL_WAIT);
           if (ok && j + 1 < nk) ok = warp_wait(&sh.kv_full[k.at], k.phase, p.c.err, DERR_FULL_WAIT);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            // one phase of p_ready per step: the one before has to be over
-            if (ok && steps[t] + j > 0) ok = warp_wait(&sh.p_ready[t], (steps[t] + j - 1) & 1, p.c.err, DERR_FULL_WAIT);
-            if (ok && lane == 0) mbar_arrive(&sh.p_ready[t]);
+          // one phase of p_ready per step: the one before has to be over
+          if (ok && steps[0] + j > 0) ok = warp_wait(&sh.p_ready[0][0], (steps[0] + j - 1) & 1, p.c.err, DERR_FULL_WAIT);
+          if (ok && lane == 0) mbar_arrive(&sh.p_ready[0][0]);
+          if (ok) ok = warp_wait(&sh.s_full[1], (steps[1] + j) & 1, p.c.err, DERR_FULL_WAIT);
+          if (ok && steps[1] + j > 0) ok = warp_wait(&sh.p_ready[1][0], (steps[1] + j - 1) & 1, p.c.err, DERR_FULL_WAIT);
+          if (ok && lane == 0) {
+            if (j > 0) mbar_arrive(&sh.kv_empty[wide_place(u, j - 1, 1).at]);
+            mbar_arrive(&sh.kv_empty[wide_place(u, j, 0).at]);
+            mbar_arrive(&sh.p_ready[1][0]);
           }
         }
+        // and the last V's; so stream 1's products, which narrow units take from this warp, are over
+        if (ok) ok = warp_wait(&sh.o_done[1], ends[1] & 1, p.c.err, DERR_FULL_WAIT);
+        if (ok && lane == 0) mbar_arrive(&sh.kv_empty[wide_place(u, nk - 1, 1).at]);
       }
       ok = __all_sync(0xffffffffu, ok);
       // both warps count both streams' steps (those that they made themselves are counted)
@@ -832,7 +849,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       steps[1] = __shfl_sync(0xffffffffu, steps[1], 0) + ((wide ? me == 0 : me == 1) ? 0 : n1);
       ends[0] += n0 > 0;
       ends[1] += n1 > 0;
-      kind_before = u.kind;
     }
     if (lane == 0) {  // and so are the products, before tensor memory is given back
       mma_commit(&sh.drained[me]);
@@ -851,21 +867,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = steps_of(u, t);
       const int row = r + (wide ? t * 128 : 0);  // of the unit
       const bool busy = row - lane < u.rows;     // a row of this warp is the unit's
-      // In wide units stream 1's products come last in a step.  (In narrow ones commits
-      // say that a tile is free.)
-      const bool frees = wide && r == 0 && t == 1;
       float m = -INFINITY, l = 0.0f;
       for (int k = 0; k < n && ok; ++k) {
         const int j = tile_of(u, t, k);
         if (!(ok = warp_wait(&sh.s_full[t], steps & 1, p.c.err, DERR_FULL_WAIT))) break;
         ++steps;
         tc_fence_after();
-        if (frees) {  // the tiles of the products before are free
-          if (j > 0) mbar_arrive(&sh.kv_empty[wide_place(u, j - 1, 1).at]);
-          mbar_arrive(&sh.kv_empty[wide_place(u, j, 0).at]);
-        }
         if (r == 0 && k == n - 1) mbar_arrive(&sh.q_free[t]);  // the stream's last product with Q
         const int lim = u.have - j * kKeys;                 // keys of the tile that exist
+        if (lim < kKeys) {
+          // slots behind the last token hold anything: their V becomes zero
+          const Place v = wide ? wide_place(u, j, 1) : narrow_place(u, t, k, 1);
+          if (!(ok = warp_wait(&sh.kv_full[v.at], v.phase, p.c.err, DERR_FULL_WAIT))) break;
+          uint8_t* tile = tiles + (2 + v.at) * S::kTile;
+          for (int i = lim * 8 + r; i < kKeys * 8; i += 128)
+#pragma unroll
+            for (int half = 0; half < S::H; ++half)
+              *reinterpret_cast<uint4*>(tile + (i >> 6) * S::kRows8 + half * 1024 + (i & 63) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+        }
         if (busy) {
           // In pieces of 32 keys, by loops that stay loops: a CTA has few steps, and its
           // instructions come from L2, or from DRAM behind everybody's tiles.  (All 128 keys in
@@ -932,29 +952,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               ph[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
             }
             tmem_st16(s_at + 16 * q, ph);
+            if (q == kKeys / 64 - 1) {  // the product with the first half while the second is made
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(&sh.p_ready[t][0]);
+            }
           }
           const float2 st = unpack2(sum);
           l += st.x + st.y;
           tmem_wait_st();
         }
-        if (lim < kKeys) {
-          // slots behind the last token hold anything: their V becomes zero
-          const Place v = wide ? wide_place(u, j, 1) : narrow_place(u, t, k, 1);
-          if (!(ok = warp_wait(&sh.kv_full[v.at], v.phase, p.c.err, DERR_FULL_WAIT))) break;
-          uint8_t* tile = tiles + (2 + v.at) * S::kTile;
-          for (int i = lim * 8 + r; i < kKeys * 8; i += 128)
-#pragma unroll
-            for (int half = 0; half < S::H; ++half)
-              *reinterpret_cast<uint4*>(tile + (i >> 6) * S::kRows8 + half * 1024 + (i & 63) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async();
-        }
+        if (!busy) mbar_arrive(&sh.p_ready[t][0]);
         tc_fence_before();
-        mbar_arrive(&sh.p_ready[t]);
+        mbar_arrive(&sh.p_ready[t][1]);
       }
       if (ok && n > 0) ok = warp_wait(&sh.o_done[t], ends & 1, p.c.err, DERR_FULL_WAIT);
       ends += n > 0;
       tc_fence_after();
-      if (frees) mbar_arrive(&sh.kv_empty[wide_place(u, u.tiles - 1, 1).at]);
       // the part: a thread has its row of O, 32 bytes a store
       if (ok && n > 0 && busy) {
         const Scratch to = scratch_of<G>(p, false);
