@@ -27,6 +27,10 @@
 //   warp 5     (one thread) the MMAs, S a tile ahead of O
 //   warps 6-7  the next pair's Q
 // A second kernel joins the parts of pairs that several CTAs had a share of.
+//
+// Measured: 16 sequences of 16384 tokens (64 query heads on 8 of 128) 82 us, 6.3 TB/s; 32 of 257 to
+// 2176 (32 on 8) 22 us, 3.5 TB/s, of which 8 us are a CTA's beginning and the join; one of 2113
+// 8.3 us, one of 33 (4 on 2 of 64, no join) 5.3 us: latency.
 #include <limits.h>
 #include <math.h>
 
