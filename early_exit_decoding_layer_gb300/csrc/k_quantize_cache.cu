@@ -9,14 +9,14 @@
 //
 // Both kernels stream: eight values a thread, so that 16-byte (or two) loads and stores of
 // half a row stand side by side.  Memory is the bound: 35000 tokens of 8 heads of 128 written in
-// 39 us (5.5 TB/s), 37000 read back in 39 us (5.9 TB/s); one token 2.2 us, the launch.
+// 36.5 us (5.9 TB/s), 37000 read back in 38.6 us (5.9 TB/s); one token 2.2 us, the launch.
 #include "ee_cache_ops.cuh"
 #include "ee_tcgen05.cuh"
 
 namespace ee {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMinExponent = -15;
 constexpr float kHalfEnd = 65520.0f;  // from here on fp16 rounds to infinity
 
@@ -65,10 +65,13 @@ struct Eight<float> {
 // A warp has a row: where it goes is found once for all of its heads, of which 256 / HD stand
 // side by side, HD / 8 lanes each, U of these steps in flight.  (With a search, a
 // division and a table entry for every head instructions were the bound: 36000 rows of 8 heads of
-// 128 in fp16 took 49 us, now 39.)
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads) k_quantize_cache(const QuantizeParams p) {
-  constexpr int L = HD / 8, kHeads = 32 / L, U = sizeof(T) == 2 ? 4 : 2;
+// 128 in fp16 took 49 us, then 39.)  U = 4 in fp16 has few warps per SM: it is for calls whose
+// rows are all on their way at once (8 heads of 128, 64 rows: 2.7 us, with U = 2 3.0; 2048: 4.0, 4.2);
+// others are faster with U = 2 and registers for ten CTAs per SM (8192 rows: 11.0 us, with U = 4
+// 11.9; 35000: 36.5, 39).
+template <typename T, int HD, int U>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U == 2 ? 10 : 1) k_quantize_cache(const QuantizeParams p) {
+  constexpr int L = HD / 8, kHeads = 32 / L;
   const int lane = threadIdx.x & 31, col = (lane % L) * 8, hkv = p.c.n_kv_heads;
   const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (row >= p.total) return;
@@ -200,8 +203,12 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_cache(const DequantizeP
 
 template <typename T, int HD>
 cudaError_t quantize_t(const QuantizeParams& p, cudaStream_t st) {
+  constexpr int kAtOnce = 24 * 152;  // rows, 24 warps per SM
   const int n = (p.total + kThreads / 32 - 1) / (kThreads / 32);
-  k_quantize_cache<T, HD><<<n, kThreads, 0, st>>>(p);
+  // nor where the heads of a row fit into a step of two
+  const bool four = sizeof(T) == 2 && p.total <= kAtOnce && p.c.n_kv_heads > 2 * (256 / HD);
+  if (four) k_quantize_cache<T, HD, sizeof(T) == 2 ? 4 : 2><<<n, kThreads, 0, st>>>(p);
+  else k_quantize_cache<T, HD, 2><<<n, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
