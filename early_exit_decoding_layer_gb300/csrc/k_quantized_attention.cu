@@ -30,7 +30,7 @@
 //
 // Measured: 16 sequences of 16384 tokens (64 query heads on 8 of 128) 82 us, 6.3 TB/s; 32 of 257 to
 // 2176 (32 on 8) 22 us, 3.5 TB/s, of which 8 us are a CTA's beginning and the join; one of 2113
-// 8.3 us, one of 33 (4 on 2 of 64, no join) 5.3 us: latency.
+// 8.1 us, one of 33 (4 on 2 of 64, no join) 5.3 us: latency.
 #include <limits.h>
 #include <math.h>
 
@@ -610,24 +610,16 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   k_quantized_attention<HD, G><<<pieces, kThreads, Lay::kSmem, st>>>(p, map, 1.44269504f / sqrtf((float)HD), least, whole);
   e = cudaGetLastError();
   if (e != cudaSuccess || whole) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   int J = 1;
   while (J < G && p.batch * p.n_heads > 2 * sms * J) J *= 2;
-  cfg.gridDim = dim3((unsigned)(p.batch * (p.n_heads / J)));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  auto join = [&](auto kernel) { return launch_join(kernel, p.batch * (p.n_heads / J), kJoinThreads, sms, Lay::kSmem, st, p, pieces, least); };
   if constexpr (G >= 8)
-    if (J == 8) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 8>, p, pieces, least);
+    if (J == 8) return join(k_join<HD, G, 8>);
   if constexpr (G >= 4)
-    if (J == 4) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 4>, p, pieces, least);
+    if (J == 4) return join(k_join<HD, G, 4>);
   if constexpr (G >= 2)
-    if (J == 2) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 2>, p, pieces, least);
-  return cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, pieces, least);
+    if (J == 2) return join(k_join<HD, G, 2>);
+  return join(k_join<HD, G, 1>);
 }
 
 }  // namespace

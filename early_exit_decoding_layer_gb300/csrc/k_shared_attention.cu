@@ -36,8 +36,8 @@
 //
 // Measured: 64 sequences behind 15000 tokens (64 query heads on 8 of 128) 64 us, 510 TFLOP/s and
 // 3.6 TB/s; a wide step takes 3350 cycles, of which the tensor core is busy with 2400 (S's operands
-// come from shared memory, at 90 bytes a cycle).  32 behind 2048 (32 on 8) 20.5 us, 4 behind 512 (32
-// on 8 of 64) 10.9 us: a CTA's beginning (4.5 us), few steps, and the join (3 us).
+// come from shared memory, at 90 bytes a cycle).  32 behind 2048 (32 on 8) 19.7 us, 4 behind 512 (32
+// on 8 of 64) 10.5 us: a CTA's beginning (4.5 us), few steps, and the join (2 to 3 us).
 #include <limits.h>
 #include <math.h>
 
@@ -1154,24 +1154,16 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   k_shared_attention<HD, G><<<ctas, kThreads, S::kSmem, st>>>(p, maps, make_exponent(HD).c);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   int J = 1;
   while (J < G && p.batch * p.n_heads > 2 * sms * J) J *= 2;
-  cfg.gridDim = dim3((unsigned)(p.batch * (p.n_heads / J)));
-  cfg.blockDim = dim3(kJoinThreads);
+  auto join = [&](auto kernel) { return launch_join(kernel, p.batch * (p.n_heads / J), kJoinThreads, sms, S::kSmem, st, p, ctas); };
   if constexpr (G >= 8)
-    if (J == 8) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 8>, p, ctas);
+    if (J == 8) return join(k_join<HD, G, 8>);
   if constexpr (G >= 4)
-    if (J == 4) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 4>, p, ctas);
+    if (J == 4) return join(k_join<HD, G, 4>);
   if constexpr (G >= 2)
-    if (J == 2) return cudaLaunchKernelEx(&cfg, k_join<HD, G, 2>, p, ctas);
-  return cudaLaunchKernelEx(&cfg, k_join<HD, G, 1>, p, ctas);
+    if (J == 2) return join(k_join<HD, G, 2>);
+  return join(k_join<HD, G, 1>);
 }
 
 }  // namespace
