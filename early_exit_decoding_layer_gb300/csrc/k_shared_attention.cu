@@ -103,7 +103,7 @@ struct Own {
 struct Scratch {
   float *o, *ml;
 };
-__host__ __device__ inline int prefix_rows(int batch, int G) { return batch * G > 128 ? 256 : 2 * batch * G; }
+__host__ __device__ inline int prefix_rows(int batch, int G) { return batch * G < 256 ? batch * G : 256; }
 __host__ __device__ inline int64_t prefix_slots(int batch, int G, int hkv, int prefix) {
   return prefix > 0 ? (int64_t)(batch * G + 255) / 256 * hkv + kMaxPieces : 0;
 }
@@ -261,6 +261,7 @@ struct Shared {
   static constexpr int NST = Shape<HD>::NST;
   uint64_t q_full[2], q_free[2], kv_full[NST], kv_empty[NST], s_full[2], p_ready[2][2], o_done[2];  // P in halves
   uint64_t drained[2];  // every MMA issued is over
+  uint64_t both;        // narrow units: both streams' m, l and O are there; have been read
   Ring<Work> units;
   Stream<HD, G> own[2];
   int role;  // kPrefix: this CTA has a piece of it; kDeep
@@ -577,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.o_done[lane], 1);
         mbar_init(&sh.drained[lane], 1);
       }
+      if (lane == 0) mbar_init(&sh.both, 256);
     }
     fence_mbar_init();
     __syncwarp();
@@ -974,23 +976,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && n > 0) ok = warp_wait(&sh.o_done[t], ends & 1, p.c.err, DERR_FULL_WAIT);
       ends += n > 0;
       tc_fence_after();
-      // the part: a thread has its row of O, 32 bytes a store
+      // the part: a thread has its row of O, 32 bytes a store.  Of a narrow unit with two streams each
+      // warpgroup has half of the columns, of both: O = a_0 O_0 + a_1 O_1.  (A part of each
+      // stream is twice as much to store, 5000 cycles instead of 2500, and to join: 32 sequences
+      // behind 2048 19.7 us instead of 18.1.)
+      const bool two = !wide && u.tiles > 1;
+      float a0 = 1.0f, a1 = 0.0f;
+      if (two) {
+        // m and l, by unit & 1, stream and row, in the ring's place that narrow units (the last ones) leave free
+        static_assert(4 * S::D < S::NST, "a free place");
+        float2* ml = reinterpret_cast<float2*>(tiles + (1 + S::NST) * S::kTile) + (i & 1) * 256;
+        ml[t * 128 + r] = make_float2(m, l);
+        mbar_arrive(&sh.both);
+        if (ok) ok = warp_wait(&sh.both, 0, p.c.err, DERR_FULL_WAIT);
+        tc_fence_after();
+        const float2 x = ml[r], y = ml[128 + r];
+        m = fmaxf(x.x, y.x);
+        a0 = x.x == m ? 1.0f : ex2((x.x - m) * c);
+        a1 = y.x == m ? 1.0f : ex2((y.x - m) * c);
+        l = fmaf(a0, x.y, a1 * y.y);
+      }
       if (ok && n > 0 && busy) {
         const Scratch to = scratch_of<G>(p, false);
-        const int R = prefix_rows(p.batch, G), at = row + (wide ? 0 : t * u.rows);
-        float* o_to = to.o + u.slot * R * HD + at * 8;
+        const int R = prefix_rows(p.batch, G);
+        float* o_to = to.o + u.slot * R * HD + row * 8;
+        const int first = two ? t * (HD / 2) : 0, last = two ? first + HD / 2 : HD;
 #pragma unroll 1
-        for (int i = 0; i < HD; i += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_at + i, o);
+        for (int d = first; d < last; d += 32) {
+          uint32_t o[32], other[32];
+          tmem_ld32((two ? o_col(0) + lane_base : o_at) + d, o);
+          if (two) tmem_ld32(o_col(1) + lane_base + d, other);
           tmem_wait_ld();
           tmem_pin<32>(o);
+          if (two) {
+            tmem_pin<32>(other);
+#pragma unroll
+            for (int w = 0; w < 32; ++w)
+              o[w] = __float_as_uint(fmaf(a0, __uint_as_float(o[w]), a1 * __uint_as_float(other[w])));
+          }
           if (row < u.rows) {
 #pragma unroll
-            for (int w = 0; w < 32; w += 8) st_global_v8(o_to + (i + w) / 8 * R * 8, o + w);
+            for (int w = 0; w < 32; w += 8) st_global_v8(o_to + (d + w) / 8 * R * 8, o + w);
           }
         }
-        if (row < u.rows) *reinterpret_cast<float2*>(to.ml + (u.slot * R + at) * 2) = make_float2(m * c, l);
+        if (row < u.rows && (!two || t == 0)) *reinterpret_cast<float2*>(to.ml + (u.slot * R + row) * 2) = make_float2(m * c, l);
+      }
+      if (two) {  // no product of the next unit's goes over what the other has not read
+        tc_fence_before();
+        mbar_arrive(&sh.both);
+        if (ok) ok = warp_wait(&sh.both, 1, p.c.err, DERR_FULL_WAIT);
       }
       tc_fence_before();
     }
@@ -1017,7 +1051,7 @@ constexpr int kJoinThreads = 256;
 template <int HD, int G, int J>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, const int ctas) {
   constexpr int P = HD / 32, U = 8, kStripes = 8 / J;  // dims per lane; parts in flight
-  __shared__ int64_t ml_at[4 * kMaxPieces], o_at[4 * kMaxPieces];  // where head 0's parts are; -1: none
+  __shared__ int64_t ml_at[3 * kMaxPieces], o_at[3 * kMaxPieces];  // where head 0's parts are; -1: none
   __shared__ float ms[8], ls[8], outs[8][HD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x / (p.n_heads / J), first = (blockIdx.x - s * (p.n_heads / J)) * J;  // its heads
@@ -1029,7 +1063,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   const int all = s * G, rt = all >> 8, row = all & 255, rows = plan.rows_of(rt), R = prefix_rows(p.batch, G);
   const bool wide = rows > 128;
   int n_pre = 0, count = 0;
-  // the prefix's parts: one a piece of a wide unit, of a narrow one two
+  // the prefix's parts: one a piece
   if (pre > 0) {
     const int cost = wide ? kWideCost : kNarrowCost, x = rt * plan.hkv * plan.pre_cost[0] + g * plan.pre_cost[rt];
     const int i0 = x / plan.each_pre, i1 = (pre == 1 ? x : x + kStartCost + (pre - 1) * cost) / plan.each_pre;
@@ -1037,15 +1071,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
       const int k = Plan<G>::item_at((i + 1) * plan.each_pre, x, pre, kStartCost, cost) -
                     Plan<G>::item_at(i * plan.each_pre, x, pre, kStartCost, cost);
       const int64_t slot = rt * plan.hkv + g + i;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const bool has = wide ? t == 0 && k > 0 : k > t;
-        const int at = row + t * rows;
-        ml_at[2 * (i - i0) + t] = has ? slot * R + at : -1;
-        o_at[2 * (i - i0) + t] = slot * R * HD + at * 8;
-      }
+      ml_at[i - i0] = k > 0 ? slot * R + row : -1;
+      o_at[i - i0] = slot * R * HD + row * 8;
     }
-    n_pre = count = 2 * (i1 - i0 + 1);
+    n_pre = count = i1 - i0 + 1;
   }
   // and those of its own blocks
   if (own > 0) {
