@@ -11,7 +11,8 @@
 // piece a share of the units' key tiles.  Two streams, each with a softmax warpgroup; while
 // one is busy with its probabilities the tensor core works for the other:
 //   wide (a unit of 129 to 256 rows)  each stream has 128 rows, both see every key tile
-//   narrow (up to 128 rows)  both have the same rows, and every second key tile
+//   narrow (up to 128 rows)  both have the same rows, and every second key tile;
+//                           their results are added before they go out
 //   warps 4t .. 4t + 3   a thread per row: S_t to registers, running maximum and sum,
 //                        P_t = exp2(c S - c m) as fp16 over S_t's columns, in two halves
 //                        of 64 keys, so that half of P V is done before the other is there
@@ -36,8 +37,8 @@
 //
 // Measured: 64 sequences behind 15000 tokens (64 query heads on 8 of 128) 64 us, 510 TFLOP/s and
 // 3.6 TB/s; a wide step takes 3350 cycles, of which the tensor core is busy with 2400 (S's operands
-// come from shared memory, at 90 bytes a cycle).  32 behind 2048 (32 on 8) 19.7 us, 4 behind 512 (32
-// on 8 of 64) 10.5 us: a CTA's beginning (4.5 us), few steps, and the join (2 to 3 us).
+// come from shared memory, at 90 bytes a cycle).  32 behind 2048 (32 on 8) 17.7 us, 4 behind 512 (32
+// on 8 of 64) 10.6 us: a CTA's beginning (4.5 us), few steps, and the join (2 to 3 us).
 #include <limits.h>
 #include <math.h>
 
@@ -56,7 +57,7 @@ constexpr int kMaxPieces = 160;
 // Times in 200 cycles, by which the CTAs are shared out: a prefix tile, a unit's first loads and
 // its part's way out, a CTA's beginning; an own block of a stream, a pair's beginning in blocks, a
 // stream's, and a block (of hd 128) where all SMs together are as fast as the memory.
-constexpr int kWideCost = 18, kNarrowCost = 12, kStartCost = 25, kOwnStart = 11;
+constexpr int kWideCost = 18, kNarrowCost = 12, kWideStart = 25, kNarrowStart = 18, kOwnStart = 11;
 constexpr float kPrefixBegin = 85.0f, kOwnCost = 2.1f, kOwnBegin = 50.0f, kOwnShare = 0.0126f;
 
 template <int HD>
@@ -111,8 +112,8 @@ __host__ __device__ inline int64_t scratch_rows(int batch, int G, int hkv, int p
   return prefix_slots(batch, G, hkv, prefix) * prefix_rows(batch, G) + ((int64_t)batch * hkv + 2 * kMaxPieces) * G;
 }
 
-// Where the pieces' borders lie.  A prefix unit of n tiles has the places [x, x + kStartCost + n
-// cost): its first tile stands at x, tile k at x + kStartCost + k cost.  A pair's n own blocks
+// Where the pieces' borders lie.  A prefix unit of n tiles has the places [x, x + start + n
+// cost): its first tile stands at x, tile k at x + start + k cost.  A pair's n own blocks
 // likewise, with kOwnStart and cost 1.  Two sequences per lane, the whole warp.
 template <int G>
 struct Plan {
@@ -124,6 +125,8 @@ struct Plan {
   EE_DEV int first_own(int n) const { return pre > 0 && n >= pre * 16 ? pre : 0; }  // block
   EE_DEV int own_blocks(int n) const { return ((n + 15) >> 4) - first_own(n); }
   EE_DEV int rows_of(int rt) const { return min(256, batch * G - rt * 256); }
+  EE_DEV int start_of(int rt) const { return rows_of(rt) > 128 ? kWideStart : kNarrowStart; }
+  EE_DEV int cost_of(int rt) const { return rows_of(rt) > 128 ? kWideCost : kNarrowCost; }
 
   EE_DEV void init(const DecodeParams& p, int ctas) {
     static_assert(kMaxPieces < 256, "a number of CTAs in eight bits");
@@ -157,7 +160,7 @@ struct Plan {
     const int tiles = (pre + 7) >> 3;
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
-      pre_cost[rt] = rows_of(rt) > 0 ? places(tiles, kStartCost, rows_of(rt) > 128 ? kWideCost : kNarrowCost) : 0;
+      pre_cost[rt] = rows_of(rt) > 0 ? places(tiles, start_of(rt), cost_of(rt)) : 0;
     pre_end = hkv * (pre_cost[0] + pre_cost[1]);
     // of 32 numbers of prefix CTAs, one a lane, the one with which the slower kind is done first
     n_pre = 0;
@@ -190,9 +193,9 @@ struct Plan {
     while (*c < stop) {
       const int rt = *c < hkv * pre_cost[0] ? 0 : 1, c0 = rt * hkv * pre_cost[0];
       w.g = (*c - c0) / pre_cost[rt];
-      const int x = c0 + w.g * pre_cost[rt], cost = rows_of(rt) > 128 ? kWideCost : kNarrowCost;
+      const int x = c0 + w.g * pre_cost[rt], start = start_of(rt), cost = cost_of(rt);
       *c = x + pre_cost[rt];
-      const int k0 = item_at(begin, x, tiles, kStartCost, cost), k1 = item_at(stop, x, tiles, kStartCost, cost);
+      const int k0 = item_at(begin, x, tiles, start, cost), k1 = item_at(stop, x, tiles, start, cost);
       if (k1 == k0) continue;
       w.rows = rows_of(rt);
       w.kind = w.rows > 128 ? 2 : 1;
@@ -1060,16 +1063,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   plan.init(p, ctas);
   const int n = plan.of(plan.tokens, s), own_x = plan.of(plan.base, s) * plan.hkv + g * plan.of(plan.size, s);
   const int own = plan.own_blocks(n), pre = plan.first_own(n) > 0 ? (plan.pre + 7) >> 3 : 0;
-  const int all = s * G, rt = all >> 8, row = all & 255, rows = plan.rows_of(rt), R = prefix_rows(p.batch, G);
-  const bool wide = rows > 128;
+  const int all = s * G, rt = all >> 8, row = all & 255, R = prefix_rows(p.batch, G);
   int n_pre = 0, count = 0;
   // the prefix's parts: one a piece
   if (pre > 0) {
-    const int cost = wide ? kWideCost : kNarrowCost, x = rt * plan.hkv * plan.pre_cost[0] + g * plan.pre_cost[rt];
-    const int i0 = x / plan.each_pre, i1 = (pre == 1 ? x : x + kStartCost + (pre - 1) * cost) / plan.each_pre;
+    const int start = plan.start_of(rt), cost = plan.cost_of(rt), x = rt * plan.hkv * plan.pre_cost[0] + g * plan.pre_cost[rt];
+    const int i0 = x / plan.each_pre, i1 = (pre == 1 ? x : x + start + (pre - 1) * cost) / plan.each_pre;
     for (int i = i0 + tid; i <= i1; i += kJoinThreads) {
-      const int k = Plan<G>::item_at((i + 1) * plan.each_pre, x, pre, kStartCost, cost) -
-                    Plan<G>::item_at(i * plan.each_pre, x, pre, kStartCost, cost);
+      const int k = Plan<G>::item_at((i + 1) * plan.each_pre, x, pre, start, cost) -
+                    Plan<G>::item_at(i * plan.each_pre, x, pre, start, cost);
       const int64_t slot = rt * plan.hkv + g + i;
       ml_at[i - i0] = k > 0 ? slot * R + row : -1;
       o_at[i - i0] = slot * R * HD + row * 8;
