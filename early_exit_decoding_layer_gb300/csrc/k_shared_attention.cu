@@ -14,8 +14,8 @@
 //   narrow (up to 128 rows)  both have the same rows, and every second key tile;
 //                           their results are added before they go out
 //   warps 4t .. 4t + 3   a thread per row: S_t to registers, running maximum and sum,
-//                        P_t = exp2(c S - c m) as fp16 over S_t's columns, in two halves
-//                        of 64 keys, so that half of P V is done before the other is there
+//                        P_t = exp2(c S - c m) over S_t's columns, in two halves of 64
+//                        keys, so that half of P V is done before the other is there
 //   warp 9 (one thread)  the products, O_t += P_t V_j and S_t = Q K_j'^T; in narrow units
 //                        stream 0's
 //   warp 10              narrow: stream 1's products.  wide: waits for K and V tiles in warp
@@ -35,10 +35,16 @@
 // parts in the order of the pieces.  Maxima may lag behind by up to 8 (in log2), so
 // that O is rarely rescaled.
 //
-// Measured: 64 sequences behind 15000 tokens (64 query heads on 8 of 128) 64 us, 510 TFLOP/s and
-// 3.6 TB/s; a wide step takes 3350 cycles, of which the tensor core is busy with 2400 (S's operands
-// come from shared memory, at 90 bytes a cycle).  32 behind 2048 (32 on 8) 17.7 us, 4 behind 512 (32
-// on 8 of 64) 10.6 us: a CTA's beginning (4.5 us), few steps, and the join (2 to 3 us).
+// Probabilities go to the product as two fp16 terms, P = P_hi + P_lo: 22 bits, down to 2^-32 of
+// a row's largest (they are lifted by 2^7, and 2^15 at most).  The second term is more MMAs with
+// the same V in prefix units, and free in own blocks, whose products have 16 columns for G <= 8
+// heads.  Rounded to fp16 once, each would be off by up to 2^-12, which in a mean of V is as much as
+// the result's own rounding.
+//
+// Measured: 64 sequences behind 15000 tokens (64 query heads on 8 of 128) 73 us, 450 TFLOP/s and
+// 3.2 TB/s; a wide step takes 4900 cycles, of which the tensor core is busy with 3400 (P_lo's MMAs
+// 1000 of them; without them 3350 and 64 us).  32 behind 2048 (32 on 8) 17.7 us, 4 behind 512 (32
+// on 8 of 64) 11.0 us: a CTA's beginning (4.5 us), few steps, and the join (2 to 3 us).
 #include <limits.h>
 #include <math.h>
 
@@ -57,8 +63,10 @@ constexpr int kMaxPieces = 160;
 // Times in 200 cycles, by which the CTAs are shared out: a prefix tile, a unit's first loads and
 // its part's way out, a CTA's beginning; an own block of a stream, a pair's beginning in blocks, a
 // stream's, and a block (of hd 128) where all SMs together are as fast as the memory.
-constexpr int kWideCost = 18, kNarrowCost = 12, kWideStart = 25, kNarrowStart = 18, kOwnStart = 11;
+constexpr int kWideCost = 24, kNarrowCost = 12, kWideStart = 25, kNarrowStart = 18, kOwnStart = 11;
 constexpr float kPrefixBegin = 85.0f, kOwnCost = 2.1f, kOwnBegin = 50.0f, kOwnShare = 0.0126f;
+// P is 2^kLift at the maximum, 2^(kLift + kLag) at most.
+constexpr float kLift = 7.0f, kLag = 8.0f;
 
 template <int HD>
 struct Shape {
@@ -235,6 +243,15 @@ struct Plan {
     }
   }
 };
+
+// Two probabilities as fp16 terms, the first in the low half.
+EE_DEV void two_halves(float a, float b, uint32_t* hi, uint32_t* lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
+  *hi = *reinterpret_cast<const uint32_t*>(&h);
+  *lo = *reinterpret_cast<const uint32_t*>(&r);
+}
 
 template <int G>
 EE_DEV Scratch scratch_of(const DecodeParams& p, bool own) {
@@ -429,7 +446,7 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
           : "memory");
       if (!go) break;
       const int tiles = (u.blocks + 7) >> 3;
-      float m[G], l[G];
+      float m[G], l[G];  // m: kLift below the maximum
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         m[h] = -INFINITY;
@@ -450,7 +467,7 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           z[h] = live ? __uint_as_float(v[h]) * c : -INFINITY;
-          grow |= z[h] - m[h] > 8.0f;
+          grow |= z[h] - m[h] > kLift + kLag;
           a[h] = 1.0f;
         }
         asm volatile(
@@ -467,22 +484,27 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
           asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float mn = fmaxf(fmaxf(fmaxf(sh.red[0][h], sh.red[1][h]), fmaxf(sh.red[2][h], sh.red[3][h])), m[h]);
+            const float mn = fmaxf(fmaxf(fmaxf(sh.red[0][h], sh.red[1][h]), fmaxf(sh.red[2][h], sh.red[3][h])) - kLift, m[h]);
             a[h] = m[h] == mn ? 1.0f : ex2(m[h] - mn);
             m[h] = mn;
             l[h] *= a[h];
           }
         }
-        uint32_t x4[4] = {};  // the token's row of P
+        uint32_t hi[4] = {}, lo[4] = {};  // the token's row of P: columns h, and 8 + h
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          const float e = ex2(z[h] - (m[h] == -INFINITY ? 0.0f : m[h]));
-          l[h] += e;
-          x4[h >> 1] |= (uint32_t)float_to_half_bits(e) << (16 * (h & 1));
+        for (int h = 0; h < G; h += 2) {
+          float e[2] = {0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < (G == 1 ? 1 : 2); ++i) {
+            e[i] = ex2(z[h + i] - (m[h + i] == -INFINITY ? 0.0f : m[h + i]));
+            l[h + i] += e[i];
+          }
+          two_halves(e[0], e[1], &hi[h >> 1], &lo[h >> 1]);
         }
         // the product before has read P and is in O
         if (k > 0 && ok) ok = warp_wait(&sh.o_done, (k - 1) & 1, p.c.err, DERR_FULL_WAIT);
-        *reinterpret_cast<uint4*>(ps + (tid >> 3) * 256 + row_chunk<32>(tid & 7, 0)) = make_uint4(x4[0], x4[1], x4[2], x4[3]);
+        *reinterpret_cast<uint4*>(ps + (tid >> 3) * 256 + row_chunk<32>(tid & 7, 0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(ps + (tid >> 3) * 256 + row_chunk<32>(tid & 7, 1)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (left < kKeys) {
           // slots behind the last token hold anything: their V becomes zero
           const int item = 2 * k + 1;
@@ -500,7 +522,10 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
           tmem_wait_ld();
           tmem_pin<16>(o);
 #pragma unroll
-          for (int h = 0; h < G; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * a[h]);
+          for (int h = 0; h < G; ++h) {
+            o[h] = __float_as_uint(__uint_as_float(o[h]) * a[h]);
+            o[8 + h] = __float_as_uint(__uint_as_float(o[8 + h]) * a[h]);
+          }
           tmem_st16(o_col(r) + lane_base, o);
           tmem_wait_st();
         }
@@ -524,7 +549,7 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
       const Scratch to = scratch_of<G>(p, true);
 #pragma unroll
       for (int h = 0; h < G; ++h)
-        if (has_dim) to.o[(u.slot * G + h) * HD + dim] = __uint_as_float(o[h]);
+        if (has_dim) to.o[(u.slot * G + h) * HD + dim] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]);
 #pragma unroll
       for (int h = 0; h < G; ++h)
         if (tid == h)
@@ -609,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = loads ? 0 : sh.tmem;
   const uint32_t q_s = smem_addr(tiles), kv_s = q_s + 2 * S::kTile;
-  // tensor memory: S_t (128 columns, P_t over its first 64), then O_t
+  // tensor memory: S_t (128 columns; P_t over them, of 32 keys each the 16 of P_hi, then P_lo's), then O_t
   auto s_col = [&](int t) { return tmem + t * 128; };
   auto o_col = [&](int t) { return tmem + 256 + t * HD; };
   // Steps of stream t in a unit, and the key tile of step k.
@@ -654,7 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t b = v_desc + at * (S::kTile >> 4);
 #pragma unroll
     for (int kk = h * kKeys / 32; kk < (h + 1) * kKeys / 32; ++kk)
-      mma_f16_ta(o_col(t), s_col(t) + kk * 8, b + (kk * 2 * S::kRows8 >> 4), id_pv, acc || kk > h * kKeys / 32);
+#pragma unroll
+      for (int low = 0; low < 2; ++low)
+        mma_f16_ta(o_col(t), s_col(t) + (kk >> 1) * 32 + low * 16 + (kk & 1) * 8, b + (kk * 2 * S::kRows8 >> 4), id_pv,
+                   acc || kk > h * kKeys / 32 || low > 0);
   };
 
   if (!(role & kPrefix)) {
@@ -877,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = steps_of(u, t);
       const int row = r + (wide ? t * 128 : 0);  // of the unit
       const bool busy = row - lane < u.rows;     // a row of this warp is the unit's
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f;  // m: c times the maximum, less kLift
       for (int k = 0; k < n && ok; ++k) {
         const int j = tile_of(u, t, k);
         if (!(ok = warp_wait(&sh.s_full[t], steps & 1, p.c.err, DERR_FULL_WAIT))) break;
@@ -925,13 +953,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mt = fmaxf(mx[0], mx[1]);
           }
           if (k == 0) {
-            m = mt;
-          } else if (__any_sync(0xffffffffu, row < u.rows && (mt - m) * c > 8.0f)) {
+            m = fmaf(mt, c, -kLift);
+          } else if (__any_sync(0xffffffffu, row < u.rows && fmaf(mt, c, -m) > kLift + kLag)) {
             // some row's maximum has grown too far (rows that are not the unit's have no say: what
             // they hold depends on what was there before): this warp's rows of O and l go over to
             // the new maxima (O has every product before: S_t came after)
-            const float mn = fmaxf(m, mt);
-            const float a = m == mn ? 1.0f : ex2((m - mn) * c);
+            const float mn = fmaxf(m, fmaf(mt, c, -kLift));
+            const float a = m == mn ? 1.0f : ex2(m - mn);
             m = mn;
             l *= a;
 #pragma unroll 1
@@ -946,22 +974,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // a row that has seen nothing yet has m = -inf: its P is 0
-          const float mc = m == -INFINITY ? 0.0f : m * c;
-          const uint64_t c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
+          const float ms = m == -INFINITY ? 0.0f : m;
+          const uint64_t c2 = pack2(c, c), nm2 = pack2(-ms, -ms);
           uint64_t sum = 0;
 #pragma unroll 1
           for (int q = 0; q < kKeys / 32; ++q) {
             load(q);
-            uint32_t ph[16];
+            uint32_t hi[16], lo[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 x = unpack2(fma2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2));
               const float e0 = ex2(x.x), e1 = ex2(x.y);
               sum = add2(sum, pack2(e0, e1));
-              const __half2 h = __floats2half2_rn(e0, e1);
-              ph[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+              two_halves(e0, e1, &hi[i >> 1], &lo[i >> 1]);
             }
-            tmem_st16(s_at + 16 * q, ph);
+            tmem_st16(s_at + 32 * q, hi);
+            tmem_st16(s_at + 32 * q + 16, lo);
             if (q == kKeys / 64 - 1) {  // the product with the first half while the second is made
               tmem_wait_st();
               tc_fence_before();
@@ -995,8 +1023,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float2 x = ml[r], y = ml[128 + r];
         m = fmaxf(x.x, y.x);
-        a0 = x.x == m ? 1.0f : ex2((x.x - m) * c);
-        a1 = y.x == m ? 1.0f : ex2((y.x - m) * c);
+        a0 = x.x == m ? 1.0f : ex2(x.x - m);
+        a1 = y.x == m ? 1.0f : ex2(y.x - m);
         l = fmaf(a0, x.y, a1 * y.y);
       }
       if (ok && n > 0 && busy) {
@@ -1022,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < 32; w += 8) st_global_v8(o_to + (d + w) / 8 * R * 8, o + w);
           }
         }
-        if (row < u.rows && (!two || t == 0)) *reinterpret_cast<float2*>(to.ml + (u.slot * R + row) * 2) = make_float2(m * c, l);
+        if (row < u.rows && (!two || t == 0)) *reinterpret_cast<float2*>(to.ml + (u.slot * R + row) * 2) = make_float2(m, l);
       }
       if (two) {  // no product of the next unit's goes over what the other has not read
         tc_fence_before();
@@ -1039,8 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// o is a mean of fp16 values and no larger than they are.  P's rounding may take it past the
-// largest one by up to 2^-11 of it, which would be infinite in fp16.
+// o is a mean of fp16 values and no larger than they are.  The sums' rounding may take it past the
+// largest one, which would be infinite in fp16 if it were by 2^-12 of it.
 EE_DEV float within_half(float y) {
   return fabsf(y) > 65504.0f && fabsf(y) < INFINITY ? copysignf(65504.0f, y) : y;
 }

@@ -591,8 +591,8 @@ ee_status ee_op_quantized_attention(int32_t B, int32_t n_heads, int32_t n_kv_hea
 
 /* ---- a batch that shares a prefix -------------------------------------------------
  * Decode attention over the fp16 cache of sequences whose first `prefix` tokens are the
- * same and sit in the same blocks: these are read once for the whole batch.  The
- * results are those of one query position per sequence as in ee_op_attention,
+ * same and sit in the same blocks: these are read once for the whole batch.  What
+ * ee_op_attention computes for one query position per sequence, with q and o in fp16:
  *   o[s, h] = sum_{t <= pos[s]} softmax_t(q_h . k_t / sqrt(hd)) v_t,
  * with the first prefix / 16 blocks (whole blocks; 0 <= prefix <= 16384, and 0 shares
  * nothing) taken from block_table's first row for every sequence, whatever
@@ -601,8 +601,8 @@ ee_status ee_op_quantized_attention(int32_t B, int32_t n_heads, int32_t n_kv_hea
  *   q, o, scratch as for ee_op_quantized_attention, with
  *   ee_shared_attention_scratch_bytes(...) bytes; the caches and the rules of values that are
  *   not finite as for ee_op_prompt_attention.
- * Products are exact in fp32 accumulators and statistics fp32; the probabilities are rounded
- * to fp16 for the product with V. */
+ * Products are exact in fp32 accumulators and statistics fp32; probabilities have 22 bits,
+ * down to 2^-32 of a row's largest, for the product with V. */
 size_t ee_shared_attention_scratch_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                          int32_t max_ctx, int32_t prefix);
 ee_status ee_op_shared_attention(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_ctx,
