@@ -52,19 +52,13 @@
 #include <atomic>
 
 #include "ee_decode_plan.cuh"
+#include "ee_shared_plan.cuh"
 #include "ee_tcgen05.cuh"
 
 namespace ee {
 namespace {
 
-constexpr int kKeys = 128;     // of a tile, eight blocks
 constexpr int kThreads = 384;  // two softmax warpgroups, TMA, two for MMA, units
-constexpr int kMaxPieces = 160;
-// Times in 200 cycles, by which the CTAs are shared out: a prefix tile, a unit's first loads and
-// its part's way out, a CTA's beginning; an own block of a stream, a pair's beginning in blocks, a
-// stream's, and a block (of hd 128) where all SMs together are as fast as the memory.
-constexpr int kWideCost = 24, kNarrowCost = 12, kWideStart = 25, kNarrowStart = 18, kOwnStart = 11;
-constexpr float kPrefixBegin = 85.0f, kOwnCost = 2.1f, kOwnBegin = 50.0f, kOwnShare = 0.0126f;
 // P is 2^kLift at the maximum, 2^(kLift + kLag) at most.
 constexpr float kLift = 7.0f, kLag = 8.0f;
 
@@ -89,70 +83,33 @@ struct Maps {
   CUtensorMap q, q1, k, v;  // q1: the rows of one sequence
 };
 
-// A prefix unit's share of a CTA: `tiles` key tiles, `have` tokens in them, from block `first`
-// on.
-struct Work {
-  int kind;  // 0: no more, 1: narrow, 2: wide
-  int s, g, first, tiles, have, rows;
-  int64_t slot;  // of its part
-  uint32_t par;  // bit i: of place i's tiles before this unit, odd or even
-  int start;     // of a wide unit in the ring
-};
-
-// A stream's share of a (sequence, kv head): `blocks` from block `first` of table row `row` on,
-// `have` tokens in them.
-struct Own {
-  int s, g, row, first, blocks, have;  // s = -1: no more
-  int64_t slot;
-};
-
 // The parts in the scratch, rows of O and of (m, l).  First the prefix's, a slot of
 // prefix_rows() rows each, with O as [hd / 8][rows][8]: rows next to each other, a thread's 32
 // bytes each, are stored in one go.  Then the own blocks', G rows a slot.
 struct Scratch {
   float *o, *ml;
 };
-__host__ __device__ inline int prefix_rows(int batch, int G) { return batch * G < 256 ? batch * G : 256; }
-__host__ __device__ inline int64_t prefix_slots(int batch, int G, int hkv, int prefix) {
-  return prefix > 0 ? (int64_t)(batch * G + 255) / 256 * hkv + kMaxPieces : 0;
-}
-__host__ __device__ inline int64_t scratch_rows(int batch, int G, int hkv, int prefix) {
-  return prefix_slots(batch, G, hkv, prefix) * prefix_rows(batch, G) + ((int64_t)batch * hkv + 2 * kMaxPieces) * G;
-}
 
-// Where the pieces' borders lie.  A prefix unit of n tiles has the places [x, x + start + n
-// cost): its first tile stands at x, tile k at x + start + k cost.  A pair's n own blocks
-// likewise, with kOwnStart and cost 1.  Two sequences per lane, the whole warp.
+// The pieces (ee_shared_plan.cuh), from lengths on the device: two sequences per lane, the whole
+// warp.
 template <int G>
-struct Plan {
+struct Plan : Pieces<G> {
+  using P = Pieces<G>;
   int tokens[2], base[2], size[2];  // of sequences lane and lane + 32: their own blocks' places, and those before them
-  int hkv, batch, prefix, pre, pre_cost[2], pre_end, own_end;
-  int n_pre, each_pre, each_own;  // CTAs for the prefix; places of a CTA's piece, and of a stream's
-
-  EE_DEV static int places(int n, int start, int cost) { return n > 0 ? start + n * cost : 0; }
-  EE_DEV int first_own(int n) const { return pre > 0 && n >= pre * 16 ? pre : 0; }  // block
-  EE_DEV int own_blocks(int n) const { return ((n + 15) >> 4) - first_own(n); }
-  EE_DEV int rows_of(int rt) const { return min(256, batch * G - rt * 256); }
-  EE_DEV int start_of(int rt) const { return rows_of(rt) > 128 ? kWideStart : kNarrowStart; }
-  EE_DEV int cost_of(int rt) const { return rows_of(rt) > 128 ? kWideCost : kNarrowCost; }
 
   EE_DEV void init(const DecodeParams& p, int ctas) {
-    static_assert(kMaxPieces < 256, "a number of CTAs in eight bits");
     static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
     static_assert((kOwnStart + kCacheMaxCtx / 16) * 32 < 1 << 16, "two sums in a word");
     const int lane = threadIdx.x & 31;
-    hkv = p.c.n_kv_heads;
-    batch = p.batch;
-    prefix = p.prefix;
     int at[2];  // both loads before either is waited for
 #pragma unroll
     for (int u = 0; u < 2; ++u) at[u] = lane + 32 * u < p.batch ? p.pos[lane + 32 * u] : -1;
 #pragma unroll
     for (int u = 0; u < 2; ++u) tokens[u] = checked_length(at[u] == INT32_MAX ? at[u] : at[u] + 1, p.c.max_ctx, p.c.err);
-    // the prefix is read if a sequence sees it whole; who does not has all its blocks to itself
-    pre = __any_sync(0xffffffffu, max(tokens[0], tokens[1]) >= p.prefix) ? p.prefix >> 4 : 0;
+    // the prefix is read if a sequence sees it whole
+    P::init(p.c.n_kv_heads, p.batch, p.prefix, __any_sync(0xffffffffu, max(tokens[0], tokens[1]) >= p.prefix));
 #pragma unroll
-    for (int u = 0; u < 2; ++u) size[u] = places(own_blocks(tokens[u]), kOwnStart, 1);
+    for (int u = 0; u < 2; ++u) size[u] = P::own_places(tokens[u]);
     const uint32_t mine = (uint32_t)size[0] | (uint32_t)size[1] << 16;
     uint32_t sum = mine;
 #pragma unroll
@@ -164,82 +121,29 @@ struct Plan {
     sum -= mine;
     base[0] = (int)(sum & 0xffffu);
     base[1] = (int)(all & 0xffffu) + (int)(sum >> 16);
-    own_end = hkv * ((int)(all & 0xffffu) + (int)(all >> 16));
-    const int tiles = (pre + 7) >> 3;
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-      pre_cost[rt] = rows_of(rt) > 0 ? places(tiles, start_of(rt), cost_of(rt)) : 0;
-    pre_end = hkv * (pre_cost[0] + pre_cost[1]);
-    // of 32 numbers of prefix CTAs, one a lane, the one with which the slower kind is done first
-    n_pre = 0;
-    if (pre_end > 0 && own_end > 0) {
-      const int n = 1 + lane * max(0, ctas - 2) / 31;
-      const int pairs = hkv * (__popc(__ballot_sync(0xffffffffu, size[0] > 0)) + __popc(__ballot_sync(0xffffffffu, size[1] > 0)));
-      const float a = kPrefixBegin + fmaxf(kNarrowCost, __fdividef(pre_end, n));
-      const float b = kOwnBegin + fmaxf(kOwnCost * fmaxf(kOwnStart + 1, __fdividef(own_end, 2 * max(1, ctas - n))),
-                                        kOwnShare / 128 * p.c.head_dim * (own_end - kOwnStart * pairs));
-      n_pre = (int)(__reduce_min_sync(0xffffffffu, (unsigned)fminf(fmaxf(a, b) * 8.0f, 16777215.0f) << 8 | (unsigned)n) & 255u);
-    } else if (pre_end > 0) {
-      n_pre = ctas;
+    P::own_end = P::hkv * ((int)(all & 0xffffu) + (int)(all >> 16));
+    int n = 0;
+    if (P::pre_end > 0 && P::own_end > 0) {
+      const int pairs = P::hkv * (__popc(__ballot_sync(0xffffffffu, size[0] > 0)) + __popc(__ballot_sync(0xffffffffu, size[1] > 0)));
+      n = (int)(__reduce_min_sync(0xffffffffu, P::estimate(lane, ctas, pairs, p.c.head_dim)) & 255u);
     }
-    const int n = max(1, n_pre), streams = 2 * max(1, ctas - n_pre);
-    each_pre = max(kNarrowCost, (pre_end + n - 1) / n);
-    each_own = max(kOwnStart + 1, (own_end + streams - 1) / streams);
-  }
-  // The first tile (or block) of a unit at x that stands at place c or behind it.
-  EE_DEV static int item_at(int c, int x, int n, int start, int cost) {
-    return c <= x ? 0 : min(n, max(1, (c - x - start + cost - 1) / cost));
+    P::share_out(ctas, n);
   }
   EE_DEV int of(const int (&a)[2], int s) const { return s < 32 ? __shfl_sync(0xffffffffu, a[0], s) : __shfl_sync(0xffffffffu, a[1], s - 32); }
 
-  // The share of CTA `me` of the prefix unit that holds place *c, or of the next one that has any;
-  // *c: behind the unit.
-  EE_DEV Work prefix_at(int* c, int me) const {
-    Work w;
-    const int begin = me * each_pre, stop = min(pre_end, begin + each_pre), tiles = (pre + 7) >> 3;
-    w.kind = w.tiles = 0;
-    while (*c < stop) {
-      const int rt = *c < hkv * pre_cost[0] ? 0 : 1, c0 = rt * hkv * pre_cost[0];
-      w.g = (*c - c0) / pre_cost[rt];
-      const int x = c0 + w.g * pre_cost[rt], start = start_of(rt), cost = cost_of(rt);
-      *c = x + pre_cost[rt];
-      const int k0 = item_at(begin, x, tiles, start, cost), k1 = item_at(stop, x, tiles, start, cost);
-      if (k1 == k0) continue;
-      w.rows = rows_of(rt);
-      w.kind = w.rows > 128 ? 2 : 1;
-      w.s = rt * 256 / G;
-      w.slot = rt * hkv + w.g + me;
-      w.first = k0 * 8;
-      w.have = min(pre * 16, k1 * kKeys) - k0 * kKeys;
-      w.tiles = k1 - k0;
-      break;
-    }
-    return w;
-  }
   // The share of stream `me` of the pair that holds place *c, or of the next one that has any;
   // *c: behind the pair.
   EE_DEV Own own_at(int* c, int me) const {
     Own w;
-    const int begin = me * each_own, stop = min(own_end, begin + each_own);
+    const int hkv = P::hkv, stop = min(P::own_end, (me + 1) * P::each_own);
     for (;;) {
       w.s = -1;
       w.blocks = 0;
       if (*c >= stop) return w;
       const unsigned lo = __ballot_sync(0xffffffffu, *c >= base[0] * hkv && *c < (base[0] + size[0]) * hkv);
       const unsigned hi = __ballot_sync(0xffffffffu, *c >= base[1] * hkv && *c < (base[1] + size[1]) * hkv);
-      w.s = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
-      const int b0 = of(base, w.s) * hkv, len = of(size, w.s), n = of(tokens, w.s), from = first_own(n), nb = own_blocks(n);
-      w.g = (*c - b0) / len;
-      const int x = b0 + w.g * len;
-      *c = x + len;
-      const int k0 = item_at(begin, x, nb, kOwnStart, 1), k1 = item_at(stop, x, nb, kOwnStart, 1);
-      if (k1 == k0) continue;
-      w.row = prefix > 0 && from == 0 ? 0 : w.s;  // who ends within the prefix has its blocks
-      w.first = from + k0;
-      w.blocks = k1 - k0;
-      w.have = min(n - w.first * 16, w.blocks * 16);
-      w.slot = (int64_t)w.s * hkv + w.g + me;
-      return w;
+      const int s = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+      if (P::own_at(c, me, s, of(base, s) * hkv, of(tokens, s), &w)) return w;
     }
   }
 };
@@ -1089,34 +993,29 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   const int g = first / G, h = first % G + warp % J;
   Plan<G> plan;
   plan.init(p, ctas);
-  const int n = plan.of(plan.tokens, s), own_x = plan.of(plan.base, s) * plan.hkv + g * plan.of(plan.size, s);
-  const int own = plan.own_blocks(n), pre = plan.first_own(n) > 0 ? (plan.pre + 7) >> 3 : 0;
+  const int n = plan.of(plan.tokens, s);
+  const int own = plan.own_blocks(n);
   const int all = s * G, rt = all >> 8, row = all & 255, R = prefix_rows(p.batch, G);
   int n_pre = 0, count = 0;
   // the prefix's parts: one a piece
-  if (pre > 0) {
-    const int start = plan.start_of(rt), cost = plan.cost_of(rt), x = rt * plan.hkv * plan.pre_cost[0] + g * plan.pre_cost[rt];
-    const int i0 = x / plan.each_pre, i1 = (pre == 1 ? x : x + start + (pre - 1) * cost) / plan.each_pre;
-    for (int i = i0 + tid; i <= i1; i += kJoinThreads) {
-      const int k = Plan<G>::item_at((i + 1) * plan.each_pre, x, pre, start, cost) -
-                    Plan<G>::item_at(i * plan.each_pre, x, pre, start, cost);
-      const int64_t slot = rt * plan.hkv + g + i;
-      ml_at[i - i0] = k > 0 ? slot * R + row : -1;
-      o_at[i - i0] = slot * R * HD + row * 8;
+  if (plan.first_own(n) > 0) {
+    const auto pieces = plan.prefix_range(rt, g);
+    for (int i = pieces.first + tid; i <= pieces.last; i += kJoinThreads) {
+      const int64_t slot = plan.pre_slot(rt, g, i);
+      ml_at[i - pieces.first] = pieces.has(i) ? slot * R + row : -1;
+      o_at[i - pieces.first] = slot * R * HD + row * 8;
     }
-    n_pre = count = i1 - i0 + 1;
+    n_pre = count = pieces.last - pieces.first + 1;
   }
   // and those of its own blocks
   if (own > 0) {
-    const int i0 = own_x / plan.each_own, i1 = (own == 1 ? own_x : own_x + kOwnStart + own - 1) / plan.each_own;
-    for (int i = i0 + tid; i <= i1; i += kJoinThreads) {
-      const bool has = Plan<G>::item_at((i + 1) * plan.each_own, own_x, own, kOwnStart, 1) >
-                       Plan<G>::item_at(i * plan.each_own, own_x, own, kOwnStart, 1);
-      const int64_t at = ((int64_t)s * plan.hkv + g + i) * G;
-      ml_at[n_pre + i - i0] = has ? at : -1;
-      o_at[n_pre + i - i0] = at * HD;
+    const auto pieces = plan.own_range(plan.of(plan.base, s) * plan.hkv, g, n);
+    for (int i = pieces.first + tid; i <= pieces.last; i += kJoinThreads) {
+      const int64_t at = plan.own_slot(s, g, i) * G;
+      ml_at[n_pre + i - pieces.first] = pieces.has(i) ? at : -1;
+      o_at[n_pre + i - pieces.first] = at * HD;
     }
-    count += i1 - i0 + 1;
+    count += pieces.last - pieces.first + 1;
   }
   // this lane's dims, lane * P and on: eight floats of a prefix row lie together
   const Scratch sp = scratch_of<G>(p, false), so = scratch_of<G>(p, true);
