@@ -1,11 +1,11 @@
-"""What decode attention behind a shared prefix keeps of its probabilities: results within
-their own rounding of 64 bits."""
+"""Decode attention behind a shared prefix: what it keeps of its probabilities, results within
+their own rounding of 64 bits; and scores that are infinite."""
 import math
 
 import numpy as np
 import pytest
 
-from tests.cache_cases import U16, U32
+from tests.cache_cases import U16, U32, prompt_reference
 from tests.test_gpu_shared_attention import Shared, UNUSED
 
 torch = pytest.importorskip("torch")
@@ -86,3 +86,66 @@ def test_probabilities_keep_their_bits(hq, hkv, hd, prefix, ctxs, faint):
     for s in range(len(ctxs)):
         want, bound = exact_rows(h, s, q[s])
         assert np.all(np.abs(o[s] - want) <= bound), (s, np.max(np.abs(o[s] - want) / bound))
+
+
+# (kv heads, hd, prefix, ctxs): own blocks alone; rows of one tile with one stream and with two;
+# 129 to 256 rows, and 512; long own blocks.  Query heads: four to a kv head
+INFINITE = [
+    (2, 64, 0, [300, 40, 700]), (2, 128, 112, [112, 130, 250, 400]), (2, 64, 640, [640, 900, 655, 1300]),
+    (1, 64, 300, [304 + 9 * i for i in range(40)]), (1, 128, 400, [401 + i for i in range(64)]), (2, 128, 64, [3000, 65, 90]),
+]
+
+
+class Without:
+    """A history that lacks some tokens of a kv head."""
+
+    def __init__(self, h, s, g, keep):
+        self.K, self.V, self.hkv = {s: h.K[s][keep][:, g:g + 1]}, {s: h.V[s][keep][:, g:g + 1]}, 1
+
+
+def check_infinite(h, q, hit, sign, o):
+    """Tokens `hit(s)` have an infinite component 0 in kv head 0's keys, q's is `sign` times a finite one
+    or 0: heads with a score of -inf go without them, those with +inf or NaN are NaN."""
+    for s, c in enumerate(h.ctxs):
+        at = np.zeros(c, dtype=bool)
+        at[[t for t in hit(s) if t < c]] = True
+        for g in range(h.hkv):
+            for a in range(g * 4, g * 4 + 4):
+                gone = at if g == 0 else np.zeros_like(at)
+                if gone.any() and not sign[a] < 0:
+                    assert np.isnan(o[s, a]).all(), (s, a)
+                    continue
+                if not (~gone).any():
+                    assert np.all(o[s, a] == 0), (s, a)
+                    continue
+                want, _, _, bound, _, _ = prompt_reference(Without(h, s, g, ~gone), s, q[s, a:a + 1][None])
+                assert np.all(np.abs(o[s, a] - want[0, 0]) <= bound[0, 0]), (s, a)
+
+
+@pytest.mark.parametrize("where", ["first", "few", "last of the prefix", "tile", "prefix", "own", "but the last", "all"])
+@pytest.mark.parametrize("hkv,hd,prefix,ctxs", INFINITE)
+def test_infinite_keys(hkv, hd, prefix, ctxs, where):
+    """A score of -infinity weighs nothing, wherever and however many there are (a whole tile, a
+    whole part, all of them: then o = 0); one of +infinity makes its row NaN and no other."""
+    h = Shared(hd + prefix + len(ctxs), ctxs, prefix, hkv, hd)
+    once, most = prefix // 16 * 16, max(ctxs)
+    tokens = {
+        "first": lambda s: [0], "few": lambda s: [1, once + 1, once + 20, 290, once // 2], "last of the prefix": lambda s: [max(once - 1, 0)],
+        "tile": lambda s: range(128, 256), "prefix": lambda s: range(once), "own": lambda s: range(once, most),
+        "but the last": lambda s: range(ctxs[s] - 1) if s == 0 else range(once), "all": lambda s: range(most),
+    }[where]
+    if where == "but the last" and once and once >= ctxs[0]:
+        tokens = lambda s: range(once - 1)  # noqa: E731
+    q = h.rng.standard_normal((len(ctxs), 4 * hkv, hd)).astype(np.float16)
+    sign = np.tile([-1.0, -1.0, 1.0, -1.0], hkv)
+    if where == "few":
+        sign[0] = 0.0
+    q[:, :, 0] = np.abs(q[:, :, 0] + np.float16(0.1)) * sign
+    q[:, :, 0] = np.where((q[:, :, 0] == 0) & (sign != 0), sign.astype(np.float16), q[:, :, 0])
+    k = h.k.copy()
+    for s, c in enumerate(ctxs):
+        for t in tokens(s):
+            if t < c:
+                k[h.table[0 if t < once else s, t // 16], 0, t % 16, 0] = np.inf
+    o = h.call(q, 4 * hkv, k=k).cpu().numpy().astype(np.float64).reshape(q.shape)
+    check_infinite(h, q, lambda s: [t for t in tokens(s) if t < ctxs[s]], sign, o)
