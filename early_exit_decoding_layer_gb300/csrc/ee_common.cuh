@@ -73,16 +73,13 @@ EE_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
 // Waits for the phase with the given parity to complete.  Gives up after
 // kWaitTimeoutNs, records `code` in *err (first writer wins) and returns false.
 EE_DEV bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, int32_t* err, int32_t code) {
-  uint64_t since = 0;  // the clock is slow to read: not before a wait is long
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      const uint64_t now = globaltimer();
-      if (since == 0) since = now;
-      if (now - since > kWaitTimeoutNs) {
-        if (err) atomicCAS(err, 0, code);
-        return false;
-      }
+    if ((i & 255u) == 0 && globaltimer() - t0 > kWaitTimeoutNs) {
+      if (err) atomicCAS(err, 0, code);
+      return false;
     }
   }
 }
