@@ -7,13 +7,14 @@
 // operand:
 //   S = K_tile Q^T      128 tokens x N columns
 //   O^T += V_tile^T X   head dims x N columns, K = 128 tokens
-// Then Q and X have to be e4m3 too.  They go in as three parts of four bits,
-//   x = a + 2^-5 b + 2^-10 c,
-// each a column of its own (N = 3 G, to 16 or 32), so that fp16 queries are exact and
-// X has 12 bits; a part's remainder is at most 2^-4 of it, and times 2^5 the next part is
-// as large again, so that small values stay small relative to the largest and no part
-// falls below e4m3's range.  The columns that this adds are free: the tensor core is at
-// a few percent.
+// Then Q and X have to be e4m3 too.  They go in as parts of four bits, three of Q and four of X,
+//   x = a + 2^-5 b + 2^-10 c + 2^-15 d,
+// each a column of its own (N = 4 G, at least 16).  A part's remainder is at most 2^-4 of it, and
+// times 2^5 the next part is at most twice as large, so that it is off by 2^-4 of that again: three
+// parts have 2^-14 of a value and so all bits of an fp16 query, four have 2^-19.  The parts end at
+// 2^-9 in e4m3: queries are exact down to 2^-27 of a head's largest component (which is 2^7 or more),
+// X is down to 2^-29 of its largest (2^4 or more).  The columns that this adds are free: the tensor
+// core is at a few percent.
 //
 // The rows' scales are powers of two.  K's multiplies a score.  V's goes into the
 // probability: with w_t = log2(e) z_t + e_t the product takes X_t = 2^(w_t - M), M a
@@ -50,7 +51,7 @@ constexpr float kLift = 4.0f, kLag = 4.0f;  // X is 2^kLift at the maximum, 2^(k
 
 template <int HD, int G>
 struct Layout {
-  static constexpr int N = G == 8 ? 32 : 16;          // columns: part 0 of G heads, part 1, part 2
+  static constexpr int N = G == 8 ? 32 : 16;          // columns: part 0 of G heads, part 1, and so on
   static constexpr int kCtas = G == 8 ? 2 : 3;        // per SM
   static constexpr uint32_t kBlock = 32 * HD;         // K and V of a block: [2 groups][K, V][8][HD]
   static constexpr uint32_t kRows8 = 16 * HD;         // from 8 tokens to the next 8
@@ -85,12 +86,13 @@ EE_DEV float2 from_e4m3x2(uint32_t c) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// The three parts of two values of at most 2^8.
-EE_DEV void parts3(float a, float b, uint32_t (&c)[3]) {
+// The parts of two values of at most 2^8.
+template <int N>
+EE_DEV void parts(float a, float b, uint32_t (&c)[N]) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < N; ++i) {
     c[i] = to_e4m3x2(a, b);
-    if (i < 2) {
+    if (i < N - 1) {
       const float2 f = from_e4m3x2(c[i]);
       a = (a - f.x) * 32.0f;
       b = (b - f.y) * 32.0f;
@@ -98,9 +100,12 @@ EE_DEV void parts3(float a, float b, uint32_t (&c)[3]) {
   }
 }
 
-// A value from the columns of its parts.
+// A value from the columns of its parts, the smallest first.
 EE_DEV float joined(uint32_t a, uint32_t b, uint32_t c) {
-  return fmaf(__uint_as_float(c), 0x1p-10f, fmaf(__uint_as_float(b), 0x1p-5f, __uint_as_float(a)));
+  return fmaf(fmaf(__uint_as_float(c), 0x1p-5f, __uint_as_float(b)), 0x1p-5f, __uint_as_float(a));
+}
+EE_DEV float joined(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return joined(a, b, __float_as_uint(fmaf(__uint_as_float(d), 0x1p-5f, __uint_as_float(c))));
 }
 
 EE_DEV float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
 #pragma unroll
           for (int e = 0; e < kPer; e += 2) {
             uint32_t a[3];
-            parts3(x[i][e] * up, x[i][e + 1] * up, a);
+            parts(x[i][e] * up, x[i][e + 1] * up, a);
             const int d = lane * kPer + e;
 #pragma unroll
             for (int part = 0; part < 3; ++part) {
@@ -420,10 +425,10 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
             x[i] = ex2(w[h + i] - (m[h + i] == -INFINITY ? 0.0f : m[h + i]) + kLift);
             l[h + i] = live ? fmaf(x[i], down, l[h + i]) : l[h + i];
           }
-          uint32_t cs[3];
-          parts3(x[0], x[1], cs);
+          uint32_t cs[4];
+          parts(x[0], x[1], cs);
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
+          for (int part = 0; part < 4; ++part) {
             const int n = part * G + h;
             x8[n >> 2] |= (G == 1 ? cs[part] & 0xffu : cs[part]) << (8 * (n & 3));
           }
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
           tmem_wait_ld();
           tmem_pin<N>(o);
 #pragma unroll
-          for (int i = 0; i < 3 * G; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a[i % G]);
+          for (int i = 0; i < 4 * G; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a[i % G]);
           tmem_st16(o_col(r) + lane_base, o);
           if constexpr (N == 32) tmem_st16(o_col(r) + 16 + lane_base, o + 16);
           tmem_wait_st();
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         const float sum = (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]);
-        const float y = joined(o[h], o[G + h], o[2 * G + h]);
+        const float y = joined(o[h], o[G + h], o[2 * G + h], o[3 * G + h]);
         if (u.slot < 0) {
           if (has_dim && ok) p.o[u.s * p.o_stride + (u.g * G + h) * HD + dim] = float_to_half_bits(within_half(__fdividef(y, sum)));
         } else {

@@ -575,8 +575,10 @@ ee_status ee_op_dequantize_cache(int32_t B, int32_t n_kv_heads, int32_t head_dim
  *   o[s, h] = sum_{t <= pos[s]} softmax_t(q_h . k_t / sqrt(hd)) v_t,  k and v as held.
  *   q [B, q_stride] fp16 in natural order, head h at column h * hd; o [B, o_stride] fp16
  *   likewise, not overlapping q; strides multiples of 8, at least Hq * hd.
- * Products are exact in fp32 accumulators, statistics and sums fp32; probabilities have 12
- * bits.  A NaN in a key, or a value of q that is not finite, makes the rows
+ * Products are exact in fp32 accumulators, statistics and sums fp32.  Queries are exact down
+ * to 2^-27 of a head's largest component.  Probabilities count with the scale of their token's V
+ * row, p 2^e: 18 bits each, down to 2^-29 of a head's largest p 2^e (so a token has fewer where its V
+ * row is smaller by more than 2^10 than that of another that weighs).  A NaN in a key, or a value of q that is not finite, makes the rows
  * that see it NaN, a NaN in a value its own component of them.
  * scratch: device buffer of ee_quantized_attention_scratch_bytes(...) bytes, 16-byte
  * aligned.  It needs no contents and keeps none; calls that may overlap in time
