@@ -9,7 +9,8 @@
 //
 // Both kernels stream: eight values a thread, so that 16-byte (or two) loads and stores of
 // half a row stand side by side.  Memory is the bound: 35000 tokens of 8 heads of 128 written in
-// 36.5 us (5.9 TB/s), 37000 read back in 38.6 us (5.9 TB/s); one token 2.2 us, the launch.
+// 36.5 us (5.9 TB/s), from fp32 rows in 55.9 (6.4 TB/s), 37000 read back in 38.6 us (5.9 TB/s); one
+// token 2.2 us, the launch.
 #include "ee_cache_ops.cuh"
 #include "ee_tcgen05.cuh"
 
@@ -68,7 +69,8 @@ struct Eight<float> {
 // 128 in fp16 took 49 us, then 39.)  U = 4 in fp16 has few warps per SM: it is for calls whose
 // rows are all on their way at once (8 heads of 128, 64 rows: 2.7 us, with U = 2 3.0; 2048: 4.0, 4.2);
 // others are faster with U = 2 and registers for ten CTAs per SM (8192 rows: 11.0 us, with U = 4
-// 11.9; 35000: 36.5, 39).
+// 11.9; 35000: 36.5, 39).  fp32 rows are twice the bytes in flight with U = 2 (64: 3.3 us, 2048: 5.2,
+// 8192: 15.2).
 template <typename T, int HD, int U>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U == 2 ? 10 : 1) k_quantize_cache(const QuantizeParams p) {
   constexpr int L = HD / 8, kHeads = 32 / L;
@@ -203,10 +205,16 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_cache(const DequantizeP
 
 template <typename T, int HD>
 cudaError_t quantize_t(const QuantizeParams& p, cudaStream_t st) {
-  constexpr int kAtOnce = 24 * 152;  // rows, 24 warps per SM
   const int n = (p.total + kThreads / 32 - 1) / (kThreads / 32);
-  // nor where the heads of a row fit into a step of two
-  const bool four = sizeof(T) == 2 && p.total <= kAtOnce && p.c.n_kv_heads > 2 * (256 / HD);
+  // U = 4 is of no use where the heads of a row fit into a step of two
+  bool four = false;
+  if (sizeof(T) == 2 && p.c.n_kv_heads > 2 * (256 / HD)) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    four = p.total <= 24 * sms;  // rows at once, 24 warps per SM
+  }
   if (four) k_quantize_cache<T, HD, sizeof(T) == 2 ? 4 : 2><<<n, kThreads, 0, st>>>(p);
   else k_quantize_cache<T, HD, 2><<<n, kThreads, 0, st>>>(p);
   return cudaGetLastError();
