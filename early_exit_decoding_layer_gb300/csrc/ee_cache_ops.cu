@@ -1,5 +1,6 @@
 // C entry points of the operators on the paged cache: argument checks, all
-// on the host and before any CUDA call, then one launch.
+// on the host and before any CUDA call, then one launch (the decode attentions
+// over the eight-bit cache and behind a shared prefix: two, the second joins).
 #include <algorithm>
 #include <initializer_list>
 

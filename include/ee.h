@@ -546,7 +546,7 @@ enum { EE_ROWS_F16 = 0, EE_ROWS_F32 = 1 };
  * device, [n_seqs + 1], ascending, within [0, total]) and ctx[s] tokens with them; row
  * i goes to position ctx[s] - n + i (one before position 0 goes nowhere).  For each row,
  * kv head, K and V:
- *   exponent = the least e >= -15 with max |x| <= 448 * 2^e over the finite x,
+ *   exponent = the least e >= -15 with max |x| <= 448 * 2^e over the x that fp16 holds,
  *   code     = x * 2^-e rounded to e4m3 (nearest, ties to even).
  * An x that fp16 does not hold (infinite, NaN, |x| >= 65520) becomes NaN.
  *   k, v [total, stride] of rows_type, head g at column g * hd, 16-byte aligned, strides
