@@ -142,6 +142,22 @@ size_t shared_attention_scratch(int32_t batch, int32_t n_heads, int32_t n_kv_hea
                                 int32_t prefix);
 
 #ifdef __CUDACC__
+// o is a mean of the values that the cache holds and no larger than they are.  Its rounding on the way
+// may take it past the largest one, which would be infinite in fp16.
+constexpr float kMostHalf = 65504.0f;
+EE_DEV float within_half(float y) {
+  return fabsf(y) > kMostHalf && fabsf(y) < INFINITY ? copysignf(kMostHalf, y) : y;
+}
+
+// Two values as e4m3, the first in the low byte.
+EE_DEV uint32_t to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+EE_DEV float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 EE_DEV void report(int32_t* err, int32_t code) {
   if (err) atomicCAS(err, 0, code);
 }

@@ -84,6 +84,20 @@ EE_DEV bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, int32_t* err, int3
   }
 }
 
+// The same limit for a loop that tests several barriers in turn.
+struct Patience {
+  uint64_t since = 0;
+  uint32_t tries = 0;
+  EE_DEV bool over(int32_t* err, int32_t code) {  // asked after every failed try
+    if ((++tries & 255u) != 0) return false;
+    const uint64_t now = globaltimer();
+    if (since == 0) since = now;
+    if (now - since <= kWaitTimeoutNs) return false;
+    if (err) atomicCAS(err, 0, code);
+    return true;
+  }
+};
+
 EE_DEV uint64_t l2_evict_first_policy() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));

@@ -16,6 +16,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ee_cache_ops.cuh"
 #include "ee_tcgen05.cuh"
@@ -157,12 +158,88 @@ struct Ring {
   }
 };
 
+// A join: a CTA adds the parts of J query heads of a sequence: 8 / J warps each, kAtOnce parts in
+// flight a warp.  J is as small as two CTAs per SM allow: CTAs start 6 ns after one another,
+// whatever they do (one for each of 4096 rows took 20 us), but a warp that walks many parts takes
+// long too (one sequence of 16384 tokens, 57 parts: 13 us, with J = G = 4 17).
+constexpr int kJoinThreads = 256;
+
+template <int HD, int J>
+struct Join {
+  static constexpr int P = HD / 32, kAtOnce = 8, kStripes = 8 / J;  // a lane's dims; parts; warps of a head
+  struct Stripes {
+    float m[8], l[8], o[8][HD];
+  };
+  float m = -INFINITY, l = 0.0f, o[P] = {};
+
+  // (m, l, O) of parts; m = -inf and l = 0: nothing was seen, and O is 0.  A factor may go to 0, but
+  // every part is multiplied: an infinity or NaN of l and O stays.  (A part of NaN alone has no
+  // maximum.)
+  EE_DEV void add(const float (&mk)[kAtOnce], const float (&lk)[kAtOnce], const float (&x)[kAtOnce][P]) {
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) mn = fmaxf(mn, mk[u]);
+    const float a = m == mn ? 1.0f : ex2(m - mn);
+    m = mn;
+    l *= a;
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] *= a;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const float f = mk[u] == m ? 1.0f : ex2(mk[u] - m);
+      l = fmaf(f, lk[u], l);
+#pragma unroll
+      for (int i = 0; i < P; ++i) o[i] = fmaf(f, x[u][i], o[i]);
+    }
+  }
+  // All warps' sums, written to J heads side by side: 0 where nothing was seen.
+  EE_DEV void finish(Stripes& all, uint16_t* to) const {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (lane == 0) {
+      all.m[warp] = m;
+      all.l[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) all.o[warp][lane * P + i] = o[i];
+    __syncthreads();
+    for (int i = tid; i < J * HD; i += kJoinThreads) {
+      const int head = i / HD, d = i % HD;
+      float mm = -INFINITY, sum = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kStripes; ++w) mm = fmaxf(mm, all.m[w * J + head]);
+#pragma unroll
+      for (int w = 0; w < kStripes; ++w) {
+        const int at = w * J + head;
+        const float f = all.m[at] == mm ? 1.0f : ex2(all.m[at] - mm);
+        sum = fmaf(f, all.l[at], sum);
+        y = fmaf(f, all.o[at][d], y);
+      }
+      const float il = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // NaN stays
+      to[i] = float_to_half_bits(within_half(y * il));
+    }
+  }
+};
+
+// launch(J) with the J for this many rows, J as a type's value.
+template <int G, typename Launch>
+cudaError_t join_by_rows(int rows, int sms, Launch launch) {
+  int J = 1;
+  while (J < G && rows > 2 * sms * J) J *= 2;
+  if constexpr (G >= 8)
+    if (J == 8) return launch(std::integral_constant<int, 8>());
+  if constexpr (G >= 4)
+    if (J == 4) return launch(std::integral_constant<int, 4>());
+  if constexpr (G >= 2)
+    if (J == 2) return launch(std::integral_constant<int, 2>());
+  return launch(std::integral_constant<int, 1>());
+}
+
 // Launches a join behind the kernel that writes the parts.  Its CTAs start where that one's end, and
 // the first SMs to be free would take them all, eight or more each: shared memory that they do not
 // use keeps them apart, as many on an SM as it takes, but no more of it than a CTA before them had.
 // (16 sequences behind 1000 shared tokens: 15.1 -> 13.4 us, 8 behind 15000: 27.7 -> 26.0.)
 template <typename... Params, typename... Args>
-cudaError_t launch_join(void (*kernel)(Params...), int ctas, int threads, int sms, size_t before, cudaStream_t st, Args... args) {
+cudaError_t launch_join(void (*kernel)(Params...), int ctas, int sms, size_t before, cudaStream_t st, Args... args) {
   cudaFuncAttributes has;
   cudaError_t e = cudaFuncGetAttributes(&has, kernel);
   if (e != cudaSuccess) return e;
@@ -177,7 +254,7 @@ cudaError_t launch_join(void (*kernel)(Params...), int ctas, int threads, int sm
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = apart;
   cfg.stream = st;
   cfg.attrs = attr;

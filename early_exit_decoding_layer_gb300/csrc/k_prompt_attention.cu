@@ -85,13 +85,6 @@ EE_DEV float log_sum(float m, float l, const Exponent& ex) {
   return l == 0.0f ? -INFINITY : fmaf(m, ex.unit_hi, fmaf(m, ex.unit_lo, logf(l)));
 }
 
-// o is a mean of fp16 values and no larger than they are.  P's rounding may take it past the
-// largest one by up to 2^-11 of it, which would be infinite in fp16.
-constexpr float kMostHalf = 65504.0f;
-EE_DEV float within_half(float y) {
-  return fabsf(y) > kMostHalf && fabsf(y) < INFINITY ? copysignf(kMostHalf, y) : y;
-}
-
 // The work of one CTA on one (tile of rows, kv head): key tiles [ka, kb) of 128,
 // of which row tile t takes the first n[t]; those from jm[t] on are not seen whole by
 // every row of it.

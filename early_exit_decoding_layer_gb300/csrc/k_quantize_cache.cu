@@ -21,15 +21,6 @@ constexpr int kThreads = 128;
 constexpr int kMinExponent = -15;
 constexpr float kHalfEnd = 65520.0f;  // from here on fp16 rounds to infinity
 
-// Two values as e4m3, the first in the low byte.
-EE_DEV uint32_t to_e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-EE_DEV float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
 // Eight values of a row in registers, 16 or 32 bytes.
 template <typename T>
 struct Eight;

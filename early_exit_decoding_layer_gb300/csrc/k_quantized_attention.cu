@@ -74,12 +74,7 @@ struct Shared {
   float unscale[2][G], red[4][G], sum[4][G];
 };
 
-// Two values as e4m3, the first in the low byte, and what they stand for.
-EE_DEV uint32_t to_e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
-  return r;
-}
+// What two e4m3 codes stand for.
 EE_DEV float2 from_e4m3x2(uint32_t c) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
@@ -108,17 +103,10 @@ EE_DEV float joined(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return joined(a, b, __float_as_uint(fmaf(__uint_as_float(d), 0x1p-5f, __uint_as_float(c))));
 }
 
-EE_DEV float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
 // A part in the scratch: O of every head, then m and l.
 template <int HD, int G>
 EE_DEV float* part(const DecodeParams& p, int slot) {
   return static_cast<float*>(p.scratch) + (size_t)slot * G * (HD + 2);
-}
-
-// o is a mean of held values; fp16 ends at 65504.
-EE_DEV float within_half(float y) {
-  return fabsf(y) > 65504.0f && fabsf(y) < INFINITY ? copysignf(65504.0f, y) : y;
 }
 
 template <int HD, int G>
@@ -252,20 +240,15 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
           const int rn = j + 1 < tiles ? r : r + 1;
           const bool more = j + 1 < tiles || then.s >= 0, last = j + 1 < tiles ? j + 2 == tiles : then.blocks <= 8;
           out = false;
-          uint64_t since = 0;
-          for (int i = 1; !mbar_test(&sh.x_ready, t & 1); ++i) {
+          Patience patience;
+          while (!mbar_test(&sh.x_ready, t & 1)) {
             if (more && !out && mbar_test(&sh.q_ready[rn & 1], (rn >> 1) & 1) && mbar_test(&sh.full[(t + 1) % NS], ((t + 1) / NS) & 1)) {
               scores(t + 1, rn, last);
               out = true;
             }
-            if ((i & 255) == 0) {
-              const uint64_t now = globaltimer();
-              if (since == 0) since = now;
-              if (now - since > kWaitTimeoutNs) {
-                if (p.c.err) atomicCAS(p.c.err, 0, DERR_FULL_WAIT);
-                ok = false;
-                break;
-              }
+            if (patience.over(p.c.err, DERR_FULL_WAIT)) {
+              ok = false;
+              break;
             }
           }
           if (!ok) break;
@@ -504,16 +487,12 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, G>::kCtas)
   if (!ok) __nanosleep(1000000);  // what this CTA no longer waited for may be on its way
 }
 
-// The join: a CTA adds the parts of J query heads of a sequence, where there are any: 8 / J warps
-// each, eight parts in flight a warp.  J is as small as two CTAs per SM allow: CTAs start 6 ns after
-// one another, whatever they do, but a warp that walks many parts takes long too (one sequence
-// of 16384 tokens, 57 parts: 13 us, with J = G = 4 17).
-constexpr int kJoinThreads = 256;
-
+// Adds the parts of pairs that several CTAs had a share of.
 template <int HD, int G, int J>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, const int pieces, const int least) {
-  constexpr int P = HD / 32, U = 8, kStripes = 8 / J;  // dims per lane; parts in flight
-  __shared__ float ms[8], ls[8], outs[8][HD];
+  using Sum = Join<HD, J>;
+  constexpr int P = Sum::P, U = Sum::kAtOnce, kStripes = Sum::kStripes;
+  __shared__ typename Sum::Stripes stripes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x / (p.n_heads / J), first = (blockIdx.x - s * (p.n_heads / J)) * J;  // its heads
   const int g = first / G, h = first % G + warp % J;
@@ -528,7 +507,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   if (n < 2) return;
   // the first CTA has the pair as its last one, unless it begins with it
   const int late = from > w0 * plan.each;
-  float m = -INFINITY, l = 0.0f, o[P] = {};
+  Sum sum;
   for (int k0 = warp / J; k0 < n; k0 += kStripes * U) {
     float mk[U], lk[U], x[U][P];
 #pragma unroll
@@ -549,44 +528,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
             *reinterpret_cast<float2*>(x[u] + i) = *reinterpret_cast<const float2*>(y + h * HD + lane * P + i);
       }
     }
-    float mn = m;
-#pragma unroll
-    for (int u = 0; u < U; ++u) mn = fmaxf(mn, mk[u]);
-    const float a = m == mn ? 1.0f : ex2(m - mn);
-    m = mn;
-    l *= a;
-#pragma unroll
-    for (int i = 0; i < P; ++i) o[i] *= a;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // a part of NaN alone has no maximum; its l and O are NaN, which stays
-      const float f = mk[u] == m ? 1.0f : ex2(mk[u] - m);
-      l = fmaf(f, lk[u], l);
-#pragma unroll
-      for (int i = 0; i < P; ++i) o[i] = fmaf(f, x[u][i], o[i]);
-    }
+    sum.add(mk, lk, x);
   }
-  if (lane == 0) {
-    ms[warp] = m;
-    ls[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < P; ++i) outs[warp][lane * P + i] = o[i];
-  __syncthreads();
-  for (int i = tid; i < J * HD; i += kJoinThreads) {
-    const int head = i / HD, d = i % HD;
-    float mm = -INFINITY, sum = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kStripes; ++w) mm = fmaxf(mm, ms[w * J + head]);
-#pragma unroll
-    for (int w = 0; w < kStripes; ++w) {
-      const int at = w * J + head;
-      const float f = ms[at] == mm ? 1.0f : ex2(ms[at] - mm);
-      sum = fmaf(f, ls[at], sum);
-      y = fmaf(f, outs[at][d], y);
-    }
-    p.o[s * p.o_stride + (first + head) * HD + d] = float_to_half_bits(within_half(__fdividef(y, sum)));
-  }
+  sum.finish(stripes, p.o + s * p.o_stride + first * HD);
 }
 
 template <int HD, int G>
@@ -615,16 +559,9 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   k_quantized_attention<HD, G><<<pieces, kThreads, Lay::kSmem, st>>>(p, map, 1.44269504f / sqrtf((float)HD), least, whole);
   e = cudaGetLastError();
   if (e != cudaSuccess || whole) return e;
-  int J = 1;
-  while (J < G && p.batch * p.n_heads > 2 * sms * J) J *= 2;
-  auto join = [&](auto kernel) { return launch_join(kernel, p.batch * (p.n_heads / J), kJoinThreads, sms, Lay::kSmem, st, p, pieces, least); };
-  if constexpr (G >= 8)
-    if (J == 8) return join(k_join<HD, G, 8>);
-  if constexpr (G >= 4)
-    if (J == 4) return join(k_join<HD, G, 4>);
-  if constexpr (G >= 2)
-    if (J == 2) return join(k_join<HD, G, 2>);
-  return join(k_join<HD, G, 1>);
+  return join_by_rows<G>(p.batch * p.n_heads, sms, [&](auto J) {
+    return launch_join(k_join<HD, G, J.value>, p.batch * (p.n_heads / J.value), sms, Lay::kSmem, st, p, pieces, least);
+  });
 }
 
 }  // namespace

@@ -297,20 +297,15 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
           const int rn = j + 1 < tiles ? r : r + 1;
           const bool more = j + 1 < tiles || then.s >= 0, last = j + 1 < tiles ? j + 2 == tiles : then.blocks <= 8;
           out = false;
-          uint64_t since = 0;
-          for (int i = 1; !(mbar_test(&sh.p_ready, k & 1) && there(2 * k + 1)); ++i) {
+          Patience patience;
+          while (!(mbar_test(&sh.p_ready, k & 1) && there(2 * k + 1))) {
             if (more && !out && mbar_test(&sh.q_full[rn & 1], (rn >> 1) & 1) && there(2 * k + 2)) {
               scores(k + 1, rn, last);
               out = true;
             }
-            if ((i & 255) == 0) {
-              const uint64_t now = globaltimer();
-              if (since == 0) since = now;
-              if (now - since > kWaitTimeoutNs) {
-                if (p.c.err) atomicCAS(p.c.err, 0, DERR_FULL_WAIT);
-                ok = false;
-                break;
-              }
+            if (patience.over(p.c.err, DERR_FULL_WAIT)) {
+              ok = false;
+              break;
             }
           }
           if (!ok) break;
@@ -971,23 +966,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// o is a mean of fp16 values and no larger than they are.  The sums' rounding may take it past the
-// largest one, which would be infinite in fp16 if it were by 2^-12 of it.
-EE_DEV float within_half(float y) {
-  return fabsf(y) > 65504.0f && fabsf(y) < INFINITY ? copysignf(65504.0f, y) : y;
-}
-
-// The join: a CTA adds the parts, of the prefix and of its own blocks, of J query heads of a
-// sequence: 8 / J warps each, eight parts in flight a warp.  J is as small as two CTAs per SM allow:
-// CTAs start 6 ns after one another, whatever they do (one for each of 4096 rows took 20 us), but
-// a warp that walks many parts takes long too.
-constexpr int kJoinThreads = 256;
-
+// Adds the parts, of the prefix and of its own blocks, of every row.
 template <int HD, int G, int J>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, const int ctas) {
-  constexpr int P = HD / 32, U = 8, kStripes = 8 / J;  // dims per lane; parts in flight
+  using Sum = Join<HD, J>;
+  constexpr int P = Sum::P, U = Sum::kAtOnce, kStripes = Sum::kStripes;
   __shared__ int64_t ml_at[3 * kMaxPieces], o_at[3 * kMaxPieces];  // where head 0's parts are; -1: none
-  __shared__ float ms[8], ls[8], outs[8][HD];
+  __shared__ typename Sum::Stripes stripes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x / (p.n_heads / J), first = (blockIdx.x - s * (p.n_heads / J)) * J;  // its heads
   const int g = first / G, h = first % G + warp % J;
@@ -1022,63 +1007,29 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   const float *pre_o = sp.o + h * 8 + (int64_t)(lane * P / 8) * R * 8 + lane * P % 8, *own_o = so.o + h * HD + lane * P;
   grid_dep_wait();
   __syncthreads();
-  float m = -INFINITY, l = 0.0f, o[P] = {};
+  Sum sum;
   for (int k0 = warp / J; k0 < count; k0 += kStripes * U) {
-    float2 ml[U];
-    float x[U][P];
+    float mk[U], lk[U], x[U][P];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + kStripes * u;
       const int64_t at = k < count ? ml_at[k] : -1;
-      ml[u] = make_float2(-INFINITY, 0.0f);
+      mk[u] = -INFINITY;
+      lk[u] = 0.0f;
 #pragma unroll
       for (int i = 0; i < P; ++i) x[u][i] = 0.0f;
       if (at >= 0) {
-        ml[u] = *reinterpret_cast<const float2*>((k < n_pre ? sp.ml : so.ml) + (at + h) * 2);
+        const float2 ml = *reinterpret_cast<const float2*>((k < n_pre ? sp.ml : so.ml) + (at + h) * 2);
+        mk[u] = ml.x;
+        lk[u] = ml.y;
         const float* from = (k < n_pre ? pre_o : own_o) + o_at[k];
         if constexpr (P == 4) *reinterpret_cast<float4*>(x[u]) = *reinterpret_cast<const float4*>(from);
         else *reinterpret_cast<float2*>(x[u]) = *reinterpret_cast<const float2*>(from);
       }
     }
-    float mn = m;
-#pragma unroll
-    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
-    const float a = l == 0.0f ? 0.0f : m == mn ? 1.0f : ex2(m - mn);
-    m = mn;
-    l *= a;
-#pragma unroll
-    for (int i = 0; i < P; ++i) o[i] *= a;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // f may go to 0, or be it where nothing was seen: an infinity or NaN of O and l stays
-      const float f = ml[u].y == 0.0f ? 0.0f : ml[u].x == m ? 1.0f : ex2(ml[u].x - m);
-      l = fmaf(f, ml[u].y, l);
-#pragma unroll
-      for (int i = 0; i < P; ++i) o[i] = fmaf(f, x[u][i], o[i]);
-    }
+    sum.add(mk, lk, x);
   }
-  if (lane == 0) {
-    ms[warp] = m;
-    ls[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < P; ++i) outs[warp][lane * P + i] = o[i];
-  __syncthreads();
-  for (int i = tid; i < J * HD; i += kJoinThreads) {
-    const int head = i / HD, d = i % HD;
-    float mm = -INFINITY, sum = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kStripes; ++w) mm = fmaxf(mm, ms[w * J + head]);
-#pragma unroll
-    for (int w = 0; w < kStripes; ++w) {
-      const int at = w * J + head;
-      const float f = ls[at] == 0.0f ? 0.0f : ms[at] == mm ? 1.0f : ex2(ms[at] - mm);
-      sum = fmaf(f, ls[at], sum);
-      y = fmaf(f, outs[at][d], y);
-    }
-    const float il = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // NaN stays
-    p.o[s * p.o_stride + (first + head) * HD + d] = float_to_half_bits(within_half(y * il));
-  }
+  sum.finish(stripes, p.o + s * p.o_stride + first * HD);
 }
 
 template <int HD, int G>
@@ -1112,16 +1063,9 @@ cudaError_t launch_t(const DecodeParams& p, cudaStream_t st) {
   k_shared_attention<HD, G><<<ctas, kThreads, S::kSmem, st>>>(p, maps, make_exponent(HD).c);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  int J = 1;
-  while (J < G && p.batch * p.n_heads > 2 * sms * J) J *= 2;
-  auto join = [&](auto kernel) { return launch_join(kernel, p.batch * (p.n_heads / J), kJoinThreads, sms, S::kSmem, st, p, ctas); };
-  if constexpr (G >= 8)
-    if (J == 8) return join(k_join<HD, G, 8>);
-  if constexpr (G >= 4)
-    if (J == 4) return join(k_join<HD, G, 4>);
-  if constexpr (G >= 2)
-    if (J == 2) return join(k_join<HD, G, 2>);
-  return join(k_join<HD, G, 1>);
+  return join_by_rows<G>(p.batch * p.n_heads, sms, [&](auto J) {
+    return launch_join(k_join<HD, G, J.value>, p.batch * (p.n_heads / J.value), sms, S::kSmem, st, p, ctas);
+  });
 }
 
 }  // namespace
