@@ -178,8 +178,6 @@ struct Stream {
   float red[4][G], sum[4][G];
 };
 
-constexpr int kPrefix = 1, kDeep = 2;
-
 template <int HD, int G>
 struct Shared {
   static constexpr int NST = Shape<HD>::NST;
@@ -188,14 +186,14 @@ struct Shared {
   uint64_t both;        // narrow units: both streams' m, l and O are there; have been read
   Ring<Work> units;
   Stream<HD, G> own[2];
-  int role;  // kPrefix: this CTA has a piece of it; kDeep
+  bool prefix;  // this CTA has a piece of it
   uint32_t tmem;
 };
 
 // The CTA's two streams of own blocks, `first` and the next of all.
 template <int HD, int G>
 EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const Plan<G>& plan, Stream<HD, G>* streams, uint8_t* memory,
-                       uint32_t tmem, bool deep) {
+                       uint32_t tmem) {
   using S = Shape<HD>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
   const int t = warp < 8 ? warp >> 2 : warp >= 10;  // the stream
@@ -204,13 +202,10 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
   uint8_t *qs = ring + S::oQ, *ps = ring + S::oP;
   auto s_col = [&](int k) { return tmem + t * 64 + (k & 1) * 16; };
   auto o_col = [&](int r) { return tmem + t * 64 + 32 + (r & 1) * 16; };
-  // Tile k's K is ring item 2 k, its V item 2 k + 1; tiles and shares count on.  Where most SMs
-  // have own blocks two thirds of the ring are enough to keep the memory busy; with all of it
-  // loads queue up, and everybody's first ones wait 4 us (32 sequences of 500 to 2000 behind 256:
-  // 50 us, now 42).  After a wait
+  // Tile k's K is ring item 2 k, its V item 2 k + 1; tiles and shares count on.  After a wait
   // that gave up the softmax warps go on without waiting: they still meet each other.
-  auto place = [&](int item) { return deep ? item % S::NR : item % (S::NR / 3 * 2); };
-  auto turn = [&](int item) { return deep ? item / S::NR : item / (S::NR / 3 * 2); };
+  auto place = [&](int item) { return item % S::NR; };
+  auto turn = [&](int item) { return item / S::NR; };
   bool ok = true;
   Own u;
   if (warp == 8 || warp == 11) {
@@ -260,7 +255,7 @@ EE_DEV void own_blocks(const DecodeParams& p, const Maps& maps, float c, const P
       u = then;
     }
     // Copies land before the CTA ends, whichever warp gave up (where none did, they have).
-    for (int i = max(0, item - (deep ? S::NR : S::NR / 3 * 2)); i < item; ++i)
+    for (int i = max(0, item - S::NR); i < item; ++i)
       mbar_wait_bounded(&sh.full[place(i)], (uint32_t)turn(i) & 1, p.c.err, DERR_DRAIN_WAIT);
     for (int i = max(0, r - 2); i < r; ++i) mbar_wait_bounded(&sh.q_full[i & 1], (i >> 1) & 1, p.c.err, DERR_DRAIN_WAIT);
   } else if (warp >= 9) {
@@ -512,12 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("bar.arrive 3, %0;" ::"n"(kThreads) : "memory");
   }
   Plan<G> plan;
-  int role;
+  bool prefix;
   if (loads) {
     plan.init(p, gridDim.x);
-    role = ((int)blockIdx.x < plan.n_pre ? kPrefix : 0) | (2 * plan.n_pre >= (int)gridDim.x ? kDeep : 0);
+    prefix = (int)blockIdx.x < plan.n_pre;
     if (warp == 8) {
-      if (lane == 0) sh.role = role;
+      if (lane == 0) sh.prefix = prefix;
       __syncwarp();
       asm volatile("bar.arrive 4, %0;" ::"n"(kThreads - 32) : "memory");
     }
@@ -529,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
     tc_fence_after();
     asm volatile("bar.sync 4, %0;" ::"n"(kThreads - 32) : "memory");
-    role = sh.role;
+    prefix = sh.prefix;
   }
   const uint32_t tmem = loads ? 0 : sh.tmem;
   const uint32_t q_s = smem_addr(tiles), kv_s = q_s + 2 * S::kTile;
@@ -584,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    acc || kk > h * kKeys / 32 || low > 0);
   };
 
-  if (!(role & kPrefix)) {
-    own_blocks<HD, G>(p, maps, c, plan, sh.own, tiles, tmem, role & kDeep);
+  if (!prefix) {
+    own_blocks<HD, G>(p, maps, c, plan, sh.own, tiles, tmem);
   } else if (warp == 8) {
     // this CTA's next unit
     int c0 = blockIdx.x * plan.each_pre, start = 0, n = 0;
