@@ -43,8 +43,8 @@
 //
 // Measured: 64 sequences behind 15000 tokens (64 query heads on 8 of 128) 73 us, 450 TFLOP/s and
 // 3.2 TB/s; a wide step takes 4900 cycles, of which the tensor core is busy with 3400 (P_lo's MMAs
-// 1000 of them; without them 3350 and 64 us).  32 behind 2048 (32 on 8) 17.7 us, 4 behind 512 (32
-// on 8 of 64) 11.0 us: a CTA's beginning (4.5 us), few steps, and the join (2 to 3 us).
+// 1000 of them; without them 3350 and 64 us).  32 behind 2048 (32 on 8) 16.7 us, 4 behind 512 (32
+// on 8 of 64) 10.4 us: a CTA's beginning (4.5 us), few steps, and the join (2 to 3 us).
 #include <limits.h>
 #include <math.h>
 
