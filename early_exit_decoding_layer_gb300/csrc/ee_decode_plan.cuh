@@ -7,11 +7,10 @@
 // CTAs.  A CTA has at most two of them, of its first pair and of its last; pairs that lie
 // within a piece are finished where they are.
 //
-// A pair's beginning takes a CTA as long as some blocks do, so a pair of n blocks has the places
-// [x, x + start + n): its first block stands at x, block b at x + start + b.  (Without that
-// CTAs with several short pairs were done last: 18 us, where half of all were done in 14.)
-// Where all pairs can be cut by themselves into pieces that are no longer, no CTA has blocks of
-// two: start is 0, and a pair's places are rounded up to whole pieces (8 sequences of 500, 8 kv heads:
+// A pair's beginning takes a CTA as long as some blocks do, and counts like them in the pieces'
+// borders (ee_decode_pieces.cuh).  (Without that CTAs with several short pairs were done last: 18 us,
+// where half of all were done in 14.)  Where all pairs can be cut by themselves into pieces that are
+// no longer, no CTA has blocks of two, and beginnings do not count (8 sequences of 500, 8 kv heads:
 // 10.9 us with the beginnings counted, 9.3 without).
 #pragma once
 
@@ -19,28 +18,20 @@
 #include <type_traits>
 
 #include "ee_cache_ops.cuh"
+#include "ee_decode_pieces.cuh"
 #include "ee_tcgen05.cuh"
 
 namespace ee {
 
-// A CTA's share of a pair: blocks first .. first + blocks - 1, `have` tokens in them.
-struct Share {
-  int s, g, first, blocks, have;
-  int slot;  // of its part in the scratch; -1: the whole pair
-};
-
-struct DecodePlan {
-  static constexpr int kStart = 6;
-  int start;
+struct DecodePlan : DecodePieces {
   int tokens[2], base[2], size[2];  // of sequences lane and lane + 32: their places, and those before them
-  int hkv, total, each, begin, end;
+  int total, begin, end;
 
   // `least`: places of a piece at least.  whole: a CTA takes the pairs that begin in its
   // piece.  The whole warp.
   EE_DEV void init(const DecodeParams& p, int pieces, int least, bool whole, int me) {
     static_assert(EE_MAX_BATCH <= 64, "two sequences per lane");
     const int lane = threadIdx.x & 31;
-    hkv = p.c.n_kv_heads;
     int at[2];  // both loads before either is waited for
 #pragma unroll
     for (int u = 0; u < 2; ++u) at[u] = lane + 32 * u < p.batch ? p.pos[lane + 32 * u] : -1;
@@ -51,19 +42,14 @@ struct DecodePlan {
     }
     const int blocks = (int)__reduce_add_sync(0xffffffffu, size[0] + size[1]);
     const int pairs = __popc(__ballot_sync(0xffffffffu, size[0] > 0)) + __popc(__ballot_sync(0xffffffffu, size[1] > 0));
-    // (a piece of kStart + 1 places has a block of every pair that it lies within)
-    each = max(max(least, kStart + 1), (hkv * (blocks + kStart * pairs) + pieces - 1) / pieces);
-    start = kStart;
+    cut(p.c.n_kv_heads, blocks, pairs, pieces, least);
     if (!whole) {
 #pragma unroll
       for (int c = 8; c <= 32; c += 8)
-        if (start && c <= each && hkv * (int)__reduce_add_sync(0xffffffffu, (size[0] + c - 1) / c + (size[1] + c - 1) / c) <= pieces) {
-          start = 0;
-          each = c;
-        }
+        cut_alone(c, (int)__reduce_add_sync(0xffffffffu, (size[0] + c - 1) / c + (size[1] + c - 1) / c), pieces);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) size[u] = start ? (size[u] > 0 ? start + size[u] : 0) : (size[u] + each - 1) / each * each;
+    for (int u = 0; u < 2; ++u) size[u] = places(size[u]);
     // both scans at once: sums of 32 sequences' places are below 2^16
     static_assert((32 + kCacheMaxCtx / 16) * 32 < 1 << 16, "two sums in a word");
     const uint32_t mine = (uint32_t)size[0] | (uint32_t)size[1] << 16;
@@ -97,8 +83,6 @@ struct DecodePlan {
     const int len = of(size, lo, hi), b0 = of(base, lo, hi) * hkv;
     return b0 + (c - b0 + len - 1) / len * len;
   }
-  // The first block of a pair of n at x that stands at place c or behind it.
-  EE_DEV int block_at(int c, int x, int n) const { return c <= x ? 0 : min(n, max(1, c - x - start)); }
   // The share of CTA `me` of the pair that holds place *c, or of the next one that has any (s = -1:
   // no more); *c: behind the pair.
   EE_DEV Share at(int* c, int me) const {
@@ -107,19 +91,9 @@ struct DecodePlan {
       r.s = -1;
       r.blocks = 0;
       if (*c >= end) return r;
-      const int from = *c;
-      const unsigned lo = __ballot_sync(0xffffffffu, holds(0, from)), hi = __ballot_sync(0xffffffffu, holds(1, from));
-      const int len = of(size, lo, hi), b0 = of(base, lo, hi) * hkv, n = of(tokens, lo, hi), nb = (n + 15) >> 4;
-      r.g = (from - b0) / len;
-      const int x = b0 + r.g * len;
-      *c = x + len;
-      r.first = block_at(begin, x, nb);
-      r.blocks = block_at(end, x, nb) - r.first;
-      if (r.blocks <= 0) continue;
-      r.s = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
-      r.have = min(n - r.first * 16, r.blocks * 16);
-      r.slot = r.blocks < nb ? 2 * me + (from > begin) : -1;
-      return r;
+      const unsigned lo = __ballot_sync(0xffffffffu, holds(0, *c)), hi = __ballot_sync(0xffffffffu, holds(1, *c));
+      const int s = lo ? __ffs(lo) - 1 : 31 + __ffs(hi), b0 = of(base, lo, hi) * hkv, n = of(tokens, lo, hi);
+      if (share(c, me, begin, end, s, b0, n, &r)) return r;
     }
   }
 };

@@ -8,10 +8,12 @@
 
 #include <stdint.h>
 
+#ifndef EE_HD
 #ifdef __CUDACC__
 #define EE_HD __host__ __device__ __forceinline__
 #else
 #define EE_HD inline
+#endif
 #endif
 
 namespace ee {

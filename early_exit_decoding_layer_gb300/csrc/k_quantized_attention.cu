@@ -501,19 +501,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const DecodeParams p, con
   const int nb = (__shfl_sync(0xffffffffu, s < 32 ? plan.tokens[0] : plan.tokens[1], s & 31) + 15) >> 4;
   const int from = __shfl_sync(0xffffffffu, s < 32 ? plan.base[0] : plan.base[1], s & 31) * plan.hkv +
                    g * __shfl_sync(0xffffffffu, s < 32 ? plan.size[0] : plan.size[1], s & 31);
-  const int last = nb < 2 ? from : from + plan.start + nb - 1;  // the last block's place
-  const int w0 = from / plan.each, n = nb == 0 ? 0 : last / plan.each - w0 + 1;
+  const DecodePieces::Parts parts = plan.parts(from, nb);
+  const int n = parts.count;
   grid_dep_wait();
   if (n < 2) return;
-  // the first CTA has the pair as its last one, unless it begins with it
-  const int late = from > w0 * plan.each;
   Sum sum;
   for (int k0 = warp / J; k0 < n; k0 += kStripes * U) {
     float mk[U], lk[U], x[U][P];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + kStripes * u;
-      const float* y = part<HD, G>(p, 2 * (w0 + k) + (k == 0 ? late : 0));
+      const float* y = part<HD, G>(p, parts.slot(k));
       mk[u] = -INFINITY;
       lk[u] = 0.0f;
 #pragma unroll

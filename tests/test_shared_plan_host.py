@@ -10,6 +10,7 @@ import pytest
 from early_exit_decoding_layer_gb300 import build
 
 SOURCE = """
+#include <cstdint>
 #include <map>
 #include <set>
 #include <vector>
